@@ -35,6 +35,9 @@ __all__ = [
     "SLOTS_TRAINING",
     "SLOTS_INFERENCE",
     "STORES_AUTO", "STORES_CACHED", "STORES_STREAMING", "FP8_SCALES_AMAX", "FP8_SCALES_POW2",
+    "RouteRule", "ep_route_scored", "ep_route_scored_bwd", "ep_add_rmsnorm", "ep_add_rmsnorm_bwd",
+    "ep_add_rmsnorm_bwd_workspace_bytes", "ep_quantize_int8", "ep_dispatch_quantized",
+    "ep_expert_gemm_int8", "ep_expert_gemm_int8_swiglu",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,7 +47,8 @@ LAYOUT_LL, LAYOUT_HT, LAYOUT_STATIC = 0, 1, 2
 _LAYOUTS = {"ll": LAYOUT_LL, "ht": LAYOUT_HT, "static": LAYOUT_STATIC}
 FLAG_INDEX_RANGE, FLAG_CAPACITY, FLAG_SLOT_BUDGET, FLAG_PLAN_STALL, FLAG_SCALE_FORMAT = 1, 2, 4, 8, 16
 TAG_TOKENS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS, TAG_FP8_SCALES, TAG_EXPERT_GRADS = 0, 1, 2, 3, 4
-TAG_ROUTER_LOGITS, TAG_EXPERT_WEIGHTS = 5, 6
+TAG_ROUTER_LOGITS, TAG_EXPERT_WEIGHTS, TAG_ROW_SCALES, TAG_ROUTER_BIAS = 5, 6, 7, 8
+TAG_NORM_WEIGHT, TAG_WORKSPACE = 9, 10
 SLOTS_TRAINING, SLOTS_INFERENCE = 0, 1
 _SLOT_MODES = {"training": SLOTS_TRAINING, "inference": SLOTS_INFERENCE}
 STORES_AUTO, STORES_CACHED, STORES_STREAMING = 0, 1, 2
@@ -52,7 +56,13 @@ _STORES = {"auto": STORES_AUTO, "cached": STORES_CACHED, "streaming": STORES_STR
 FP8_SCALES_AMAX, FP8_SCALES_POW2, FP8_SCALES_AMAX_POW2_WEIGHTS = 0, 1, 2
 _FP8_SCALES = {"amax": FP8_SCALES_AMAX, "pow2": FP8_SCALES_POW2,
                "amax_pow2w": FP8_SCALES_AMAX_POW2_WEIGHTS}
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float8_e4m3fn: 2, torch.int32: 3}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+GROUP_MAX, GROUP_TOP2 = 0, 1
+_GROUP_SCORES = {"max": GROUP_MAX, "top2": GROUP_TOP2}
+QUANT_NONE, QUANT_FP8, QUANT_FP8_POW2, QUANT_INT8 = 0, 1, 2, 3
+_QUANTS = {"none": QUANT_NONE, "fp8": QUANT_FP8, "fp8_pow2": QUANT_FP8_POW2, "int8": QUANT_INT8}
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float8_e4m3fn: 2, torch.int32: 3, torch.int8: 4}
 _STATUS = ["EP_OK", "EP_ERR_INVALID_ARG", "EP_ERR_BAD_TAG", "EP_ERR_BAD_DTYPE",
            "EP_ERR_BAD_SHAPE", "EP_ERR_NOT_PLANNED", "EP_ERR_WORKSPACE_TOO_SMALL",
            "EP_ERR_UNSUPPORTED", "EP_ERR_HIP"]
@@ -86,7 +96,19 @@ class ep_call_t(ctypes.Structure):
 _OPS = {"ep_route": 1, "ep_route_plan": 2, "ep_plan": 3, "ep_dispatch": 4, "ep_plan_dispatch": 5,
         "ep_quantize_fp8": 6, "ep_combine": 7, "ep_combine_bwd": 8, "ep_dup_grad_reduce": 9,
         "ep_prefetch_replicas": 10, "ep_expert_gemm": 11, "ep_expert_gemm_swiglu": 12,
-        "ep_expert_gemm_fp8": 13, "ep_expert_gemm_fp8_swiglu": 14}
+        "ep_expert_gemm_fp8": 13, "ep_expert_gemm_fp8_swiglu": 14, "ep_route_scored": 15,
+        "ep_route_scored_bwd": 16, "ep_add_rmsnorm": 17, "ep_add_rmsnorm_bwd": 18,
+        "ep_quantize_int8": 19, "ep_dispatch_quantized": 20, "ep_expert_gemm_int8": 21,
+        "ep_expert_gemm_int8_swiglu": 22}
+
+
+class ep_route_rule_t(ctypes.Structure):
+    _fields_ = [("score", c_int32), ("num_groups", c_int32), ("kept_groups", c_int32),
+                ("group_score", c_int32), ("renormalise", c_int32), ("scale", ctypes.c_float)]
+
+
+class ep_norm_rule_t(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("quant", c_int32), ("reserved", c_int32)]
 
 
 class ep_handle_view_t(ctypes.Structure):
@@ -144,6 +166,15 @@ def load_library():
         "ep_expert_gemm_fp8": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
         "ep_expert_gemm_swiglu": (S, [c_void_p, _T, _T, _T, _T, c_void_p]),
         "ep_expert_gemm_fp8_swiglu": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_route_scored": (S, [c_void_p, POINTER(ep_route_rule_t), _T, _T, _T, _T, _T, c_void_p]),
+        "ep_route_scored_bwd": (S, [c_void_p, POINTER(ep_route_rule_t), _T, _T, _T, _T, _T, c_void_p]),
+        "ep_add_rmsnorm": (S, [POINTER(ep_norm_rule_t), _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_add_rmsnorm_bwd_workspace_bytes": (S, [c_int64, c_int32, POINTER(c_size_t)]),
+        "ep_add_rmsnorm_bwd": (S, [POINTER(ep_norm_rule_t), _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_quantize_int8": (S, [_T, _T, _T, c_void_p]),
+        "ep_dispatch_quantized": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_expert_gemm_int8": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_expert_gemm_int8_swiglu": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
         "ep_run_calls": (S, [POINTER(ep_call_t), c_int32, POINTER(c_int32)]),
     }
     for name, (res, args) in sig.items():
@@ -219,6 +250,7 @@ def _enqueue(name: str, *args) -> None:
     calls = getattr(_RECORDING, "calls", None)
     if calls is not None:
         calls.append((fn, args, name))
+        _RECORDING.keep.extend(args)   # rules live as long as the recorded call
         return
     _check(fn(*args), name)
 
@@ -415,9 +447,10 @@ def ep_dup_grad_reduce(h: int, replica_grads: torch.Tensor, replica_expert: torc
 
 
 def ep_prefetch_replicas(h: int, expert_weights: torch.Tensor, slot_weights: torch.Tensor,
-                         stream=None, scales: bool = False) -> None:
-    """``scales``: the tensors are the fp32 scales of FP8 weights (tag FP8_SCALES)."""
-    tag = TAG_FP8_SCALES if scales else TAG_EXPERT_WEIGHTS
+                         stream=None, scales: bool | str = False) -> None:
+    """``scales``: the tensors are the fp32 scales of FP8 weights (tag
+    FP8_SCALES), or with ``"row"`` those of INT8 weights (tag ROW_SCALES)."""
+    tag = TAG_ROW_SCALES if scales == "row" else TAG_FP8_SCALES if scales else TAG_EXPERT_WEIGHTS
     _enqueue("ep_prefetch_replicas", c_void_p(h), _tensor(expert_weights, tag),
              _tensor(slot_weights, tag), _stream(stream))
 
@@ -453,6 +486,140 @@ def ep_expert_gemm_fp8_swiglu(h: int, recv_tokens: torch.Tensor, recv_scales: to
                               out: torch.Tensor, stream=None) -> None:
     ep_expert_gemm_fp8(h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
                        slot_scales, out, stream, swiglu=True)
+
+
+class RouteRule:
+    """How a token chooses its experts (ep_route_rule_t): ``score`` "softmax"
+    or "sigmoid"; of ``num_groups`` expert groups the ``kept_groups`` best
+    stay, a group counting its best expert ("max") or the sum of its two best
+    ("top2"); the weights are ``scale`` times the scores, ``renormalise``d to
+    sum to it or not."""
+
+    def __init__(self, score: str | int = "softmax", num_groups: int = 1, kept_groups: int = 1,
+                 group_score: str | int = "max", renormalise: bool = True, scale: float = 1.0):
+        self.c = ep_route_rule_t(
+            _SCORES[score] if isinstance(score, str) else int(score), num_groups, kept_groups,
+            _GROUP_SCORES[group_score] if isinstance(group_score, str) else int(group_score),
+            int(renormalise), scale)
+        self.ptr = ctypes.pointer(self.c)
+
+
+_NORM_RULES: dict = {}
+
+
+def _norm_rule(eps: float, quant: str | int):
+    p = _NORM_RULES.get((eps, quant))
+    if p is None:
+        q = _QUANTS[quant] if isinstance(quant, str) else int(quant)
+        if len(_NORM_RULES) >= _VIEWS_MAX:
+            _NORM_RULES.clear()
+        p = _NORM_RULES[(eps, quant)] = ctypes.pointer(ep_norm_rule_t(eps, q, 0))
+    return p
+
+
+def _same_device(stream, *tensors) -> None:
+    """The tensors live on the device the call runs on (the stream's, or the
+    current one)."""
+    dev = stream.device.index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the call runs on cuda:{dev}")
+
+
+def ep_route_scored(h: int, rule: RouteRule, logits: torch.Tensor, bias: torch.Tensor | None,
+                    topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+                    scores: torch.Tensor | None = None, stream=None) -> None:
+    _same_device(stream, logits, bias, topk_idx, topk_weights, scores)
+    _enqueue("ep_route_scored", c_void_p(h), rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS),
+             _tensor(bias, TAG_ROUTER_BIAS), _tensor(topk_idx, TAG_TOPK_IDX),
+             _tensor(topk_weights, TAG_TOPK_WEIGHTS), _tensor(scores, TAG_ROUTER_LOGITS),
+             _stream(stream))
+
+
+def ep_route_scored_bwd(h: int, rule: RouteRule, logits: torch.Tensor, topk_idx: torch.Tensor,
+                        grad_topk_weights: torch.Tensor, grad_scores: torch.Tensor | None,
+                        grad_logits: torch.Tensor, stream=None) -> None:
+    _same_device(stream, logits, topk_idx, grad_topk_weights, grad_scores, grad_logits)
+    _enqueue("ep_route_scored_bwd", c_void_p(h), rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS),
+             _tensor(topk_idx, TAG_TOPK_IDX), _tensor(grad_topk_weights, TAG_TOPK_WEIGHTS),
+             _tensor(grad_scores, TAG_ROUTER_LOGITS), _tensor(grad_logits, TAG_ROUTER_LOGITS),
+             _stream(stream))
+
+
+def _scale_tag(codes: torch.Tensor | None) -> int:
+    return TAG_ROW_SCALES if codes is not None and codes.dtype == torch.int8 else TAG_FP8_SCALES
+
+
+def ep_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
+                   residual_out: torch.Tensor | None, y: torch.Tensor | None,
+                   codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                   eps: float = 1e-6, quant: str | int = "none", stream=None) -> None:
+    _same_device(stream, x, residual, weight, residual_out, y, codes, scales)
+    _enqueue("ep_add_rmsnorm", _norm_rule(eps, quant), _tensor(x, TAG_TOKENS),
+             _tensor(residual, TAG_TOKENS), _tensor(weight, TAG_NORM_WEIGHT),
+             _tensor(residual_out, TAG_TOKENS), _tensor(y, TAG_TOKENS), _tensor(codes, TAG_TOKENS),
+             _tensor(scales, _scale_tag(codes)), _stream(stream))
+
+
+def ep_add_rmsnorm_bwd_workspace_bytes(rows: int, hidden: int) -> int:
+    out = c_size_t()
+    _check(load_library().ep_add_rmsnorm_bwd_workspace_bytes(rows, hidden, ctypes.byref(out)),
+           "ep_add_rmsnorm_bwd_workspace_bytes")
+    return out.value
+
+
+def ep_add_rmsnorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor,
+                       grad_residual_out: torch.Tensor | None, grad: torch.Tensor,
+                       grad_weight: torch.Tensor | None, workspace: torch.Tensor | None,
+                       eps: float = 1e-6, stream=None) -> None:
+    _same_device(stream, hidden, weight, grad_y, grad_residual_out, grad, grad_weight, workspace)
+    _enqueue("ep_add_rmsnorm_bwd", _norm_rule(eps, QUANT_NONE), _tensor(hidden, TAG_TOKENS),
+             _tensor(weight, TAG_NORM_WEIGHT), _tensor(grad_y, TAG_TOKENS),
+             _tensor(grad_residual_out, TAG_TOKENS), _tensor(grad, TAG_TOKENS),
+             _tensor(grad_weight, TAG_NORM_WEIGHT), _tensor(workspace, TAG_WORKSPACE),
+             _stream(stream))
+
+
+def ep_quantize_int8(tokens: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                     stream=None) -> None:
+    _same_device(stream, tokens, codes, scales)
+    _enqueue("ep_quantize_int8", _tensor(tokens, TAG_TOKENS), _tensor(codes, TAG_TOKENS),
+             _tensor(scales, TAG_ROW_SCALES), _stream(stream))
+
+
+def ep_dispatch_quantized(h: int, tokens: torch.Tensor, token_scales: torch.Tensor,
+                          topk_weights: torch.Tensor | None, recv_tokens: torch.Tensor,
+                          recv_scales: torch.Tensor, recv_topk_idx: torch.Tensor | None = None,
+                          recv_topk_weights: torch.Tensor | None = None, stream=None) -> None:
+    _same_device(stream, tokens, token_scales, topk_weights, recv_tokens, recv_scales,
+                 recv_topk_idx, recv_topk_weights)
+    tag = _scale_tag(tokens)
+    _enqueue("ep_dispatch_quantized", c_void_p(h), _tensor(tokens, TAG_TOKENS),
+             _tensor(token_scales, tag), _tensor(topk_weights, TAG_TOPK_WEIGHTS),
+             _tensor(recv_tokens, TAG_TOKENS), _tensor(recv_scales, tag),
+             _tensor(recv_topk_idx, TAG_TOPK_IDX), _tensor(recv_topk_weights, TAG_TOPK_WEIGHTS),
+             _stream(stream))
+
+
+def ep_expert_gemm_int8(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,
+                        expert_weights: torch.Tensor, expert_scales: torch.Tensor,
+                        slot_weights: torch.Tensor | None, slot_scales: torch.Tensor | None,
+                        out: torch.Tensor, stream=None, swiglu: bool = False) -> None:
+    _same_device(stream, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
+                 slot_scales, out)
+    name = "ep_expert_gemm_int8_swiglu" if swiglu else "ep_expert_gemm_int8"
+    _enqueue(name, c_void_p(h), _tensor(recv_tokens, TAG_TOKENS),
+             _tensor(recv_scales, TAG_ROW_SCALES), _tensor(expert_weights, TAG_EXPERT_WEIGHTS),
+             _tensor(expert_scales, TAG_ROW_SCALES), _tensor(slot_weights, TAG_EXPERT_WEIGHTS),
+             _tensor(slot_scales, TAG_ROW_SCALES), _tensor(out, TAG_TOKENS), _stream(stream))
+
+
+def ep_expert_gemm_int8_swiglu(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,
+                               expert_weights: torch.Tensor, expert_scales: torch.Tensor,
+                               slot_weights: torch.Tensor | None, slot_scales: torch.Tensor | None,
+                               out: torch.Tensor, stream=None) -> None:
+    ep_expert_gemm_int8(h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
+                        slot_scales, out, stream, swiglu=True)
 
 
 # ---------------------------------------------------------------------------
@@ -538,6 +705,25 @@ class Handle:
         w = torch.empty((self.num_tokens, k), dtype=torch.float32, device=logits.device)
         ep_route_plan(self.ptr, logits, idx, w, stream)
         return idx, w
+
+    def route_scored(self, logits: torch.Tensor, rule: RouteRule, bias: torch.Tensor | None = None,
+                     scores: bool = False, stream=None):
+        """Top-k routing by scores (fp32 or bf16 logits): returns (topk_idx,
+        weights), and with ``scores`` also the fp32 scores [T, E]."""
+        k = self.group.top_k
+        idx = torch.empty((self.num_tokens, k), dtype=torch.int32, device=logits.device)
+        w = torch.empty((self.num_tokens, k), dtype=torch.float32, device=logits.device)
+        s = torch.empty(logits.shape, dtype=torch.float32, device=logits.device) if scores else None
+        ep_route_scored(self.ptr, rule, logits, bias, idx, w, s, stream)
+        return (idx, w, s) if scores else (idx, w)
+
+    def route_scored_bwd(self, logits: torch.Tensor, rule: RouteRule, topk_idx: torch.Tensor,
+                         grad_weights: torch.Tensor, grad_scores: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+        """Gradient of the logits from those of the weights (and scores)."""
+        grad = torch.empty_like(logits)
+        ep_route_scored_bwd(self.ptr, rule, logits, topk_idx, grad_weights, grad_scores, grad, stream)
+        return grad
 
     def plan(self, topk_idx: torch.Tensor, stream=None) -> "Handle":
         ep_plan(self.ptr, topk_idx, stream)
@@ -650,11 +836,11 @@ class Buffer:
 
     def prefetch_replicas(self, expert_weights: torch.Tensor, handle: Handle,
                           slots: torch.Tensor | None = None, stream=None,
-                          scales: bool = False) -> torch.Tensor:
+                          scales: bool | str = False) -> torch.Tensor:
         """Copy the plan's replica experts' weights ([E, P...]) into their
         prefetch slots ([R, S, P...]); slots the plan leaves empty keep their
         contents (uninitialised if ``slots`` is None).  ``scales``: the
-        tensor is the fp32 scales of FP8 weights."""
+        tensor is the fp32 scales of FP8 weights (``"row"``: of INT8 weights)."""
         c = self.group.cfg
         if slots is None:
             slots = torch.empty((c.num_ranks, c.slots_per_rank) + tuple(expert_weights.shape[1:]),
@@ -710,6 +896,83 @@ class Buffer:
             scales = torch.empty(tuple(x.shape[:-1]) + (K // 128,), dtype=torch.float32, device=x.device)
         ep_quantize_fp8(x, codes, scales, stream, pow2=pow2)
         return codes, scales
+
+    @staticmethod
+    def add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
+                    eps: float = 1e-6, quant: str = "none", y: bool = True, stream=None):
+        """Residual addition and RMS norm of bf16 rows [..., H]: returns
+        (hidden, y, codes, scales), None for what was not asked for (hidden is
+        x itself without a residual).  ``quant``: "int8", "fp8", "fp8_pow2"."""
+        hidden = torch.empty_like(residual) if residual is not None else None
+        out = torch.empty_like(x) if y else None
+        codes = scales = None
+        if quant != "none":
+            i8 = quant == "int8"
+            codes = torch.empty(x.shape, dtype=torch.int8 if i8 else torch.float8_e4m3fn, device=x.device)
+            scales = torch.empty(tuple(x.shape[:-1]) + (() if i8 else (x.shape[-1] // 128,)),
+                                 dtype=torch.float32, device=x.device)
+        ep_add_rmsnorm(x, residual, weight, hidden, out, codes, scales, eps, quant, stream)
+        return x if hidden is None else hidden, out, codes, scales
+
+    @staticmethod
+    def add_rmsnorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor,
+                        grad_residual_out: torch.Tensor | None = None, eps: float = 1e-6,
+                        workspace: torch.Tensor | None = None, stream=None):
+        """Gradients (of x and the residual alike, of the weight in fp32)."""
+        H = hidden.shape[-1]
+        grad = torch.empty_like(hidden)
+        gw = torch.empty(H, dtype=torch.float32, device=hidden.device)
+        if workspace is None:
+            n = ep_add_rmsnorm_bwd_workspace_bytes(hidden.numel() // H, H) // 4
+            workspace = torch.empty(n, dtype=torch.float32, device=hidden.device)
+        ep_add_rmsnorm_bwd(hidden, weight, grad_y, grad_residual_out, grad, gw, workspace, eps, stream)
+        return grad, gw
+
+    @staticmethod
+    def quantize_int8(x: torch.Tensor, codes: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None, stream=None):
+        """bf16 rows [..., K] to int8 codes of the same shape and one fp32
+        scale a row; for the activation between the two FFN products, or
+        for INT8 weights."""
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        if scales is None:
+            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        ep_quantize_int8(x, codes, scales, stream)
+        return codes, scales
+
+    def dispatch_quantized(self, codes: torch.Tensor, scales: torch.Tensor,
+                           topk_weights: torch.Tensor | None, handle: Handle,
+                           recv_meta: bool = True, stream=None):
+        """Dispatch of rows that are 8 bits already (int8 with a scale a row,
+        or e4m3 with one per 128 channels) by a planned handle: returns
+        ``(recv_codes, recv_scales), recv_i, recv_w, handle, event`` like
+        ``dispatch``."""
+        rows, dev = handle.recv_rows, codes.device
+        recv = torch.empty(self.group.recv_shape(handle.num_tokens), dtype=codes.dtype, device=dev)
+        rs = torch.empty((rows,) + tuple(scales.shape[1:]), dtype=torch.float32, device=dev)
+        ri = torch.empty(rows, dtype=torch.int32, device=dev) if recv_meta else None
+        rw = torch.empty(rows, dtype=torch.float32, device=dev) if recv_meta and topk_weights is not None else None
+        ep_dispatch_quantized(handle.ptr, codes, scales, topk_weights, recv, rs, ri, rw, stream)
+        ev = torch.cuda.Event()
+        ev.record(torch.cuda.current_stream() if stream is None else stream)
+        return (recv, rs), ri, rw, handle, ev
+
+    def expert_gemm_int8(self, recv: torch.Tensor, recv_scales: torch.Tensor,
+                         expert_weights: torch.Tensor, expert_scales: torch.Tensor, handle: Handle,
+                         slots: torch.Tensor | None = None, slot_scales: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, stream=None,
+                         swiglu: bool = False) -> torch.Tensor:
+        """The grouped GEMM on INT8 operands: ``recv`` int8 [rows, K] with one
+        fp32 scale a row, weights int8 [E, N, K] with fp32 scales [E, N].
+        ``swiglu`` as in ``expert_gemm``."""
+        N, K = expert_weights.shape[1], expert_weights.shape[2]
+        rows = handle.recv_rows
+        if out is None:
+            out = torch.empty((rows, N // 2 if swiglu else N), dtype=torch.bfloat16, device=recv.device)
+        ep_expert_gemm_int8(handle.ptr, recv.view(rows, K), recv_scales.view(rows), expert_weights,
+                            expert_scales, slots, slot_scales, out, stream, swiglu=swiglu)
+        return out
 
     def dup_grad_reduce(self, replica_grads: torch.Tensor, owner_grads: torch.Tensor,
                         handle: Handle, replica_expert: torch.Tensor | None = None,

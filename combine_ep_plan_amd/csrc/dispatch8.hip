@@ -1,0 +1,65 @@
+// dispatch8.hip -- token rows that are 8 bits already (INT8 codes with one
+// fp32 scale a row, or FP8 codes with one per 128 channels) to their receive
+// rows on gfx950, codes and scales bit for bit (see dispatch.hip for the
+// layouts).  For rows a norm quantised: they are read at half the bytes of
+// bf16 and quantised once instead of once per copy.
+//
+// Copies: every row is read once and written k times, so the kernel is bound
+// by its writes.  One workgroup per token (per piece of a row for small
+// batches), 16-byte loads and stores.
+#include "device.h"
+#include "ep_internal.h"
+
+namespace epk {
+
+constexpr int kRow8Threads = 512;
+
+template <int K>
+__global__ __launch_bounds__(kRow8Threads) void k_dispatch_rows8(
+    const u32x4 *__restrict__ x, const float *__restrict__ xs, const int32_t *__restrict__ dst,
+    u32x4 *__restrict__ recv, float *__restrict__ recv_s, int64_t rows, int32_t V, int32_t S,
+    int32_t kr, int32_t chunk) {
+  constexpr int KN = K > 0 ? K : kMaxTopK;
+  const int64_t t = blockIdx.x;
+  const int32_t k = K > 0 ? K : kr;
+  const int32_t lo = blockIdx.y * chunk;
+  const int32_t hi = lo + chunk < V ? lo + chunk : V;
+  int32_t d[KN];
+#pragma unroll
+  for (int j = 0; j < KN; ++j) {
+    const int32_t r = (K > 0 || j < k) ? dst[t * k + j] : -1;
+    d[j] = r < rows ? r : -1;
+  }
+  for (int32_t v = lo + (int32_t)threadIdx.x; v < hi; v += kRow8Threads) {
+    const u32x4 val = x[t * V + v];
+#pragma unroll
+    for (int j = 0; j < KN; ++j)
+      if (d[j] >= 0) recv[(int64_t)d[j] * V + v] = val;
+  }
+  if (blockIdx.y == 0) {
+    for (int32_t i = threadIdx.x; i < S; i += kRow8Threads) {
+      const float s = xs[t * S + i];
+#pragma unroll
+      for (int j = 0; j < KN; ++j)
+        if (d[j] >= 0) recv_s[(int64_t)d[j] * S + i] = s;
+    }
+  }
+}
+
+hipError_t launch_dispatch_rows8(const Geometry &g, const Workspace &ws, const uint8_t *x,
+                                 const float *xs, int32_t H, int32_t S, uint8_t *recv,
+                                 float *recv_s, hipStream_t s) {
+  if (g.T == 0) return hipSuccess;
+  const int32_t V = H / 16;
+  int32_t chunk = V;
+  const int32_t pieces = row_pieces(g.T, V, &chunk);
+#define L(KK)                                                                                   \
+  hipLaunchKernelGGL((k_dispatch_rows8<KK>), dim3((unsigned)g.T, pieces), dim3(kRow8Threads), 0, \
+                     s, reinterpret_cast<const u32x4 *>(x), xs, ws.dst,                          \
+                     reinterpret_cast<u32x4 *>(recv), recv_s, g.rows, V, S, g.k, chunk)
+  EP_K_SWITCH(g.k, L)
+#undef L
+  return hipGetLastError();
+}
+
+}  // namespace epk

@@ -5,6 +5,7 @@
 // one stream synchronisation.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <new>
@@ -85,7 +86,8 @@ ep_status_t check_tensor(const ep_tensor_t *t, int32_t tag, int32_t dtype) {
   // rows of tokens, expert weights and gradients move as 16-byte vectors;
   // ids, router weights, logits and scales as 4-byte words
   const uintptr_t need =
-      (tag == EP_TAG_TOKENS || tag == EP_TAG_EXPERT_WEIGHTS || tag == EP_TAG_EXPERT_GRADS) ? 16 : 4;
+      (tag == EP_TAG_TOKENS || tag == EP_TAG_EXPERT_WEIGHTS || tag == EP_TAG_EXPERT_GRADS ||
+       tag == EP_TAG_NORM_WEIGHT || tag == EP_TAG_WORKSPACE) ? 16 : 4;
   if (reinterpret_cast<uintptr_t>(t->data) % need != 0) return EP_ERR_INVALID_ARG;
   return EP_OK;
 }
@@ -404,6 +406,31 @@ ep_status_t ep_plan(ep_handle_t h, const ep_tensor_t *topk_idx, void *stream) {
   return st;
 }
 
+// The optional weights and per-row outputs of a dispatch.
+static ep_status_t check_recv_meta(const epk::Geometry &g, const ep_tensor_t *topk_weights,
+                                   const ep_tensor_t *recv_topk_idx,
+                                   const ep_tensor_t *recv_topk_weights) {
+  ep_status_t st;
+  if (topk_weights) {
+    st = check_tensor(topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (!is_2d(topk_weights, g.T, g.k)) return EP_ERR_BAD_SHAPE;
+  }
+  if (recv_topk_idx) {
+    st = check_tensor(recv_topk_idx, EP_TAG_TOPK_IDX, EP_DTYPE_INT32);
+    if (st != EP_OK) return st;
+    if (!(recv_topk_idx->ndim == 1 && recv_topk_idx->sizes[0] == g.rows)) return EP_ERR_BAD_SHAPE;
+  }
+  if (recv_topk_weights) {
+    if (!topk_weights) return EP_ERR_INVALID_ARG;
+    st = check_tensor(recv_topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (!(recv_topk_weights->ndim == 1 && recv_topk_weights->sizes[0] == g.rows))
+      return EP_ERR_BAD_SHAPE;
+  }
+  return EP_OK;
+}
+
 // Argument checks of a dispatch (tokens, optional weights, receive rows and
 // scales, optional per-row outputs); EP_OK when all hold.
 static ep_status_t check_dispatch(const ep_handle *h, const ep_tensor_t *tokens,
@@ -425,24 +452,7 @@ static ep_status_t check_dispatch(const ep_handle *h, const ep_tensor_t *tokens,
     if (st != EP_OK) return st;
     if (!is_rows(recv_scales, g.rows, H / 128)) return EP_ERR_BAD_SHAPE;
   }
-  if (topk_weights) {
-    st = check_tensor(topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32);
-    if (st != EP_OK) return st;
-    if (!is_2d(topk_weights, g.T, g.k)) return EP_ERR_BAD_SHAPE;
-  }
-  if (recv_topk_idx) {
-    st = check_tensor(recv_topk_idx, EP_TAG_TOPK_IDX, EP_DTYPE_INT32);
-    if (st != EP_OK) return st;
-    if (!(recv_topk_idx->ndim == 1 && recv_topk_idx->sizes[0] == g.rows)) return EP_ERR_BAD_SHAPE;
-  }
-  if (recv_topk_weights) {
-    if (!topk_weights) return EP_ERR_INVALID_ARG;
-    st = check_tensor(recv_topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32);
-    if (st != EP_OK) return st;
-    if (!(recv_topk_weights->ndim == 1 && recv_topk_weights->sizes[0] == g.rows))
-      return EP_ERR_BAD_SHAPE;
-  }
-  return EP_OK;
+  return check_recv_meta(g, topk_weights, recv_topk_idx, recv_topk_weights);
 }
 
 // Enqueue a checked dispatch; fused: the layout of topk_idx in the same launch.
@@ -623,11 +633,13 @@ ep_status_t ep_prefetch_replicas(ep_handle_t h, const ep_tensor_t *expert_weight
   if (!h || !expert_weights || !slot_weights) return EP_ERR_INVALID_ARG;
   const epk::Geometry &g = h->geo;
   const int32_t dt = expert_weights->dtype;
-  // the weights themselves, or the fp32 scales of FP8 weights
-  const int32_t tag = expert_weights->tag == EP_TAG_FP8_SCALES ? EP_TAG_FP8_SCALES
-                                                                : EP_TAG_EXPERT_WEIGHTS;
-  if (tag == EP_TAG_FP8_SCALES ? dt != EP_DTYPE_FP32
-                               : dt != EP_DTYPE_BF16 && dt != EP_DTYPE_FP32 && dt != EP_DTYPE_FP8_E4M3)
+  // the weights themselves, or the fp32 scales of FP8 or INT8 weights
+  const int32_t wt = expert_weights->tag;
+  const bool scales = wt == EP_TAG_FP8_SCALES || wt == EP_TAG_ROW_SCALES;
+  const int32_t tag = scales ? wt : EP_TAG_EXPERT_WEIGHTS;
+  if (scales ? dt != EP_DTYPE_FP32
+             : dt != EP_DTYPE_BF16 && dt != EP_DTYPE_FP32 && dt != EP_DTYPE_FP8_E4M3 &&
+                   dt != EP_DTYPE_INT8)
     return EP_ERR_BAD_DTYPE;
   ep_status_t st = check_tensor(expert_weights, tag, dt);
   if (st != EP_OK) return st;
@@ -788,6 +800,368 @@ ep_status_t ep_expert_gemm_fp8_swiglu(ep_handle_t h, const ep_tensor_t *recv_tok
                          slot_scales, out, stream, true);
 }
 
+// Bounds of a routing rule for E experts.
+static bool rule_ok(const ep_route_rule_t *r, int32_t E) {
+  return r && (r->score == EP_SCORE_SOFTMAX || r->score == EP_SCORE_SIGMOID) &&
+         r->num_groups >= 1 && r->num_groups <= 64 && E % r->num_groups == 0 &&
+         r->kept_groups >= 1 && r->kept_groups <= r->num_groups &&
+         (r->group_score == EP_GROUP_MAX || r->group_score == EP_GROUP_TOP2) &&
+         (r->renormalise == 0 || r->renormalise == 1) && std::isfinite(r->scale);
+}
+
+// fp32 or bf16 logits [T, E]; *bf16 tells which.
+static ep_status_t check_logits(const ep_tensor_t *t, const epk::Geometry &g, bool *bf16) {
+  if (!t) return EP_ERR_INVALID_ARG;
+  *bf16 = t->dtype == EP_DTYPE_BF16;
+  const ep_status_t st = check_tensor(t, EP_TAG_ROUTER_LOGITS, *bf16 ? EP_DTYPE_BF16 : EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  return is_2d(t, g.T, g.E) ? EP_OK : EP_ERR_BAD_SHAPE;
+}
+
+// A [d0, d1] tensor of the given tag and dtype.
+static ep_status_t check_2d(const ep_tensor_t *t, int32_t tag, int32_t dtype, int64_t d0, int64_t d1) {
+  const ep_status_t st = check_tensor(t, tag, dtype);
+  if (st != EP_OK) return st;
+  return is_2d(t, d0, d1) ? EP_OK : EP_ERR_BAD_SHAPE;
+}
+
+ep_status_t ep_route_scored(ep_handle_t h, const ep_route_rule_t *rule, const ep_tensor_t *logits,
+                            const ep_tensor_t *bias, ep_tensor_t *topk_idx,
+                            ep_tensor_t *topk_weights, ep_tensor_t *scores, void *stream) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  const epk::Geometry &g = h->geo;
+  if (!rule_ok(rule, g.E)) return EP_ERR_INVALID_ARG;
+  bool bf16;
+  ep_status_t st = check_logits(logits, g, &bf16);
+  if (st != EP_OK) return st;
+  if (bias) {
+    st = check_tensor(bias, EP_TAG_ROUTER_BIAS, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (bias->ndim != 1 || bias->sizes[0] != g.E) return EP_ERR_BAD_SHAPE;
+  }
+  st = check_2d(topk_idx, EP_TAG_TOPK_IDX, EP_DTYPE_INT32, g.T, g.k);
+  if (st != EP_OK) return st;
+  st = check_2d(topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32, g.T, g.k);
+  if (st != EP_OK) return st;
+  if (scores) {
+    st = check_2d(scores, EP_TAG_ROUTER_LOGITS, EP_DTYPE_FP32, g.T, g.E);
+    if (st != EP_OK) return st;
+  }
+  return hip_status(epk::launch_route_scored(
+      g, *rule, logits->data, bf16, bias ? static_cast<const float *>(bias->data) : nullptr,
+      static_cast<int32_t *>(topk_idx->data), static_cast<float *>(topk_weights->data),
+      scores ? static_cast<float *>(scores->data) : nullptr, as_stream(stream)));
+}
+
+ep_status_t ep_route_scored_bwd(ep_handle_t h, const ep_route_rule_t *rule,
+                                const ep_tensor_t *logits, const ep_tensor_t *topk_idx,
+                                const ep_tensor_t *grad_topk_weights,
+                                const ep_tensor_t *grad_scores, ep_tensor_t *grad_logits,
+                                void *stream) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  const epk::Geometry &g = h->geo;
+  if (!rule_ok(rule, g.E)) return EP_ERR_INVALID_ARG;
+  bool bf16;
+  ep_status_t st = check_logits(logits, g, &bf16);
+  if (st != EP_OK) return st;
+  st = check_2d(topk_idx, EP_TAG_TOPK_IDX, EP_DTYPE_INT32, g.T, g.k);
+  if (st != EP_OK) return st;
+  st = check_2d(grad_topk_weights, EP_TAG_TOPK_WEIGHTS, EP_DTYPE_FP32, g.T, g.k);
+  if (st != EP_OK) return st;
+  if (grad_scores) {
+    st = check_2d(grad_scores, EP_TAG_ROUTER_LOGITS, EP_DTYPE_FP32, g.T, g.E);
+    if (st != EP_OK) return st;
+  }
+  st = check_2d(grad_logits, EP_TAG_ROUTER_LOGITS, logits->dtype, g.T, g.E);
+  if (st != EP_OK) return st;
+  return hip_status(epk::launch_route_scored_bwd(
+      g, h->ws, *rule, logits->data, bf16, static_cast<const int32_t *>(topk_idx->data),
+      static_cast<const float *>(grad_topk_weights->data),
+      grad_scores ? static_cast<const float *>(grad_scores->data) : nullptr, grad_logits->data,
+      as_stream(stream)));
+}
+
+// Rows of a [.., H] tensor the row kernels take (H a multiple of 8, at most
+// kRowMaxChannels; rows an int32); false if it is no such tensor.
+static bool row_tensor(const ep_tensor_t *t, int64_t *rows, int64_t *H) {
+  if (t->ndim < 2) return false;
+  *H = t->sizes[t->ndim - 1];
+  if (*H <= 0 || *H % 8 != 0) return false;
+  *rows = numel(t) / *H;
+  return *rows <= INT32_MAX;
+}
+
+// bf16 or fp32 rows of the given shape; *fp32 tells which.
+static ep_status_t check_stream_rows(const ep_tensor_t *t, int64_t rows, int64_t H, bool *fp32) {
+  if (!t) return EP_ERR_INVALID_ARG;
+  *fp32 = t->dtype == EP_DTYPE_FP32;
+  const ep_status_t st = check_tensor(t, EP_TAG_TOKENS, *fp32 ? EP_DTYPE_FP32 : EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  return is_rows(t, rows, H) ? EP_OK : EP_ERR_BAD_SHAPE;
+}
+
+static ep_status_t check_norm_weight(const ep_tensor_t *t, int64_t H, bool *fp32) {
+  if (!t) return EP_ERR_INVALID_ARG;
+  *fp32 = t->dtype == EP_DTYPE_FP32;
+  const ep_status_t st = check_tensor(t, EP_TAG_NORM_WEIGHT, *fp32 ? EP_DTYPE_FP32 : EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  return t->ndim == 1 && t->sizes[0] == H ? EP_OK : EP_ERR_BAD_SHAPE;
+}
+
+static bool norm_rule_ok(const ep_norm_rule_t *r) {
+  return r && std::isfinite(r->eps) && r->eps > 0.0 && r->reserved == 0 &&
+         r->quant >= EP_QUANT_NONE && r->quant <= EP_QUANT_INT8;
+}
+
+ep_status_t ep_add_rmsnorm(const ep_norm_rule_t *rule, const ep_tensor_t *x,
+                           const ep_tensor_t *residual, const ep_tensor_t *weight,
+                           ep_tensor_t *residual_out, ep_tensor_t *y, ep_tensor_t *codes,
+                           ep_tensor_t *scales, void *stream) {
+  if (!norm_rule_ok(rule)) return EP_ERR_INVALID_ARG;
+  const int32_t q = rule->quant;
+  if ((residual == nullptr) != (residual_out == nullptr)) return EP_ERR_INVALID_ARG;
+  if ((q != EP_QUANT_NONE) != (codes != nullptr) || (codes == nullptr) != (scales == nullptr))
+    return EP_ERR_INVALID_ARG;
+  if (!y && !codes) return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_tensor(x, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  epk::RmsNorm n{};
+  int64_t T, H;
+  if (!row_tensor(x, &T, &H)) return EP_ERR_BAD_SHAPE;
+  if (H > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
+  if (residual) {
+    st = check_stream_rows(residual, T, H, &n.res_fp32);
+    if (st != EP_OK) return st;
+    bool out_fp32;
+    st = check_stream_rows(residual_out, T, H, &out_fp32);
+    if (st != EP_OK) return st;
+    if (out_fp32 != n.res_fp32) return EP_ERR_BAD_DTYPE;
+  }
+  st = check_norm_weight(weight, H, &n.w_fp32);
+  if (st != EP_OK) return st;
+  if (y) {
+    st = check_tensor(y, EP_TAG_TOKENS, EP_DTYPE_BF16);
+    if (st != EP_OK) return st;
+    if (!is_rows(y, T, H)) return EP_ERR_BAD_SHAPE;
+  }
+  if (codes) {
+    const bool i8 = q == EP_QUANT_INT8;
+    if (!i8 && H % 128 != 0) return EP_ERR_UNSUPPORTED;
+    st = check_tensor(codes, EP_TAG_TOKENS, i8 ? EP_DTYPE_INT8 : EP_DTYPE_FP8_E4M3);
+    if (st != EP_OK) return st;
+    if (!is_rows(codes, T, H)) return EP_ERR_BAD_SHAPE;
+    st = check_tensor(scales, i8 ? EP_TAG_ROW_SCALES : EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (i8 ? numel(scales) != T : !is_rows(scales, T, H / 128)) return EP_ERR_BAD_SHAPE;
+  }
+  n.x = x->data;
+  n.residual = residual ? residual->data : nullptr;
+  n.w = weight->data;
+  n.hidden = residual_out ? residual_out->data : nullptr;
+  n.y = y ? y->data : nullptr;
+  n.codes = codes ? static_cast<uint8_t *>(codes->data) : nullptr;
+  n.scales = scales ? static_cast<float *>(scales->data) : nullptr;
+  n.T = (int32_t)T;
+  n.H = (int32_t)H;
+  n.quant = q;
+  n.eps = rule->eps;
+  return hip_status(epk::launch_add_rmsnorm(n, as_stream(stream)));
+}
+
+ep_status_t ep_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes) {
+  if (!bytes || rows < 0 || rows > INT32_MAX || H < 8 || H % 8 != 0 || H > epk::kRowMaxChannels)
+    return EP_ERR_INVALID_ARG;
+  *bytes = sizeof(float) * (size_t)epk::norm_bwd_groups((int32_t)rows) * (size_t)H;
+  return EP_OK;
+}
+
+ep_status_t ep_add_rmsnorm_bwd(const ep_norm_rule_t *rule, const ep_tensor_t *hidden,
+                               const ep_tensor_t *weight, const ep_tensor_t *grad_y,
+                               const ep_tensor_t *grad_residual_out, ep_tensor_t *grad,
+                               ep_tensor_t *grad_weight, ep_tensor_t *workspace, void *stream) {
+  if (!norm_rule_ok(rule) || rule->quant != EP_QUANT_NONE || !hidden) return EP_ERR_INVALID_ARG;
+  epk::RmsNormBwd n{};
+  int64_t T, H;
+  if (!row_tensor(hidden, &T, &H)) return EP_ERR_BAD_SHAPE;
+  ep_status_t st = check_stream_rows(hidden, T, H, &n.h_fp32);
+  if (st != EP_OK) return st;
+  if (H > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
+  st = check_norm_weight(weight, H, &n.w_fp32);
+  if (st != EP_OK) return st;
+  st = check_tensor(grad_y, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  if (!is_rows(grad_y, T, H)) return EP_ERR_BAD_SHAPE;
+  bool fp32;
+  if (grad_residual_out) {
+    st = check_stream_rows(grad_residual_out, T, H, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.h_fp32) return EP_ERR_BAD_DTYPE;
+  }
+  st = check_stream_rows(grad, T, H, &fp32);
+  if (st != EP_OK) return st;
+  if (fp32 != n.h_fp32) return EP_ERR_BAD_DTYPE;
+  if (grad_weight) {
+    st = check_tensor(grad_weight, EP_TAG_NORM_WEIGHT, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (grad_weight->ndim != 1 || grad_weight->sizes[0] != H) return EP_ERR_BAD_SHAPE;
+    const int64_t need = (int64_t)epk::norm_bwd_groups((int32_t)T) * H;
+    if (need > 0) {
+      st = check_tensor(workspace, EP_TAG_WORKSPACE, EP_DTYPE_FP32);
+      if (st != EP_OK) return st;
+      if (workspace->ndim != 1) return EP_ERR_BAD_SHAPE;
+      if (workspace->sizes[0] < need) return EP_ERR_WORKSPACE_TOO_SMALL;
+      n.part = static_cast<float *>(workspace->data);
+    }
+    n.gw = static_cast<float *>(grad_weight->data);
+  }
+  n.hidden = hidden->data;
+  n.w = weight->data;
+  n.gy = grad_y->data;
+  n.ghidden = grad_residual_out ? grad_residual_out->data : nullptr;
+  n.gx = grad->data;
+  n.T = (int32_t)T;
+  n.H = (int32_t)H;
+  n.eps = rule->eps;
+  return hip_status(epk::launch_rmsnorm_bwd(n, as_stream(stream)));
+}
+
+ep_status_t ep_quantize_int8(const ep_tensor_t *tokens, ep_tensor_t *codes, ep_tensor_t *scales,
+                             void *stream) {
+  ep_status_t st = check_tensor(tokens, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  st = check_tensor(codes, EP_TAG_TOKENS, EP_DTYPE_INT8);
+  if (st != EP_OK) return st;
+  st = check_tensor(scales, EP_TAG_ROW_SCALES, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  int64_t rows, K;
+  if (!row_tensor(tokens, &rows, &K)) return EP_ERR_BAD_SHAPE;
+  if (!is_rows(codes, rows, K) || numel(scales) != rows) return EP_ERR_BAD_SHAPE;
+  if (K > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
+  return hip_status(epk::launch_quantize_int8(static_cast<const uint16_t *>(tokens->data), rows,
+                                              (int32_t)K, static_cast<uint8_t *>(codes->data),
+                                              static_cast<float *>(scales->data),
+                                              as_stream(stream)));
+}
+
+ep_status_t ep_dispatch_quantized(ep_handle_t h, const ep_tensor_t *tokens,
+                                  const ep_tensor_t *token_scales,
+                                  const ep_tensor_t *topk_weights, ep_tensor_t *recv_tokens,
+                                  ep_tensor_t *recv_scales, ep_tensor_t *recv_topk_idx,
+                                  ep_tensor_t *recv_topk_weights, void *stream) {
+  if (!h || !tokens) return EP_ERR_INVALID_ARG;
+  const epk::Geometry &g = h->geo;
+  const int32_t H = h->g->cfg.hidden;
+  const bool i8 = tokens->dtype == EP_DTYPE_INT8;
+  const int32_t dt = i8 ? EP_DTYPE_INT8 : EP_DTYPE_FP8_E4M3;
+  const int32_t tag = i8 ? EP_TAG_ROW_SCALES : EP_TAG_FP8_SCALES;
+  ep_status_t st = check_2d(tokens, EP_TAG_TOKENS, dt, g.T, H);
+  if (st != EP_OK) return st;
+  if (H % (i8 ? 16 : 128) != 0) return EP_ERR_UNSUPPORTED;
+  const int32_t S = i8 ? 1 : H / 128;
+  const auto scales_ok = [&](const ep_tensor_t *t, int64_t rows) {
+    return i8 ? numel(t) == rows : is_rows(t, rows, S);
+  };
+  st = check_tensor(token_scales, tag, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  if (!scales_ok(token_scales, g.T)) return EP_ERR_BAD_SHAPE;
+  st = check_tensor(recv_tokens, EP_TAG_TOKENS, dt);
+  if (st != EP_OK) return st;
+  if (!is_rows(recv_tokens, g.rows, H)) return EP_ERR_BAD_SHAPE;
+  st = check_tensor(recv_scales, tag, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  if (!scales_ok(recv_scales, g.rows)) return EP_ERR_BAD_SHAPE;
+  st = check_recv_meta(g, topk_weights, recv_topk_idx, recv_topk_weights);
+  if (st != EP_OK) return st;
+  if (g.T >= 1 << 23) return EP_ERR_UNSUPPORTED;   // a launch counts its threads in 32 bits
+  if (!h->planned) return EP_ERR_NOT_PLANNED;
+  hipError_t e = epk::launch_dispatch_rows8(
+      g, h->ws, static_cast<const uint8_t *>(tokens->data),
+      static_cast<const float *>(token_scales->data), H, S,
+      static_cast<uint8_t *>(recv_tokens->data), static_cast<float *>(recv_scales->data),
+      as_stream(stream));
+  if (e == hipSuccess && (recv_topk_idx || recv_topk_weights))
+    e = epk::launch_recv_meta(
+        g, h->ws, topk_weights ? static_cast<const float *>(topk_weights->data) : nullptr,
+        recv_topk_idx ? static_cast<int32_t *>(recv_topk_idx->data) : nullptr,
+        recv_topk_weights ? static_cast<float *>(recv_topk_weights->data) : nullptr,
+        as_stream(stream));
+  return hip_status(e);
+}
+
+static ep_status_t expert_gemm_int8(ep_handle_t h, const ep_tensor_t *recv_tokens,
+                                    const ep_tensor_t *recv_scales,
+                                    const ep_tensor_t *expert_weights,
+                                    const ep_tensor_t *expert_scales,
+                                    const ep_tensor_t *slot_weights,
+                                    const ep_tensor_t *slot_scales, ep_tensor_t *out, void *stream,
+                                    bool glu) {
+  if (!h) return EP_ERR_INVALID_ARG;
+  const epk::Geometry &g = h->geo;
+  ep_status_t st = check_tensor(recv_tokens, EP_TAG_TOKENS, EP_DTYPE_INT8);
+  if (st != EP_OK) return st;
+  st = check_tensor(recv_scales, EP_TAG_ROW_SCALES, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  st = check_tensor(expert_weights, EP_TAG_EXPERT_WEIGHTS, EP_DTYPE_INT8);
+  if (st != EP_OK) return st;
+  st = check_tensor(expert_scales, EP_TAG_ROW_SCALES, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  st = check_tensor(out, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  const ep_tensor_t *w = expert_weights;
+  if (w->ndim != 3 || w->sizes[0] != g.E) return EP_ERR_BAD_SHAPE;
+  const int64_t N = w->sizes[1], K = w->sizes[2];
+  if (K <= 0 || K % 64 != 0 || N < 1 || N > INT32_MAX) return EP_ERR_BAD_SHAPE;
+  if (glu && N % 16 != 0) return EP_ERR_BAD_SHAPE;
+  if (!is_2d(expert_scales, g.E, N) || !is_rows(recv_tokens, g.rows, K) ||
+      numel(recv_scales) != g.rows || !is_rows(out, g.rows, glu ? N / 2 : N))
+    return EP_ERR_BAD_SHAPE;
+  if ((slot_weights == nullptr) != (slot_scales == nullptr)) return EP_ERR_INVALID_ARG;
+  const uint8_t *wslot = nullptr;
+  const float *swslot = nullptr;
+  if (slot_weights) {
+    st = check_tensor(slot_weights, EP_TAG_EXPERT_WEIGHTS, EP_DTYPE_INT8);
+    if (st != EP_OK) return st;
+    st = check_tensor(slot_scales, EP_TAG_ROW_SCALES, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (g.layout != EP_LAYOUT_STATIC) return EP_ERR_UNSUPPORTED;
+    const int64_t RS = (int64_t)g.R * g.S;
+    const ep_tensor_t *a = slot_weights, *b = slot_scales;
+    const bool w4 = a->ndim == 4 && a->sizes[0] == g.R && a->sizes[1] == g.S &&
+                    a->sizes[2] == N && a->sizes[3] == K;
+    const bool w3 = a->ndim == 3 && a->sizes[0] == RS && a->sizes[1] == N && a->sizes[2] == K;
+    const bool s3 = b->ndim == 3 && b->sizes[0] == g.R && b->sizes[1] == g.S && b->sizes[2] == N;
+    if ((!w4 && !w3) || (!s3 && !is_2d(b, RS, N))) return EP_ERR_BAD_SHAPE;
+    wslot = static_cast<const uint8_t *>(a->data);
+    swslot = static_cast<const float *>(b->data);
+  }
+  if (K > epk::kI8MaxK || !epk::gemm_int8_fits(g, (int32_t)K, (int32_t)N)) return EP_ERR_UNSUPPORTED;
+  if (!h->planned) return EP_ERR_NOT_PLANNED;
+  return hip_status(epk::launch_grouped_gemm_int8(
+      g, h->ws, static_cast<const uint8_t *>(recv_tokens->data),
+      static_cast<const float *>(recv_scales->data), static_cast<const uint8_t *>(w->data),
+      static_cast<const float *>(expert_scales->data), wslot, swslot, (int32_t)K, (int32_t)N,
+      static_cast<uint16_t *>(out->data), glu, as_stream(stream)));
+}
+
+ep_status_t ep_expert_gemm_int8(ep_handle_t h, const ep_tensor_t *recv_tokens,
+                                const ep_tensor_t *recv_scales, const ep_tensor_t *expert_weights,
+                                const ep_tensor_t *expert_scales, const ep_tensor_t *slot_weights,
+                                const ep_tensor_t *slot_scales, ep_tensor_t *out, void *stream) {
+  return expert_gemm_int8(h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
+                          slot_scales, out, stream, false);
+}
+
+ep_status_t ep_expert_gemm_int8_swiglu(ep_handle_t h, const ep_tensor_t *recv_tokens,
+                                       const ep_tensor_t *recv_scales,
+                                       const ep_tensor_t *expert_weights,
+                                       const ep_tensor_t *expert_scales,
+                                       const ep_tensor_t *slot_weights,
+                                       const ep_tensor_t *slot_scales, ep_tensor_t *out,
+                                       void *stream) {
+  return expert_gemm_int8(h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
+                          slot_scales, out, stream, true);
+}
+
 ep_status_t ep_run_calls(const ep_call_t *calls, int32_t n, int32_t *failed) {
   if (failed != nullptr) *failed = 0;
   if (n < 0 || (n > 0 && calls == nullptr)) return EP_ERR_INVALID_ARG;
@@ -818,6 +1192,32 @@ ep_status_t ep_run_calls(const ep_call_t *calls, int32_t n, int32_t *failed) {
         break;
       case EP_OP_EXPERT_GEMM_FP8_SWIGLU:
         st = ep_expert_gemm_fp8_swiglu(h, t(1), t(2), t(3), t(4), t(5), t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_ROUTE_SCORED:
+        st = ep_route_scored(h, static_cast<const ep_route_rule_t *>(c.p[1]), t(2), t(3), t(4), t(5),
+                             t(6), c.p[7]);
+        break;
+      case EP_OP_ROUTE_SCORED_BWD:
+        st = ep_route_scored_bwd(h, static_cast<const ep_route_rule_t *>(c.p[1]), t(2), t(3), t(4),
+                                 t(5), t(6), c.p[7]);
+        break;
+      case EP_OP_ADD_RMSNORM:
+        st = ep_add_rmsnorm(static_cast<const ep_norm_rule_t *>(c.p[0]), t(1), t(2), t(3), t(4), t(5),
+                            t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_ADD_RMSNORM_BWD:
+        st = ep_add_rmsnorm_bwd(static_cast<const ep_norm_rule_t *>(c.p[0]), t(1), t(2), t(3), t(4),
+                                t(5), t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_QUANTIZE_INT8: st = ep_quantize_int8(t(0), t(1), t(2), c.p[3]); break;
+      case EP_OP_DISPATCH_QUANTIZED:
+        st = ep_dispatch_quantized(h, t(1), t(2), t(3), t(4), t(5), t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_EXPERT_GEMM_INT8:
+        st = ep_expert_gemm_int8(h, t(1), t(2), t(3), t(4), t(5), t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_EXPERT_GEMM_INT8_SWIGLU:
+        st = ep_expert_gemm_int8_swiglu(h, t(1), t(2), t(3), t(4), t(5), t(6), t(7), c.p[8]);
         break;
       default: st = EP_ERR_INVALID_ARG; break;
     }

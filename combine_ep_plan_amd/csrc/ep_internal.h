@@ -120,6 +120,47 @@ hipError_t launch_grouped_gemm_fp8(const Geometry &g, const Workspace &ws, const
                                    const float *sx, const uint8_t *w, const float *sw,
                                    const uint8_t *wslot, const float *swslot, int32_t K, int32_t N,
                                    uint16_t *y, bool glu, hipStream_t s);
+// largest K of an INT8 product: 128 * 128 * K stays below 2^31
+constexpr int32_t kI8MaxK = 131071;
+bool gemm_int8_fits(const Geometry &g, int32_t K, int32_t N);
+hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, const uint8_t *x,
+                                    const float *sx, const uint8_t *w, const float *sw,
+                                    const uint8_t *wslot, const float *swslot, int32_t K,
+                                    int32_t N, uint16_t *y, bool glu, hipStream_t s);
+// 8-bit rows with S scales each to their receive rows
+hipError_t launch_dispatch_rows8(const Geometry &g, const Workspace &ws, const uint8_t *x,
+                                 const float *xs, int32_t H, int32_t S, uint8_t *recv,
+                                 float *recv_s, hipStream_t s);
+hipError_t launch_route_scored(const Geometry &g, const ep_route_rule_t &r, const void *logits,
+                               bool bf16, const float *bias, int32_t *idx, float *w, float *scores,
+                               hipStream_t s);
+hipError_t launch_route_scored_bwd(const Geometry &g, const Workspace &ws,
+                                   const ep_route_rule_t &r, const void *logits, bool bf16,
+                                   const int32_t *idx, const float *gw, const float *gs, void *gl,
+                                   hipStream_t s);
+constexpr int32_t kRowMaxChannels = 32768;  // longest row the norm and the INT8 quantiser hold
+struct RmsNorm {
+  const void *x, *residual, *w;
+  void *hidden, *y;
+  uint8_t *codes;
+  float *scales;
+  int32_t T, H, quant;
+  bool res_fp32, w_fp32;
+  double eps;
+};
+hipError_t launch_add_rmsnorm(const RmsNorm &n, hipStream_t s);
+struct RmsNormBwd {
+  const void *hidden, *w, *gy, *ghidden;
+  void *gx;
+  float *gw, *part;
+  int32_t T, H;
+  bool h_fp32, w_fp32;
+  double eps;
+};
+int32_t norm_bwd_groups(int32_t T);  // partial rows of grad_weight in the workspace
+hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s);
+hipError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int32_t K, uint8_t *codes,
+                                float *scales, hipStream_t s);
 // static scratch (scratch.hip): device address on the current device, and a
 // zero-filling kernel
 hipError_t scratch_base(int *dev, void **base);

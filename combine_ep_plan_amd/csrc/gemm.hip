@@ -57,26 +57,9 @@
 //    every eighth tile of a kind, so the XCDs walk the groups together and
 //    a hot expert's row tiles, spread over all of them at once, share its
 //    weight slices through the Infinity Cache.
-#include "device.h"
-#include "ep_internal.h"
+#include "gemm_common.h"
 
 namespace epk {
-
-constexpr int kTileM = kGemmBM;
-constexpr int kBN = 128;
-constexpr int kWavesM = 2, kWavesN = 2;
-constexpr int kGemmThreads = 64 * kWavesM * kWavesN;
-constexpr int kWTM = kTileM / kWavesM, kWTN = kBN / kWavesN;  // one wave's output block
-constexpr int kFM = kWTM / 32, kFN = kWTN / 32;                // 32 x 32 MFMA blocks per wave
-constexpr int kBK = 64;
-constexpr int kChunks = kBK / 8;  // 16-byte chunks in one row of a slab
-constexpr int kXcds = 8;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-__device__ __forceinline__ int swz(int row, int c) { return row * kChunks + (c ^ ((row >> 1) & 7)); }
-static_assert(kChunks == 8, "the swizzle assumes 128-byte slab rows");
 
 // ---------------------------------------------------------------------------
 // tile table
@@ -188,35 +171,6 @@ __global__ __launch_bounds__(1024) void k_gemm_tiles(TileArgs a, int32_t max_til
     a.ws.gemm_ntiles[0] = all < max_tiles ? all : max_tiles;
     a.ws.gemm_ntiles[1] = nf < max_tiles ? nf : max_tiles;
   }
-}
-
-// Work of workgroup blockIdx.x: its row tile (an index into the table) and
-// column tile.  Workgroup b runs on XCD b % 8; XCD x takes full tiles x,
-// x + 8, x + 16, ... and short tiles x, x + 8, ..., each in group order,
-// merged in proportion (Bresenham), every row tile with its column tiles one
-// after another.  So every XCD gets the same MFMA-bound and streaming-bound
-// work and runs both kinds side by side; the column tiles of a row tile stay
-// on one XCD (they share X rows in its L2); and the eight XCDs walk the
-// groups together, so the row tiles of one expert run on all of them at about
-// the same time and its weight slices, after the first read, come from the
-// Infinity Cache that the XCDs share (with each XCD taking a contiguous
-// eighth, the row tiles of a hot expert ran one after another on one XCD and
-// read its weights from HBM again each time).  The grid holds at least
-// (max_tiles / 8 + 2) * n_col_tiles workgroups per XCD (gemm_grid).
-__device__ __forceinline__ bool balanced_tile(const int32_t *__restrict__ ntiles,
-                                              int32_t max_tiles, int32_t n_col_tiles,
-                                              int32_t &tile, int32_t &col) {
-  const int32_t nf = ntiles[1], ns = ntiles[0] - nf;
-  const int32_t x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-  // this XCD's full and short tiles: those whose index is x modulo 8
-  const int32_t b = x < nf ? (nf - x + kXcds - 1) / kXcds : 0;
-  const int32_t n = b + (x < ns ? (ns - x + kXcds - 1) / kXcds : 0);
-  const int32_t p = slot / n_col_tiles;
-  if (p >= n) return false;
-  col = slot - p * n_col_tiles;
-  const int32_t before = (int32_t)((int64_t)p * b / n), upto = (int32_t)((int64_t)(p + 1) * b / n);
-  tile = upto > before ? x + kXcds * before : max_tiles - 1 - (x + kXcds * (p - before));
-  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -442,14 +396,6 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_grouped_gemm(
 
 // ---------------------------------------------------------------------------
 // grouped GEMM, 256 x 256 tiles (large groups)
-
-constexpr int kBM2 = 256, kBN2 = 256;                     // tile
-constexpr int kWTM2 = kBM2 / 2, kWTN2 = kBN2 / 2;         // one wave's block (2 x 2 waves)
-constexpr int kFM2 = kWTM2 / 32, kFN2 = kWTN2 / 32;       // 4 x 4 MFMA accumulators per wave
-constexpr int kLoads2 = kBM2 * kChunks / kGemmThreads;    // 16-byte loads per thread per slab of X
-constexpr int kLoadsB2 = kBN2 * kChunks / kGemmThreads;   // ... and of W
-constexpr int kSlabA2 = kBM2 * kChunks, kSlabB2 = kBN2 * kChunks;
-constexpr int kBufDword3 = 0x00020000;                    // buffer resource word 3 (raw, 32-bit data)
 
 // Epilogue of the 256 x 256 kernels: the fp32 tile (a wave's 4 x 4 blocks of
 // 32 x 32) to bf16 rows of Y (plain, or SwiGLU pairs).  N % 8 == 0: through
@@ -1022,28 +968,6 @@ __device__ __forceinline__ void mfma8_rows(f32x16 (&acc)[kFM2][kFN2], const i32x
 static_assert(kFN2 == 4, "mfma8_rows writes four column blocks");
 
 
-#define LDS_PTR(p) ((__attribute__((address_space(3))) void *)(p))
-
-// A buffer load whose lanes' 16 (or 4) bytes land in LDS at m0 + lane * 16
-// (or 4), m0 being the wave's LDS base.  Written in asm on purpose: the
-// compiler tracks its own form of this load and, unable to tell which part
-// of LDS it writes, makes every later LDS read wait until it has landed --
-// which would let no slab load run under the MFMAs of the previous slab.
-// Here the caller owns the waits (s_waitcnt vmcnt before the barrier that
-// publishes the data).  No result register: nothing the compiler allocates
-// is written late.  The s_nop is the wait state the hardware needs between
-// the write of m0 and the load that reads it.
-__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_base,
-                                           uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base) : "memory");
-}
-__device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_base,
-                                          uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base) : "memory");
-}
-
 template <bool GLU>
 __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_fp8_256(
     const u32x4 *__restrict__ X, const float *__restrict__ SX, const u32x4 *__restrict__ W,
@@ -1250,7 +1174,6 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_fp8_256(
   if (any_bad != 0u && lane == 0) atomicOr(status, kFlagScaleFormat);
   wide_epilogue<GLU>(acc, lds, rows, row0, n0, N, Y, wm, wn, lane, tid);
 }
-#undef LDS_PTR
 
 // Row tiles of kTileM rows the plan can produce; the 256-row tiling needs no more.
 int32_t gemm_max_tiles(const Geometry &g) {
@@ -1268,11 +1191,8 @@ int32_t gemm_max_tiles(const Geometry &g) {
     else hipLaunchKernelGGL(KERN<false>, __VA_ARGS__);        \
   } while (0)
 
-// Workgroups of a GEMM launch: per XCD, room for an eighth of each kind of
-// row tile rounded up (at most max_tiles / 8 + 2 row tiles), times the
-// column tiles (balanced_tile).
 static unsigned gemm_grid(int32_t max_tiles, int32_t ncol) {
-  return (unsigned)((int64_t)kXcds * (max_tiles / kXcds + 2) * ncol);
+  return (unsigned)gemm_grid_blocks(max_tiles, ncol);
 }
 
 static bool gemm_uses_wide_tiles(const Geometry &g, int32_t K, int32_t N) {
@@ -1287,10 +1207,12 @@ static bool gemm_fp8_uses_wide_tiles(const Geometry &g, int32_t K, int32_t N) {
          (int64_t)kBM2 * K <= INT32_MAX;
 }
 
-// At most as many 256-row tiles as the table holds 128-row ones.
-static int32_t wide_max_tiles(const Geometry &g) {
-  const int64_t groups = g.layout == kStatic ? 2 * (int64_t)g.E + g.R : g.E;
-  return (int32_t)((g.n + kBM2 - 1) / kBM2 + groups);
+hipError_t launch_gemm_tiles(const Geometry &g, const Workspace &ws, bool slots, bool wide,
+                             int32_t max_tiles, hipStream_t s) {
+  const TileArgs ta{g, ws, slots ? 1 : 0};
+  if (wide) hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
+  else hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
+  return hipGetLastError();
 }
 
 hipError_t launch_grouped_gemm(const Geometry &g, const Workspace &ws, const uint16_t *x,

@@ -40,8 +40,10 @@
  *               status word as EP_FLAG_* bits and read with
  *               ep_handle_status, the only call that waits for the GPU.
  *   Dtypes.     tokens bf16; top-k indices int32; top-k weights fp32; FP8
- *               rows OCP e4m3fn (bias 7, max 448); FP8 scales fp32.
- *   Sizes.      H % 8 == 0 (16-byte rows); H % 128 == 0 for FP8 dispatch;
+ *               rows OCP e4m3fn (bias 7, max 448); FP8 scales fp32; INT8 rows
+ *               int8 with one fp32 scale a row.
+ *   Sizes.      H % 8 == 0 (16-byte rows); H % 128 == 0 for FP8 dispatch,
+ *               H % 16 == 0 for INT8 dispatch;
  *               1 <= top_k <= 16; 1 <= E <= 1024; E % R == 0.
  *   Threads.    A handle is used by one stream at a time; calls on one
  *               handle from two streams without ordering race.
@@ -82,25 +84,30 @@ typedef enum ep_status {
                                     grouped GEMM was not a positive normal power of two (its
                                     block was taken at the scale's exponent) */
 
-/* Tensor roles (NCCL EP paper listing, Table IV).  EP_TAG_EXPERT_GRADS,
- * EP_TAG_ROUTER_LOGITS and EP_TAG_EXPERT_WEIGHTS are this library's additions
- * for the duplicated-expert gradient reduce, the routing step and the
- * replica-weight prefetch. */
+/* Tensor roles (NCCL EP paper listing, Table IV).  EP_TAG_EXPERT_GRADS and the
+ * roles after it are this library's additions: for the duplicated-expert
+ * gradient reduce, the routing step, the replica-weight prefetch, INT8 rows and
+ * weights, the router's balance bias, and the norm. */
 typedef enum ep_tensor_tag {
   EP_TAG_TOKENS = 0,        /* token rows: dispatch in/out, combine in/out, their grads */
   EP_TAG_TOPK_IDX = 1,      /* expert ids (int32); -1 = no expert */
   EP_TAG_TOPK_WEIGHTS = 2,  /* router weights (fp32) and their gradients */
   EP_TAG_FP8_SCALES = 3,    /* one fp32 scale per 128 channels of an FP8 row */
   EP_TAG_EXPERT_GRADS = 4,  /* expert parameter gradients */
-  EP_TAG_ROUTER_LOGITS = 5,  /* router scores per token and expert (fp32) */
-  EP_TAG_EXPERT_WEIGHTS = 6  /* expert parameters: owners' weights and prefetch slots */
+  EP_TAG_ROUTER_LOGITS = 5,  /* router logits or scores per token and expert, and their gradients */
+  EP_TAG_EXPERT_WEIGHTS = 6, /* expert parameters: owners' weights and prefetch slots */
+  EP_TAG_ROW_SCALES = 7,     /* one fp32 scale per INT8 row (tokens), or per row of INT8 weights */
+  EP_TAG_ROUTER_BIAS = 8,    /* balance bias of each expert (fp32) */
+  EP_TAG_NORM_WEIGHT = 9,    /* the norm's weight per channel and its gradient */
+  EP_TAG_WORKSPACE = 10      /* scratch memory of one call (fp32, 1-D) */
 } ep_tensor_tag_t;
 
 typedef enum ep_dtype {
   EP_DTYPE_BF16 = 0,
   EP_DTYPE_FP32 = 1,
   EP_DTYPE_FP8_E4M3 = 2,
-  EP_DTYPE_INT32 = 3
+  EP_DTYPE_INT32 = 3,
+  EP_DTYPE_INT8 = 4
 } ep_dtype_t;
 
 /* Receive-buffer layouts (NCCL EP listing, Table III; MoonEP article, par. 3-4). */
@@ -161,8 +168,9 @@ typedef enum ep_fp8_scales {
 } ep_fp8_scales_t;
 
 /* Non-owning view of a contiguous row-major device tensor.  data must be
- * 16-byte aligned for the tags TOKENS, EXPERT_WEIGHTS and EXPERT_GRADS (rows
- * move as 16-byte vectors) and 4-byte aligned for the others; a misaligned
+ * 16-byte aligned for the tags TOKENS, EXPERT_WEIGHTS, EXPERT_GRADS,
+ * NORM_WEIGHT and WORKSPACE (rows move as 16-byte vectors) and 4-byte aligned
+ * for the others; a misaligned
  * view is rejected with EP_ERR_INVALID_ARG. */
 typedef struct ep_tensor {
   void *data;           /* device pointer (may be NULL only if the tensor is empty) */
@@ -465,9 +473,10 @@ ep_status_t ep_dup_grad_reduce(ep_handle_t h, const ep_tensor_t *replica_grads,
  * segments[i][0]'s row of expert_weights.  Slots the plan leaves empty, and
  * segments without a slot, are not touched (the overflow of the inference
  * slot mode reads the owner's row directly).  Call it once per projection
- * (for FP8 weights, once for the codes and once for their scales).
- * expert_weights: [E, P...], tag EXPERT_WEIGHTS, dtype bf16, fp32 or FP8;
- *                 or the scales of FP8 weights: tag FP8_SCALES, fp32.
+ * (for FP8 and INT8 weights, once for the codes and once for their scales).
+ * expert_weights: [E, P...], tag EXPERT_WEIGHTS, dtype bf16, fp32, FP8 or INT8;
+ *                 or the scales of FP8 or INT8 weights: tag FP8_SCALES or
+ *                 ROW_SCALES, fp32.
  * slot_weights:   [R, S, P...] output, same tag and dtype; the 2-D form
  *                 [R*S, P] is accepted too.
  * A row (P elements) must be a multiple of 4 bytes (rows that are a
@@ -565,6 +574,211 @@ ep_status_t ep_expert_gemm_fp8_swiglu(ep_handle_t h, const ep_tensor_t *recv_tok
                                       void *stream);
 
 /* ------------------------------------------------------------------------
+ * The front of an MoE layer: scored routing, the norm before it, 8-bit rows,
+ * and the experts' INT8 products.  The chain a layer runs is
+ *   ep_add_rmsnorm -> (router logits) -> ep_route_scored -> ep_plan ->
+ *   ep_dispatch_quantized -> ep_expert_gemm_int8_swiglu -> ep_quantize_int8 ->
+ *   ep_expert_gemm_int8 -> ep_combine. */
+
+typedef enum ep_score {
+  EP_SCORE_SOFTMAX = 0, /* s = softmax over the token's E logits */
+  EP_SCORE_SIGMOID = 1  /* s = 1 / (1 + e^-l), each expert by itself */
+} ep_score_t;
+
+typedef enum ep_group_score {
+  EP_GROUP_MAX = 0, /* an expert group counts as much as its best expert */
+  EP_GROUP_TOP2 = 1 /* ... as the sum of its two best */
+} ep_group_score_t;
+
+/* How a token chooses its experts (ep_route_scored). */
+typedef struct ep_route_rule {
+  int32_t score;       /* ep_score_t */
+  int32_t num_groups;  /* expert groups of E / num_groups consecutive experts, 1..64, dividing E */
+  int32_t kept_groups; /* groups a token may choose from, 1..num_groups */
+  int32_t group_score; /* ep_group_score_t */
+  int32_t renormalise; /* 1: the k weights are divided by their sum, 0: they are the scores */
+  float scale;         /* factor of the weights, finite */
+} ep_route_rule_t;
+
+/* Top-k routing by scores.  For every token, with scores s (rule.score):
+ *   choice_e = s_e + bias_e; a group's value is the largest choice in it, or
+ *   the sum of the two largest; the kept_groups best groups stay; the token's
+ *   experts are the k largest choices in them, in descending order; its
+ *   weights are scale * s (of the chosen; the bias takes no part), divided by
+ *   the sum of the chosen s when renormalise is 1.
+ * Equal values go to the lower group and the lower expert.  Choices are
+ * compared in double precision (where nothing is added to the scores, by the
+ * logits), so ids near a border do not depend on rounding.  A logit of -inf
+ * or NaN masks its expert: it is never chosen and scores 0 (+inf counts as
+ * the largest float; a bias that is NaN or -inf masks too).  Where fewer than
+ * k experts are left the extra choices are -1 with weight 0; a token with no
+ * expert at all gets -1 everywhere.  Renormalised weights sum to scale
+ * whatever the logits: nothing underflows on the way.
+ * logits:       fp32 or bf16 [T, E], tag ROUTER_LOGITS.
+ * bias:         NULL or fp32 [E], tag ROUTER_BIAS.
+ * topk_idx, topk_weights: as for ep_route.
+ * scores:       NULL or fp32 [T, E] output, tag ROUTER_LOGITS: s, for a
+ *               balance loss.
+ * T, E and k are the handle's; needs no ep_plan.  Errors:
+ * EP_ERR_INVALID_ARG for a rule outside the ranges above. */
+ep_status_t ep_route_scored(ep_handle_t h, const ep_route_rule_t *rule, const ep_tensor_t *logits,
+                            const ep_tensor_t *bias, ep_tensor_t *topk_idx,
+                            ep_tensor_t *topk_weights, ep_tensor_t *scores, void *stream);
+
+/* Backward of ep_route_scored: the gradient of the logits from those of the
+ * weights and, if given, of the scores.  The choice has no gradient, nor has
+ * the bias.  With s the scores, c the scale, gw the weights' gradients and p
+ * the chosen scores over their sum:
+ *   ds = grad_scores + c * gw on the chosen experts     (not renormalised)
+ *   ds = grad_scores + c * (gw_j - sum_i gw_i p_i) / sum(s chosen)
+ *   sigmoid: dl = ds s (1 - s);  softmax: dl_e = s_e (ds_e - sum ds s)
+ * (renormalised parts are formed from p, so nothing is divided by a sum that
+ * underflows).  Entries of -1 and masked experts get and give none; ids
+ * outside [0, E) other than -1 are skipped and set EP_FLAG_INDEX_RANGE; an
+ * expert that an entry list names twice gets the sum.
+ * logits:            as given to ep_route_scored.
+ * topk_idx:          int32 [T, k] (its output).
+ * grad_topk_weights: fp32 [T, k], tag TOPK_WEIGHTS.
+ * grad_scores:       NULL or fp32 [T, E], tag ROUTER_LOGITS.
+ * grad_logits:       [T, E] output of the logits' dtype, tag ROUTER_LOGITS. */
+ep_status_t ep_route_scored_bwd(ep_handle_t h, const ep_route_rule_t *rule,
+                                const ep_tensor_t *logits, const ep_tensor_t *topk_idx,
+                                const ep_tensor_t *grad_topk_weights,
+                                const ep_tensor_t *grad_scores, ep_tensor_t *grad_logits,
+                                void *stream);
+
+/* 8-bit form of the rows a norm hands on. */
+typedef enum ep_quant {
+  EP_QUANT_NONE = 0,
+  EP_QUANT_FP8 = 1,      /* e4m3, one scale per 128 channels, amax / 448 */
+  EP_QUANT_FP8_POW2 = 2, /* ... the power of two at or above it */
+  EP_QUANT_INT8 = 3      /* int8, one scale per row, amax / 127 */
+} ep_quant_t;
+
+typedef struct ep_norm_rule {
+  double eps;    /* added to the mean square; positive and finite */
+  int32_t quant; /* ep_quant_t (0 for the backward) */
+  int32_t reserved; /* must be 0 */
+} ep_norm_rule_t;
+
+/* Residual addition and RMS norm of token rows.  For every row:
+ *   h = round(x + residual) to the residual's dtype   (h = x without one)
+ *   y = h * w / sqrt(mean(h^2) + eps)
+ * The norm reads h as it is stored.  The sum of squares runs in double and
+ * 1/sqrt is rounded once to fp32; y = (h * w) * that, in fp32.
+ * x:            bf16 [T, H] (any leading shape), tag TOKENS; H % 8 == 0,
+ *               H <= 32768, T < 2^31.
+ * residual:     NULL, or bf16 or fp32 [T, H], tag TOKENS.
+ * weight:       bf16 or fp32 [H], tag NORM_WEIGHT.
+ * residual_out: [T, H] of the residual's dtype, tag TOKENS: h.  Given if and
+ *               only if residual is; may be the residual's own buffer.
+ * y:            NULL or bf16 [T, H], tag TOKENS, rounded to nearest even.
+ * codes, scales: given if and only if rule.quant is not NONE: the rows in 8
+ *               bits, quantised from the fp32 y.  FP8: e4m3 [T, H] and fp32
+ *               [T, H/128] (tag FP8_SCALES), H % 128 == 0, the FP8 dispatch's
+ *               recipe.  INT8: int8 [T, H] and fp32 [T] (tag ROW_SCALES):
+ *               scale = amax / 127 (1 for a row of zeros, at least 2^-126),
+ *               code = the integer nearest to y / scale, ties to even.  A row
+ *               (FP8: a block) with a value that is not finite gets codes 0
+ *               and a NaN scale.
+ * At least one of y and codes is given.  Enqueues one kernel. */
+ep_status_t ep_add_rmsnorm(const ep_norm_rule_t *rule, const ep_tensor_t *x,
+                           const ep_tensor_t *residual, const ep_tensor_t *weight,
+                           ep_tensor_t *residual_out, ep_tensor_t *y, ep_tensor_t *codes,
+                           ep_tensor_t *scales, void *stream);
+
+/* Bytes of the workspace ep_add_rmsnorm_bwd needs for grad_weight (partial
+ * sums; 0 for no rows).  Errors: EP_ERR_INVALID_ARG. */
+ep_status_t ep_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes);
+
+/* Backward of ep_add_rmsnorm.  With n = h / sqrt(mean(h^2) + eps), g =
+ * grad_y * w:
+ *   grad = (g - n * mean(g * n)) / sqrt(mean(h^2) + eps) + grad_residual_out
+ *   grad_weight = sum over rows of grad_y * n
+ * grad is the gradient of x and of the residual alike.
+ * hidden:            bf16 or fp32 [T, H], tag TOKENS: h (residual_out, or x).
+ * weight:            as in the forward.
+ * grad_y:            bf16 [T, H], tag TOKENS.
+ * grad_residual_out: NULL or [T, H] of hidden's dtype, tag TOKENS: the
+ *                    gradient that reaches h by the residual stream.
+ * grad:              [T, H] output of hidden's dtype, tag TOKENS; may be the
+ *                    buffer of grad_residual_out.
+ * grad_weight:       NULL or fp32 [H] output, tag NORM_WEIGHT (0 for no rows).
+ * workspace:         fp32, 1-D, tag WORKSPACE, of at least
+ *                    ep_add_rmsnorm_bwd_workspace_bytes; may be NULL without
+ *                    grad_weight.  One call in flight at a time may use it.
+ * The sums are added in a fixed order: results repeat bit for bit.
+ * Enqueues up to two kernels. */
+ep_status_t ep_add_rmsnorm_bwd(const ep_norm_rule_t *rule, const ep_tensor_t *hidden,
+                               const ep_tensor_t *weight, const ep_tensor_t *grad_y,
+                               const ep_tensor_t *grad_residual_out, ep_tensor_t *grad,
+                               ep_tensor_t *grad_weight, ep_tensor_t *workspace, void *stream);
+
+/* INT8 quantisation of bf16 rows, the recipe of EP_QUANT_INT8: the activation
+ * between the expert FFN's two INT8 products, rows for an INT8 dispatch, or
+ * INT8 weights (one scale per output row).
+ * tokens: bf16 [rows, K] (any leading shape), tag TOKENS; K % 8 == 0,
+ *         K <= 32768, rows < 2^31.
+ * codes:  int8, the same rows and K, tag TOKENS.
+ * scales: fp32 [rows] (any shape of rows elements), tag ROW_SCALES.
+ * Needs no handle.  Enqueues one kernel. */
+ep_status_t ep_quantize_int8(const ep_tensor_t *tokens, ep_tensor_t *codes, ep_tensor_t *scales,
+                             void *stream);
+
+/* ep_dispatch for rows that are 8 bits already (a norm's, or a quantiser's):
+ * codes and scales are copied bit for bit to every routed row.
+ * tokens:       INT8 or FP8 e4m3 [T, H], tag TOKENS; H % 16 == 0 (INT8),
+ *               H % 128 == 0 (FP8), else EP_ERR_UNSUPPORTED.
+ * token_scales: INT8: fp32 [T], tag ROW_SCALES; FP8: fp32 [T, H/128], tag
+ *               FP8_SCALES.
+ * recv_tokens:  the tokens' dtype, [recv_rows, H] (any leading shape), tag
+ *               TOKENS.
+ * recv_scales:  fp32 [recv_rows] or [recv_rows, H/128], the tokens' tag.
+ * topk_weights, recv_topk_idx, recv_topk_weights: as for ep_dispatch.
+ * Rows no entry maps to are not written.  EP_ERR_NOT_PLANNED before ep_plan.
+ * T < 2^23. */
+ep_status_t ep_dispatch_quantized(ep_handle_t h, const ep_tensor_t *tokens,
+                                  const ep_tensor_t *token_scales,
+                                  const ep_tensor_t *topk_weights, ep_tensor_t *recv_tokens,
+                                  ep_tensor_t *recv_scales, ep_tensor_t *recv_topk_idx,
+                                  ep_tensor_t *recv_topk_weights, void *stream);
+
+/* Grouped GEMM of the experts on INT8 operands: groups and slots as in
+ * ep_expert_gemm; for every group row i and column n < N
+ *   out[i, n] = bf16( recv_scales[i] * W_scales[n] *
+ *                     sum_c recv_tokens[i, c] * W[n, c] )
+ * The sum is exact (32-bit integers); it is converted to fp32, multiplied by
+ * the fp32 product of the two scales and rounded once to nearest even.
+ * recv_tokens:    int8 [recv_rows, K], tag TOKENS; K % 64 == 0, K <= 131071.
+ * recv_scales:    fp32 [recv_rows] (any shape of recv_rows elements), tag
+ *                 ROW_SCALES.
+ * expert_weights: int8 [E, N, K], tag EXPERT_WEIGHTS.
+ * expert_scales:  fp32 [E, N], tag ROW_SCALES.
+ * slot_weights, slot_scales: both NULL, or (STATIC only) int8 [R, S, N, K]
+ *                 (or [R*S, N, K]) and fp32 [R, S, N] (or [R*S, N]) filled
+ *                 by ep_prefetch_replicas, tags EXPERT_WEIGHTS and
+ *                 ROW_SCALES.
+ * out:            bf16 [recv_rows, N], tag TOKENS; rows no group covers are
+ *                 not written.
+ * Errors: as for ep_expert_gemm_fp8; EP_ERR_UNSUPPORTED for K > 131071 or a
+ * launch too large for one grid.  Enqueues two kernels (tile table, GEMM). */
+ep_status_t ep_expert_gemm_int8(ep_handle_t h, const ep_tensor_t *recv_tokens,
+                                const ep_tensor_t *recv_scales, const ep_tensor_t *expert_weights,
+                                const ep_tensor_t *expert_scales, const ep_tensor_t *slot_weights,
+                                const ep_tensor_t *slot_scales, ep_tensor_t *out, void *stream);
+
+/* The same with the SwiGLU store: weight rows (and scales) interleave gate
+ * (even) and up (odd); out bf16 [recv_rows, N/2], N % 16 == 0 (else
+ * EP_ERR_BAD_SHAPE): silu(gate) * up of the fp32 values, rounded once. */
+ep_status_t ep_expert_gemm_int8_swiglu(ep_handle_t h, const ep_tensor_t *recv_tokens,
+                                       const ep_tensor_t *recv_scales,
+                                       const ep_tensor_t *expert_weights,
+                                       const ep_tensor_t *expert_scales,
+                                       const ep_tensor_t *slot_weights,
+                                       const ep_tensor_t *slot_scales, ep_tensor_t *out,
+                                       void *stream);
+
+/* ------------------------------------------------------------------------
  * Recorded calls.  A launch-bound loop -- a low-latency decode step, a few
  * kernels of a few microseconds each (NCCL EP listing, Table III: the LL
  * mode for batches of 1 to 128 tokens) -- spends about as much host time
@@ -588,12 +802,20 @@ typedef enum ep_op {
   EP_OP_EXPERT_GEMM = 11,
   EP_OP_EXPERT_GEMM_SWIGLU = 12,
   EP_OP_EXPERT_GEMM_FP8 = 13,
-  EP_OP_EXPERT_GEMM_FP8_SWIGLU = 14
+  EP_OP_EXPERT_GEMM_FP8_SWIGLU = 14,
+  EP_OP_ROUTE_SCORED = 15,
+  EP_OP_ROUTE_SCORED_BWD = 16,
+  EP_OP_ADD_RMSNORM = 17,
+  EP_OP_ADD_RMSNORM_BWD = 18,
+  EP_OP_QUANTIZE_INT8 = 19,
+  EP_OP_DISPATCH_QUANTIZED = 20,
+  EP_OP_EXPERT_GEMM_INT8 = 21,
+  EP_OP_EXPERT_GEMM_INT8_SWIGLU = 22
 } ep_op_t;
 
 /* One recorded call.  p holds the entry point's pointer arguments in its
- * own order -- the handle first where it takes one, the tensor views (NULL
- * where the entry point accepts NULL), the stream last; i0 holds its one
+ * own order -- the handle first where it takes one, the tensor views and rules
+ * (NULL where the entry point accepts NULL), the stream last; i0 holds its one
  * integer argument (ep_quantize_fp8's fp8_scales; p is then tokens, codes,
  * scales, stream).  Slots past the entry point's arguments are ignored. */
 typedef struct ep_call {
