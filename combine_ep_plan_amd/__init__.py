@@ -193,20 +193,34 @@ def _check(code: int, what: str) -> None:
 _VIEWS: dict = {}
 _VIEWS_MAX = 4096
 _RECORDING = threading.local()   # prepare(): the calls being recorded and what they use
+_recorders = 0                   # threads inside prepare(): the thread-local is only asked if any
+_recorders_lock = threading.Lock()
 
 
-def _tensor(t: torch.Tensor | None, tag: int):
+def _device(stream) -> int:
+    """The device a call runs on: its stream's, or the current one."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.device_index
+    return torch._C._cuda_getDevice()
+
+
+def _tensor(t: torch.Tensor | None, tag: int, dev: int | None = None):
     """ep_tensor_t view of a contiguous device tensor (None -> NULL).  A view
     is a pure function of (address, dtype, shape, tag) and the library never
     writes to it, so built views are kept and reused: the marshalling of a
-    call that repeats its tensors costs a dictionary lookup."""
+    call that repeats its tensors costs a dictionary lookup.  With ``dev``
+    the tensor must live on that device."""
     if t is None:
         return None
-    keep = getattr(_RECORDING, "keep", None)
-    if keep is not None:   # a prepared call holds on to its tensors
-        keep.append(t)
-    if not t.is_cuda:
+    if _recorders:
+        keep = getattr(_RECORDING, "keep", None)
+        if keep is not None:   # a prepared call holds on to its tensors
+            keep.append(t)
+    on = t.get_device()
+    if on < 0:
         raise ValueError("tensors passed to the library must be on the GPU")
+    if dev is not None and on != dev:
+        raise ValueError(f"tensor on cuda:{on}, the call runs on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous")
     key = (t.data_ptr(), t.dtype, t.shape, tag)
@@ -226,7 +240,10 @@ def _tensor(t: torch.Tensor | None, tag: int):
     return v
 
 
-def _stream(stream) -> c_void_p:
+def _stream(stream):
+    """The hipStream_t of a call: the given stream's, or the current one's."""
+    if stream is None and not _recorders:   # the raw handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if stream is None:
         stream = torch.cuda.current_stream()
     keep = getattr(_RECORDING, "keep", None)
@@ -246,13 +263,16 @@ def _stream(stream) -> c_void_p:
 
 
 def _enqueue(name: str, *args) -> None:
-    fn = getattr(load_library(), name)
-    calls = getattr(_RECORDING, "calls", None)
-    if calls is not None:
-        calls.append((fn, args, name))
-        _RECORDING.keep.extend(args)   # rules live as long as the recorded call
-        return
-    _check(fn(*args), name)
+    fn = getattr(_lib or load_library(), name)
+    if _recorders:
+        calls = getattr(_RECORDING, "calls", None)
+        if calls is not None:
+            calls.append((fn, args, name))
+            _RECORDING.keep.extend(args)   # rules live as long as the recorded call
+            return
+    code = fn(*args)
+    if code:
+        raise EpError(code, name)
 
 
 class Prepared:
@@ -272,10 +292,11 @@ class Prepared:
             c.op = _OPS[name]
             m = 0
             for a in args:
-                if isinstance(a, (c_int32, int)):   # ep_quantize_fp8's scale format
-                    c.i0 = a.value if isinstance(a, c_int32) else int(a)
+                if isinstance(a, c_int32):   # ep_quantize_fp8's scale format
+                    c.i0 = a.value
                     continue
-                c.p[m] = None if a is None else ctypes.cast(a, c_void_p).value
+                # handles may come as plain addresses
+                c.p[m] = a if a is None or isinstance(a, int) else ctypes.cast(a, c_void_p).value
                 m += 1
         self._n = c_int32(n)
         self._failed = c_int32(0)
@@ -296,11 +317,16 @@ def prepare(fn) -> Prepared:
     and must not be made inside ``fn``."""
     if getattr(_RECORDING, "calls", None) is not None:
         raise RuntimeError("prepare() does not nest")
+    global _recorders
     _RECORDING.calls, _RECORDING.keep = [], []
+    with _recorders_lock:
+        _recorders += 1
     try:
         fn()
         return Prepared(_RECORDING.calls, _RECORDING.keep)
     finally:
+        with _recorders_lock:
+            _recorders -= 1
         _RECORDING.calls = _RECORDING.keep = None
 
 
@@ -517,32 +543,23 @@ def _norm_rule(eps: float, quant: str | int):
     return p
 
 
-def _same_device(stream, *tensors) -> None:
-    """The tensors live on the device the call runs on (the stream's, or the
-    current one)."""
-    dev = stream.device.index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, the call runs on cuda:{dev}")
-
-
 def ep_route_scored(h: int, rule: RouteRule, logits: torch.Tensor, bias: torch.Tensor | None,
                     topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                     scores: torch.Tensor | None = None, stream=None) -> None:
-    _same_device(stream, logits, bias, topk_idx, topk_weights, scores)
-    _enqueue("ep_route_scored", c_void_p(h), rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS),
-             _tensor(bias, TAG_ROUTER_BIAS), _tensor(topk_idx, TAG_TOPK_IDX),
-             _tensor(topk_weights, TAG_TOPK_WEIGHTS), _tensor(scores, TAG_ROUTER_LOGITS),
+    d = _device(stream)
+    _enqueue("ep_route_scored", h, rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS, d),
+             _tensor(bias, TAG_ROUTER_BIAS, d), _tensor(topk_idx, TAG_TOPK_IDX, d),
+             _tensor(topk_weights, TAG_TOPK_WEIGHTS, d), _tensor(scores, TAG_ROUTER_LOGITS, d),
              _stream(stream))
 
 
 def ep_route_scored_bwd(h: int, rule: RouteRule, logits: torch.Tensor, topk_idx: torch.Tensor,
                         grad_topk_weights: torch.Tensor, grad_scores: torch.Tensor | None,
                         grad_logits: torch.Tensor, stream=None) -> None:
-    _same_device(stream, logits, topk_idx, grad_topk_weights, grad_scores, grad_logits)
-    _enqueue("ep_route_scored_bwd", c_void_p(h), rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS),
-             _tensor(topk_idx, TAG_TOPK_IDX), _tensor(grad_topk_weights, TAG_TOPK_WEIGHTS),
-             _tensor(grad_scores, TAG_ROUTER_LOGITS), _tensor(grad_logits, TAG_ROUTER_LOGITS),
+    d = _device(stream)
+    _enqueue("ep_route_scored_bwd", h, rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS, d),
+             _tensor(topk_idx, TAG_TOPK_IDX, d), _tensor(grad_topk_weights, TAG_TOPK_WEIGHTS, d),
+             _tensor(grad_scores, TAG_ROUTER_LOGITS, d), _tensor(grad_logits, TAG_ROUTER_LOGITS, d),
              _stream(stream))
 
 
@@ -554,11 +571,11 @@ def ep_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch
                    residual_out: torch.Tensor | None, y: torch.Tensor | None,
                    codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                    eps: float = 1e-6, quant: str | int = "none", stream=None) -> None:
-    _same_device(stream, x, residual, weight, residual_out, y, codes, scales)
-    _enqueue("ep_add_rmsnorm", _norm_rule(eps, quant), _tensor(x, TAG_TOKENS),
-             _tensor(residual, TAG_TOKENS), _tensor(weight, TAG_NORM_WEIGHT),
-             _tensor(residual_out, TAG_TOKENS), _tensor(y, TAG_TOKENS), _tensor(codes, TAG_TOKENS),
-             _tensor(scales, _scale_tag(codes)), _stream(stream))
+    d = _device(stream)
+    _enqueue("ep_add_rmsnorm", _norm_rule(eps, quant), _tensor(x, TAG_TOKENS, d),
+             _tensor(residual, TAG_TOKENS, d), _tensor(weight, TAG_NORM_WEIGHT, d),
+             _tensor(residual_out, TAG_TOKENS, d), _tensor(y, TAG_TOKENS, d), _tensor(codes, TAG_TOKENS, d),
+             _tensor(scales, _scale_tag(codes), d), _stream(stream))
 
 
 def ep_add_rmsnorm_bwd_workspace_bytes(rows: int, hidden: int) -> int:
@@ -572,32 +589,31 @@ def ep_add_rmsnorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch
                        grad_residual_out: torch.Tensor | None, grad: torch.Tensor,
                        grad_weight: torch.Tensor | None, workspace: torch.Tensor | None,
                        eps: float = 1e-6, stream=None) -> None:
-    _same_device(stream, hidden, weight, grad_y, grad_residual_out, grad, grad_weight, workspace)
-    _enqueue("ep_add_rmsnorm_bwd", _norm_rule(eps, QUANT_NONE), _tensor(hidden, TAG_TOKENS),
-             _tensor(weight, TAG_NORM_WEIGHT), _tensor(grad_y, TAG_TOKENS),
-             _tensor(grad_residual_out, TAG_TOKENS), _tensor(grad, TAG_TOKENS),
-             _tensor(grad_weight, TAG_NORM_WEIGHT), _tensor(workspace, TAG_WORKSPACE),
+    d = _device(stream)
+    _enqueue("ep_add_rmsnorm_bwd", _norm_rule(eps, QUANT_NONE), _tensor(hidden, TAG_TOKENS, d),
+             _tensor(weight, TAG_NORM_WEIGHT, d), _tensor(grad_y, TAG_TOKENS, d),
+             _tensor(grad_residual_out, TAG_TOKENS, d), _tensor(grad, TAG_TOKENS, d),
+             _tensor(grad_weight, TAG_NORM_WEIGHT, d), _tensor(workspace, TAG_WORKSPACE, d),
              _stream(stream))
 
 
 def ep_quantize_int8(tokens: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                      stream=None) -> None:
-    _same_device(stream, tokens, codes, scales)
-    _enqueue("ep_quantize_int8", _tensor(tokens, TAG_TOKENS), _tensor(codes, TAG_TOKENS),
-             _tensor(scales, TAG_ROW_SCALES), _stream(stream))
+    d = _device(stream)
+    _enqueue("ep_quantize_int8", _tensor(tokens, TAG_TOKENS, d), _tensor(codes, TAG_TOKENS, d),
+             _tensor(scales, TAG_ROW_SCALES, d), _stream(stream))
 
 
 def ep_dispatch_quantized(h: int, tokens: torch.Tensor, token_scales: torch.Tensor,
                           topk_weights: torch.Tensor | None, recv_tokens: torch.Tensor,
                           recv_scales: torch.Tensor, recv_topk_idx: torch.Tensor | None = None,
                           recv_topk_weights: torch.Tensor | None = None, stream=None) -> None:
-    _same_device(stream, tokens, token_scales, topk_weights, recv_tokens, recv_scales,
-                 recv_topk_idx, recv_topk_weights)
+    d = _device(stream)
     tag = _scale_tag(tokens)
-    _enqueue("ep_dispatch_quantized", c_void_p(h), _tensor(tokens, TAG_TOKENS),
-             _tensor(token_scales, tag), _tensor(topk_weights, TAG_TOPK_WEIGHTS),
-             _tensor(recv_tokens, TAG_TOKENS), _tensor(recv_scales, tag),
-             _tensor(recv_topk_idx, TAG_TOPK_IDX), _tensor(recv_topk_weights, TAG_TOPK_WEIGHTS),
+    _enqueue("ep_dispatch_quantized", h, _tensor(tokens, TAG_TOKENS, d),
+             _tensor(token_scales, tag, d), _tensor(topk_weights, TAG_TOPK_WEIGHTS, d),
+             _tensor(recv_tokens, TAG_TOKENS, d), _tensor(recv_scales, tag, d),
+             _tensor(recv_topk_idx, TAG_TOPK_IDX, d), _tensor(recv_topk_weights, TAG_TOPK_WEIGHTS, d),
              _stream(stream))
 
 
@@ -605,13 +621,12 @@ def ep_expert_gemm_int8(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Te
                         expert_weights: torch.Tensor, expert_scales: torch.Tensor,
                         slot_weights: torch.Tensor | None, slot_scales: torch.Tensor | None,
                         out: torch.Tensor, stream=None, swiglu: bool = False) -> None:
-    _same_device(stream, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
-                 slot_scales, out)
+    d = _device(stream)
     name = "ep_expert_gemm_int8_swiglu" if swiglu else "ep_expert_gemm_int8"
-    _enqueue(name, c_void_p(h), _tensor(recv_tokens, TAG_TOKENS),
-             _tensor(recv_scales, TAG_ROW_SCALES), _tensor(expert_weights, TAG_EXPERT_WEIGHTS),
-             _tensor(expert_scales, TAG_ROW_SCALES), _tensor(slot_weights, TAG_EXPERT_WEIGHTS),
-             _tensor(slot_scales, TAG_ROW_SCALES), _tensor(out, TAG_TOKENS), _stream(stream))
+    _enqueue(name, h, _tensor(recv_tokens, TAG_TOKENS, d),
+             _tensor(recv_scales, TAG_ROW_SCALES, d), _tensor(expert_weights, TAG_EXPERT_WEIGHTS, d),
+             _tensor(expert_scales, TAG_ROW_SCALES, d), _tensor(slot_weights, TAG_EXPERT_WEIGHTS, d),
+             _tensor(slot_scales, TAG_ROW_SCALES, d), _tensor(out, TAG_TOKENS, d), _stream(stream))
 
 
 def ep_expert_gemm_int8_swiglu(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,

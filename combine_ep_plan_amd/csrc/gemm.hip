@@ -99,7 +99,7 @@ __device__ __forceinline__ void group_of(const TileArgs &a, int32_t q, int32_t &
   }
 }
 
-// PART: row tiles come in two kinds, full ones (more than TM/2 rows), whose
+// PART: row tiles come in two kinds, full ones (more than short_rows rows), whose
 // time is MFMA work, and short ones (a group's tail or a small group), whose
 // time is streaming their weight slice.  The table then holds the full tiles
 // in group order from the front and the short ones in group order from the
@@ -109,7 +109,8 @@ __device__ __forceinline__ void group_of(const TileArgs &a, int32_t q, int32_t &
 // x, x + 8, x + 16, ... of it.
 // ntiles[0] = all tiles, ntiles[1] = full tiles.
 template <int TM, bool PART>
-__global__ __launch_bounds__(1024) void k_gemm_tiles(TileArgs a, int32_t max_tiles) {
+__global__ __launch_bounds__(1024) void k_gemm_tiles(TileArgs a, int32_t max_tiles,
+                                                     int32_t short_rows) {
   __shared__ int32_t s_wave[2][16];
   __shared__ int32_t s_base[2];
   const Geometry &g = a.g;
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(1024) void k_gemm_tiles(TileArgs a, int32_t max_til
     if (q < ngroups) group_of(a, q, row0, rows, widx);
     const int32_t nt = rows > 0 ? (rows + TM - 1) / TM : 0;
     const int32_t tail = rows - (nt - 1) * TM;                 // rows of the last tile
-    const int32_t nshort = PART && nt > 0 && 2 * tail <= TM ? 1 : 0;   // the last may be short
+    const int32_t nshort = PART && nt > 0 && tail <= short_rows ? 1 : 0;   // the last may be short
     const int32_t nfull = nt - nshort;
     // inclusive scans of nfull and nshort over the workgroup: lanes, then waves
     int32_t xf = nfull, xs = nshort;
@@ -1207,11 +1208,13 @@ static bool gemm_fp8_uses_wide_tiles(const Geometry &g, int32_t K, int32_t N) {
          (int64_t)kBM2 * K <= INT32_MAX;
 }
 
-hipError_t launch_gemm_tiles(const Geometry &g, const Workspace &ws, bool slots, bool wide,
-                             int32_t max_tiles, hipStream_t s) {
+hipError_t launch_gemm_tiles(const Geometry &g, const Workspace &ws, bool slots,
+                             int32_t short_rows, int32_t max_tiles, hipStream_t s) {
   const TileArgs ta{g, ws, slots ? 1 : 0};
-  if (wide) hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
-  else hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
+  if (short_rows > 0)
+    hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max_tiles, short_rows);
+  else
+    hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles, 0);
   return hipGetLastError();
 }
 
@@ -1223,7 +1226,7 @@ hipError_t launch_grouped_gemm(const Geometry &g, const Workspace &ws, const uin
   TileArgs ta{g, ws, wslot != nullptr ? 1 : 0};
   if (gemm_uses_wide_tiles(g, K, N)) {
     const int32_t max2 = wide_max_tiles(g);
-    hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max2);
+    hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max2, kBM2 / 2);
     const int32_t ncol = (N + kBN2 - 1) / kBN2;
     GEMM_LAUNCH(k_grouped_gemm_256, dim3(gemm_grid(max2, ncol)), dim3(kGemmThreads), 0, s,
                        reinterpret_cast<const u32x4 *>(x), reinterpret_cast<const u32x4 *>(w),
@@ -1231,7 +1234,7 @@ hipError_t launch_grouped_gemm(const Geometry &g, const Workspace &ws, const uin
                        K, N, g.E, ncol, y);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
+  hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles, 0);
   const int32_t ncol = (N + kBN - 1) / kBN;
   GEMM_LAUNCH(k_grouped_gemm, dim3(gemm_grid(max_tiles, ncol)), dim3(kGemmThreads), 0, s,
                      reinterpret_cast<const u32x4 *>(x), reinterpret_cast<const u32x4 *>(w),
@@ -1249,7 +1252,7 @@ hipError_t launch_grouped_gemm_fp8(const Geometry &g, const Workspace &ws, const
   TileArgs ta{g, ws, wslot != nullptr ? 1 : 0};
   if (gemm_fp8_uses_wide_tiles(g, K, N)) {
     const int32_t max2 = wide_max_tiles(g);
-    hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max2);
+    hipLaunchKernelGGL((k_gemm_tiles<kBM2, true>), dim3(1), dim3(1024), 0, s, ta, max2, kBM2 / 2);
     const int32_t ncol = (N + kBN2 - 1) / kBN2;
     GEMM_LAUNCH(k_grouped_gemm_fp8_256, dim3(gemm_grid(max2, ncol)), dim3(kGemmThreads), 0, s,
                 reinterpret_cast<const u32x4 *>(x), sx, reinterpret_cast<const u32x4 *>(w), sw,
@@ -1257,7 +1260,7 @@ hipError_t launch_grouped_gemm_fp8(const Geometry &g, const Workspace &ws, const
                 max2, K, N, g.E, ncol, y, ws.status);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles);
+  hipLaunchKernelGGL((k_gemm_tiles<kTileM, false>), dim3(1), dim3(1024), 0, s, ta, max_tiles, 0);
   const int32_t ncol = (N + kBN - 1) / kBN;
 #define F8_ARGS                                                                                \
   dim3(gemm_grid(max_tiles, ncol)), dim3(kGemmThreads), 0, s, reinterpret_cast<const u32x4 *>(x), sx, \

@@ -78,6 +78,12 @@ __device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base) : "memory");
 }
+// ... of bytes nobody reads again soon: they do not displace what the caches hold.
+__device__ __forceinline__ void lds_load16_stream(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_base,
+                                                  uint32_t voff, uint32_t soff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base) : "memory");
+}
 __device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_base,
                                           uint32_t voff, uint32_t soff) {
   asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
@@ -97,9 +103,10 @@ inline int32_t wide_max_tiles(const Geometry &g) {
   return (int32_t)((g.n + kBM2 - 1) / kBM2 + groups);
 }
 
-// Tile table of the current plan into ws.gemm_tiles / ws.gemm_ntiles, for
-// 256-row tiles (wide, full and short tiles apart) or 128-row ones.
-hipError_t launch_gemm_tiles(const Geometry &g, const Workspace &ws, bool slots, bool wide,
-                             int32_t max_tiles, hipStream_t s);
+// Tile table of the current plan into ws.gemm_tiles / ws.gemm_ntiles: 256-row
+// tiles, those of at most short_rows rows apart from the others, or (0)
+// 128-row ones.
+hipError_t launch_gemm_tiles(const Geometry &g, const Workspace &ws, bool slots,
+                             int32_t short_rows, int32_t max_tiles, hipStream_t s);
 
 }  // namespace epk

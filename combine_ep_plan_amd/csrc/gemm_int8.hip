@@ -15,6 +15,9 @@
 // silu(gate) * up is formed from the fp32 values and rounded once (the bf16
 // and FP8 kernels round gate and up to bf16 first).
 //
+// Three kernels, chosen by rows an expert: k_grouped_gemm_i8_stream,
+// k_grouped_gemm_i8 and k_grouped_gemm_i8_256.
+//
 // k_grouped_gemm_i8: 128 x 128 tiles, 256 threads, two workgroups a CU; four
 // waves in 2 x 2, each 2 x 2 accumulators of 32 x 32; slabs of 128 bytes of
 // K, double-buffered in LDS with the chunk swizzle of gemm_common.h.
@@ -168,9 +171,491 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_grouped_gemm_i8(
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows an expert (decode): the time is streaming the weights, so nothing
+// may stand in the way of loads.  A wave by itself streams 64 weight rows (two
+// 32-column blocks; gates and ups for SwiGLU) and the tile's rows through a
+// ring of slabs in its own part of LDS: no barriers, only waits for its own
+// loads, D slabs in flight.  The loads go straight to LDS, eight lanes to a
+// 128-byte row: loaded into registers in the order the MFMAs want (32 rows, 16
+// bytes a lane) the same bytes take four times the address slots and the
+// kernel stops at 6.1 TB/s of weights.  The weights are loaded non-temporally:
+// plain loads of them stop at 6.2 TB/s on this card, non-temporal ones at 7.1.
+// Decode (1024 rows, 256 experts, K = 7168, N = 2048): 582 us, 6.5 TB/s.
+// SPLIT: the four waves of a workgroup share 64 columns and take a quarter of K
+// each, so that a batch of few experts still fills the GPU; their integer
+// partial sums are joined through LDS, exactly.
+
+constexpr int kStreamCols = 64;
+constexpr int32_t kShortRows = 64;  // row tiles of at most this only stream their weights
+
+struct StreamTile {
+  __amdgpu_buffer_rsrc_t rX, rW;
+  const float *SX, *SW;  // scales of the tile's rows and columns
+  uint16_t *Y;           // the tile's first row and column of outputs
+  int32_t rows, wrows, K, NO, cols;  // cols: outputs of the tile
+};
+
+// A buffer resource of wave-uniform bounds, kept in scalar registers (the
+// loads to LDS take no other; through a branch the compiler may lose sight of
+// its uniformity).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, int32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
+                                           __builtin_amdgcn_readfirstlane(bytes), kBufDword3);
+}
+
+// The stream's view of columns [n0, n0 + 64) of a row tile.
+template <bool GLU>
+__device__ __forceinline__ StreamTile stream_tile(const u32x4 *X, const float *SX, const u32x4 *Wm,
+                                                  const float *SWm, uint16_t *Y, int32_t row0,
+                                                  int32_t rows, int32_t n0, int32_t N, int32_t K) {
+  const int32_t KV = K / 16, NO = GLU ? N / 2 : N;
+  StreamTile t;
+  t.rows = rows;
+  t.wrows = N - n0 < kStreamCols ? N - n0 : kStreamCols;
+  t.K = K;
+  t.NO = NO;
+  t.cols = GLU ? t.wrows / 2 : t.wrows;
+  // every offset is in range by construction (rows past the end read the last
+  // row); 128 rows of K <= 131071 bytes span less than 2^31
+  t.rX = uniform_rsrc(X + (int64_t)row0 * KV, rows * K);
+  t.rW = uniform_rsrc(Wm + (int64_t)n0 * KV, t.wrows * K);
+  t.SX = SX + row0;
+  t.SW = SWm + n0;
+  t.Y = Y + (int64_t)row0 * NO + (GLU ? n0 / 2 : n0);
+  return t;
+}
+
+// 16-byte slots of a wave's ring: D slabs of 64 weight rows and 8 NX token rows.
+constexpr int stream_slots(int NX, int D) { return D * (kStreamCols + 8 * NX) * kChunks; }
+
+// Rows [m0, m0 + 8 NX) of the tile, NX in 1, 2, 4, 8; ring: the wave's
+// stream_slots(NX, D).
+template <bool GLU, int NX, int D, bool SPLIT>
+__device__ __forceinline__ void stream_rows(const StreamTile &t, int32_t m0, int wv, int lane,
+                                            u32x4 *ring, int32_t *part) {
+  constexpr int LB = NX == 8 ? 2 : 1;       // 32-row blocks
+  constexpr int SLAB = (kStreamCols + 8 * NX) * kChunks;
+  constexpr int NL = kStreamCols / 8 + NX;  // loads of a slab
+  static_assert((D - 1) * NL <= 63, "the wait counts them in six bits");
+  const int h = lane >> 5, l = lane & 31;
+  const int32_t K = t.K;
+  const int KT = (K + kI8Slab - 1) / kI8Slab;
+  const int lo = SPLIT ? KT * wv / 4 : 0, hi = SPLIT ? KT * (wv + 1) / 4 : KT;  // this wave's slabs
+  const int last = K > kI8Slab ? K - kI8Slab : 0;
+  const bool half = K % kI8Slab != 0;  // the last slab: only its upper half is new
+  // load i fills the slots i*64 + lane: LDS row r = i*8 + lane/8, holding chunk
+  // (lane % 8) ^ ((r / 2) % 8)
+  uint32_t ow[kStreamCols / 8], ox[NX];
+#pragma unroll
+  for (int i = 0; i < kStreamCols / 8; ++i) {
+    const int r = i * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7), n = weight_row<GLU>(r);
+    ow[i] = (uint32_t)((n < t.wrows ? n : t.wrows - 1) * K + (K == 64 ? c & 3 : c) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int r = i * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7), m = m0 + r;
+    ox[i] = (uint32_t)((m < t.rows ? m : t.rows - 1) * K + (K == 64 ? c & 3 : c) * 16);
+  }
+#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
+  const auto issue = [&](int kt, int buf) {
+    const int so = kt + 1 < KT ? kt * kI8Slab : last;
+#pragma unroll
+    for (int i = 0; i < kStreamCols / 8; ++i)
+      lds_load16_stream(t.rW, LDS_ADDR(&ring[buf * SLAB + i * 64]), ow[i], so);
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      lds_load16(t.rX, LDS_ADDR(&ring[buf * SLAB + (kStreamCols + 8 * i) * kChunks]), ox[i], so);
+  };
+#undef LDS_ADDR
+  i32x16 acc[LB][2];
+#pragma unroll
+  for (int i = 0; i < LB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (lo + d < hi) issue(lo + d, d);
+  int buf = 0;
+  for (int kt = lo; kt < hi; ++kt) {
+    // slab kt landed (the D - 1 after it may still be on their way)
+    if (kt + D <= hi) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * NL) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    i32x4 fa[LB][4], fb[2][4];
+    const u32x4 *sw_ = ring + buf * SLAB, *sx_ = sw_ + kStreamCols * kChunks;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[j][c] = __builtin_bit_cast(i32x4, sw_[swz(j * 32 + l, 2 * c + h)]);
+      // token rows that were not loaded (8 NX < 32) are rows nobody stores: any row serves
+#pragma unroll
+      for (int i = 0; i < LB; ++i)
+        fa[i][c] = __builtin_bit_cast(i32x4, sx_[swz((i * 32 + l) & (8 * NX - 1), 2 * c + h)]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the buffer is free
+    if (kt + D < hi) issue(kt + D, buf);
+    const bool tail = half && kt + 1 == KT;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c < 2 && tail) continue;
+#pragma unroll
+      for (int i = 0; i < LB; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i][c], fb[j][c], acc[i][j], 0, 0, 0);
+    }
+    buf = buf + 1 == D ? 0 : buf + 1;
+  }
+
+  float sw[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int n = GLU ? 2 * l + j : j * 32 + l;
+    sw[j] = t.SW[n < t.wrows ? n : t.wrows - 1];
+  }
+  const auto store = [&](int32_t rr, int32_t v0, int32_t v1) {
+    if (rr >= t.rows) return;
+    const float sx = t.SX[rr];
+    uint16_t *y = t.Y + (int64_t)rr * t.NO;
+    const float f0 = (float)v0 * (sx * sw[0]), f1 = (float)v1 * (sx * sw[1]);
+    if constexpr (GLU) {
+      if (l < t.cols) y[l] = bf16_bits(silu_mul(f0, f1));
+    } else {
+      if (l < t.cols) y[l] = bf16_bits(f0);
+      if (32 + l < t.cols) y[32 + l] = bf16_bits(f1);
+    }
+  };
+  // accumulator r of a lane: row (r / 4) * 8 + (lane / 32) * 4 + r % 4
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    if constexpr (!SPLIT) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        store(m0 + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3), acc[i][0][r], acc[i][1][r]);
+    } else {
+#define PART(w_, j_, r_) part[(((w_) * 2 + (j_)) * 16 + (r_)) * 64 + lane]
+      __syncthreads();   // the rings, and the parts of the rows before, are read
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) PART(wv, j, r) = acc[i][j][r];
+      __syncthreads();
+      // wave wv finishes accumulator elements 4 wv .. 4 wv + 3
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        int32_t v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          v[j] = PART(0, j, wv * 4 + q) + PART(1, j, wv * 4 + q) + PART(2, j, wv * 4 + q) +
+                 PART(3, j, wv * 4 + q);
+        store(m0 + i * 32 + wv * 8 + h * 4 + q, v[0], v[1]);
+      }
+#undef PART
+    }
+  }
+  if constexpr (SPLIT) __syncthreads();   // before the next rows' loads land in the rings
+}
+
+// All rows of a tile, in passes of 64 over its weights (one, unless a busier
+// expert stands among few rows); the smallest ring row count that holds them.
+template <bool GLU, int D1, int D4, int D8, bool SPLIT>
+__device__ __forceinline__ void stream_all(const StreamTile &t, int wv, int lane, u32x4 *ring,
+                                           int32_t *part) {
+  int32_t m0 = 0;
+  for (; m0 + 32 < t.rows; m0 += 64) stream_rows<GLU, 8, D8, SPLIT>(t, m0, wv, lane, ring, part);
+  const int32_t left = t.rows - m0;
+  if (left > 8) stream_rows<GLU, 4, D4, SPLIT>(t, m0, wv, lane, ring, part);
+  else if (left > 0) stream_rows<GLU, 1, D1, SPLIT>(t, m0, wv, lane, ring, part);
+}
+
+constexpr int kStreamD1 = 4, kStreamD4 = 3, kStreamD8 = 2;
+constexpr int kStreamSlots = stream_slots(1, kStreamD1);
+static_assert(stream_slots(4, kStreamD4) <= kStreamSlots && stream_slots(8, kStreamD8) <= kStreamSlots,
+              "one wave's ring");
+
+template <bool GLU, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 256 : 64) void k_grouped_gemm_i8_stream(
+    const u32x4 *__restrict__ X, const float *__restrict__ SX, const u32x4 *__restrict__ W,
+    const float *__restrict__ SW, const u32x4 *__restrict__ Wslot,
+    const float *__restrict__ SWslot, const int32_t *__restrict__ tiles,
+    const int32_t *__restrict__ ntiles, int32_t max_tiles, int32_t K, int32_t N, int32_t E,
+    int32_t n_col_tiles, uint16_t *__restrict__ Y) {
+  __shared__ u32x4 ring[(SPLIT ? 4 : 1) * kStreamSlots];   // 36 KB a wave
+  static_assert(4 * 2 * 16 * 64 * 4 <= 4 * kStreamSlots * 16, "the partial sums fit the rings");
+  int32_t tile, ctile;
+  if (!balanced_tile(ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
+  const int32_t row0 = tiles[tile * 4 + 0], rows = tiles[tile * 4 + 1], widx = tiles[tile * 4 + 2];
+  const bool own = widx < E;
+  const int64_t wsel = own ? widx : widx - E;
+  const StreamTile t = stream_tile<GLU>(X, SX, (own ? W : Wslot) + wsel * N * (K / 16),
+                                        (own ? SW : SWslot) + wsel * N, Y, row0, rows,
+                                        ctile * kStreamCols, N, K);
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  stream_all<GLU, kStreamD1, kStreamD4, kStreamD8, SPLIT>(
+      t, wv, lane, ring + wv * kStreamSlots, reinterpret_cast<int32_t *>(ring));
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles (large groups): waves, LDS geometry and pipeline of the
+// power-of-two FP8 kernel (gemm.hip, k_grouped_gemm_fp8_256) -- 4 x 4
+// accumulators of 32 x 32 a wave, 128-byte slabs straight from global memory
+// into two LDS buffers, the slab after next issued as soon as its buffer is
+// free -- with two 32-deep v_mfma_i32_32x32x32_i8 in place of each 64-deep FP8
+// step and no scales in the loop.
+
+// A lane's fragments of half a slab: chunks 2s + lane / 32 of its row, s = 0, 1
+// (within the half).
+struct Frag2 {
+  i32x4 s0, s1;
+};
+
+template <int I, int NB>
+__device__ __forceinline__ void mfma_i8_rows(i32x16 (&acc)[kFM2][kFN2], const Frag2 (&fa)[kFM2],
+                                             const Frag2 (&fb)[kFN2]) {
+  if constexpr (I < NB) {
+#pragma unroll
+    for (int j = 0; j < kFN2; ++j)
+      acc[I][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[I].s0, fb[j].s0, acc[I][j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kFN2; ++j)
+      acc[I][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[I].s1, fb[j].s1, acc[I][j], 0, 0, 0);
+    mfma_i8_rows<I + 1, NB>(acc, fa, fb);
+  }
+}
+
+template <bool GLU>
+__global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
+    const u32x4 *__restrict__ X, const float *__restrict__ SX, const u32x4 *__restrict__ W,
+    const float *__restrict__ SW, const u32x4 *__restrict__ Wslot,
+    const float *__restrict__ SWslot, const int32_t *__restrict__ tiles,
+    const int32_t *__restrict__ ntiles, int32_t max_tiles, int32_t K, int32_t N, int32_t E,
+    int32_t n_col_tiles, uint16_t *__restrict__ Y) {
+  // two slabs of X and W (128 KB), later the bf16 output tile; the row scales
+  __shared__ u32x4 lds[2 * kSlabA2 + 2 * kSlabB2];
+  __shared__ float ssx[kBM2];
+  static_assert(kBM2 * kBN2 * 2 <= (int)sizeof(lds), "output tile fits the slab buffers");
+  static_assert(kBM2 == kGemmThreads, "one row scale per thread");
+  u32x4 *const sa = lds, *const sb = lds + 2 * kSlabA2;
+  int32_t tile, ctile;
+  if (!balanced_tile(ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
+  const int32_t n0 = ctile * kBN2;
+  const int32_t row0 = tiles[tile * 4 + 0], rows = tiles[tile * 4 + 1], widx = tiles[tile * 4 + 2];
+  const int32_t KV = K / 16;
+  const bool own = widx < E;
+  const int64_t wsel = own ? widx : widx - E;
+  const int32_t wrows = N - n0 < kBN2 ? N - n0 : kBN2;
+  const float *SWt = (own ? SW : SWslot) + wsel * N + n0;
+  // every offset is in range by construction: rows past the end read the last
+  // row, and 256 rows of K <= 131071 bytes span less than 2^31
+  const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(X + (int64_t)row0 * KV), (short)0, rows * K, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)((own ? W : Wslot) + (wsel * N + n0) * KV), (short)0, wrows * K, kBufDword3);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
+  if (rows <= kShortRows) {   // wave wv streams 64 of the 256 columns
+    if (n0 + wv * kStreamCols >= N) return;
+    const StreamTile t = stream_tile<GLU>(X, SX, (own ? W : Wslot) + wsel * N * KV,
+                                          (own ? SW : SWslot) + wsel * N, Y, row0, rows,
+                                          n0 + wv * kStreamCols, N, K);
+    constexpr int kRing = (2 * kSlabA2 + 2 * kSlabB2) / 4;   // a wave's quarter of LDS
+    static_assert(stream_slots(1, 3) <= kRing && stream_slots(4, 2) <= kRing && stream_slots(8, 2) <= kRing, "");
+    stream_all<GLU, 3, 2, 2, false>(t, wv, lane, lds + wv * kRing, nullptr);
+    return;
+  }
+  const int wm = wv >> 1, wn = wv & 1;
+  ssx[tid] = SX[row0 + (tid < rows ? tid : rows - 1)];
+  // load i of wave wv fills the 64 slots i*256 + wv*64 + lane, slot q holding
+  // chunk (q % 8) ^ ((r / 2) % 8) of LDS row r = q / 8
+  uint32_t oa[kLoads2], ob[kLoadsB2];
+#pragma unroll
+  for (int i = 0; i < kLoads2; ++i) {
+    const int q = i * kGemmThreads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    oa[i] = (uint32_t)(((r < rows ? r : rows - 1) * KV + (K == 64 ? c & 3 : c)) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoadsB2; ++i) {
+    const int q = i * kGemmThreads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    const int n = weight_row<GLU>(r);
+    ob[i] = (uint32_t)(((n < wrows ? n : wrows - 1) * KV + (K == 64 ? c & 3 : c)) * 16);
+  }
+  const int KT = (K + kI8Slab - 1) / kI8Slab;
+  const bool half = K % kI8Slab != 0;  // the last slab: only its upper half is new (see k_grouped_gemm_i8)
+  const int last = K > kI8Slab ? K - kI8Slab : 0;
+#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
+#define I8W_ISSUE(kt, buf)                                                                     \
+  {                                                                                            \
+    const int so_ = (kt) + 1 < KT ? (kt) * kI8Slab : last;                                     \
+    _Pragma("unroll") for (int i = 0; i < kLoads2; ++i) lds_load16(                            \
+        rX, LDS_ADDR(&sa[(buf) * kSlabA2 + i * kGemmThreads + wv * 64]), oa[i], so_);          \
+    _Pragma("unroll") for (int i = 0; i < kLoadsB2; ++i) lds_load16(                           \
+        rW, LDS_ADDR(&sb[(buf) * kSlabB2 + i * kGemmThreads + wv * 64]), ob[i], so_);          \
+  }
+  static_assert(kLoads2 + kLoadsB2 == 16, "the waits below count 16 loads per slab");
+// half h (0 or 1) of a slab: chunks h*4 + lane/32 and h*4 + 2 + lane/32 of the lane's row
+#define READ8(FA, FB, buf, h, NBK)                                                             \
+  {                                                                                            \
+    const int c_ = (h) * 4 + (lane >> 5);                                                      \
+    _Pragma("unroll") for (int i = 0; i < (NBK); ++i) {                                        \
+      const int r_ = wm * kWTM2 + i * 32 + (lane & 31);                                        \
+      FA[i].s0 = __builtin_bit_cast(i32x4, sa[(buf) * kSlabA2 + swz(r_, c_)]);                 \
+      FA[i].s1 = __builtin_bit_cast(i32x4, sa[(buf) * kSlabA2 + swz(r_, c_ + 2)]);             \
+    }                                                                                          \
+    _Pragma("unroll") for (int j = 0; j < kFN2; ++j) {                                         \
+      const int r_ = wn * kWTN2 + j * 32 + (lane & 31);                                        \
+      FB[j].s0 = __builtin_bit_cast(i32x4, sb[(buf) * kSlabB2 + swz(r_, c_)]);                 \
+      FB[j].s1 = __builtin_bit_cast(i32x4, sb[(buf) * kSlabB2 + swz(r_, c_ + 2)]);             \
+    }                                                                                          \
+  }
+
+  i32x16 acc[kFM2][kFN2];
+#pragma unroll
+  for (int i = 0; i < kFM2; ++i)
+#pragma unroll
+    for (int j = 0; j < kFN2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+  Frag2 fa0[kFM2], fb0[kFN2], fa1[kFM2], fb1[kFN2];
+  // Each wave waits for its own loads, then the barrier publishes every
+  // wave's share; the asm reads one element of each accumulator so that the
+  // MFMAs before it stay before it.
+#define I8W_SYNC(VM)                                                                           \
+  asm volatile("s_waitcnt vmcnt(" #VM ") lgkmcnt(0)\n\ts_barrier"                             \
+               :: "a"(acc[0][0][0]), "a"(acc[0][1][0]), "a"(acc[0][2][0]), "a"(acc[0][3][0]),  \
+                  "a"(acc[1][0][0]), "a"(acc[1][1][0]), "a"(acc[1][2][0]), "a"(acc[1][3][0]),  \
+                  "a"(acc[2][0][0]), "a"(acc[2][1][0]), "a"(acc[2][2][0]), "a"(acc[2][3][0]),  \
+                  "a"(acc[3][0][0]), "a"(acc[3][1][0]), "a"(acc[3][2][0]), "a"(acc[3][3][0])   \
+               : "memory")
+  static_assert(kFM2 == 4 && kFN2 == 4, "the barrier names each of the 16 accumulators");
+  I8W_ISSUE(0, 0);
+  if (KT > 1) {
+    I8W_ISSUE(1, 1);
+    I8W_SYNC(16);   // slab 0 landed
+  } else {
+    I8W_SYNC(0);
+  }
+#define SGB8(m, n) __builtin_amdgcn_sched_group_barrier(m, n, 0)
+// one LDS read after every other MFMA (16 reads, 32 MFMAs)
+#define I8W_INTERLEAVE(NBK)                                                                    \
+  if constexpr ((NBK) == kFM2) {                                                               \
+    _Pragma("unroll") for (int q_ = 0; q_ < 16; ++q_) { SGB8(0x008, 2); SGB8(0x100, 1); }      \
+  }
+#define I8W_SLAB(NBK, ISSUE)                                                                   \
+  {                                                                                            \
+    const int buf = kt & 1;                                                                    \
+    READ8(fa1, fb1, buf, 1, NBK);                                                              \
+    mfma_i8_rows<0, NBK>(acc, fa0, fb0);                                                       \
+    I8W_INTERLEAVE(NBK);                                                                       \
+    I8W_SYNC(0);                                                                               \
+    __builtin_amdgcn_sched_barrier(0);                                                         \
+    if (ISSUE) I8W_ISSUE(kt + 2, buf);                                                         \
+    READ8(fa0, fb0, buf ^ 1, 0, NBK);                                                          \
+    mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                       \
+    I8W_INTERLEAVE(NBK);                                                                       \
+  }
+#define I8W_LOOP(NBK)                                                                          \
+  {                                                                                            \
+    READ8(fa0, fb0, 0, 0, NBK);                                                                \
+    int kt = 0;                                                                                \
+    for (; kt + 2 < KT; ++kt) I8W_SLAB(NBK, true)                                              \
+    if (kt + 1 < KT) {                                                                         \
+      I8W_SLAB(NBK, false)                                                                     \
+      ++kt;                                                                                    \
+    }                                                                                          \
+    READ8(fa1, fb1, kt & 1, 1, NBK);                                                           \
+    if (!half) mfma_i8_rows<0, NBK>(acc, fa0, fb0);                                            \
+    mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                       \
+  }
+  const int live = (rows - wm * kWTM2 + 31) / 32;  // wave-uniform
+  if (live >= kFM2) I8W_LOOP(kFM2)
+  else if (live == 3) I8W_LOOP(3)
+  else if (live == 2) I8W_LOOP(2)
+  else if (live == 1) I8W_LOOP(1)
+  else I8W_LOOP(0)
+#undef I8W_LOOP
+#undef I8W_SLAB
+#undef I8W_INTERLEAVE
+#undef SGB8
+#undef I8W_SYNC
+#undef READ8
+#undef I8W_ISSUE
+#undef LDS_ADDR
+
+  float sw[kFN2];
+#pragma unroll
+  for (int j = 0; j < kFN2; ++j) {
+    const int n = weight_row<GLU>(wn * kWTN2 + j * 32 + (lane & 31));
+    sw[j] = SWt[n < wrows ? n : wrows - 1];
+  }
+  const int32_t NO = GLU ? N / 2 : N;
+  // Through LDS as bf16 rows (TN columns, the 16-byte chunk of column c of row
+  // r at (c / 8) ^ (((r / 4) % 4) * 4), so the half-waves' rows r and r + 4
+  // land on different banks), then 16-byte row stores; 2-byte stores where a
+  // row of Y is no whole number of vectors.
+  constexpr int TN = GLU ? kBN2 / 2 : kBN2;
+  const bool vec = (NO & 7) == 0;
+  const int32_t c0 = GLU ? n0 / 2 : n0;
+  uint16_t *so = reinterpret_cast<uint16_t *>(lds);
+  __syncthreads();   // every wave is done with the slab buffers
+#define OSW(r_, cv_) ((r_) * TN + (((cv_) ^ ((((r_) >> 2) & 3) << 2)) << 3))
+#pragma unroll
+  for (int i = 0; i < kFM2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int rr = wm * kWTM2 + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
+      const float sx = ssx[rr];
+      constexpr int kOut = GLU ? kFN2 / 2 : kFN2;
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        float v;
+        if constexpr (GLU)
+          v = silu_mul((float)acc[i][2 * j][r] * (sx * sw[2 * j]),
+                       (float)acc[i][2 * j + 1][r] * (sx * sw[2 * j + 1]));
+        else
+          v = (float)acc[i][j][r] * (sx * sw[j]);
+        const int c = wn * (kOut * 32) + j * 32 + (lane & 31);
+        if (vec) so[OSW(rr, c >> 3) + (c & 7)] = bf16_bits(v);
+        else if (rr < rows && c0 + c < NO) Y[(int64_t)(row0 + rr) * NO + c0 + c] = bf16_bits(v);
+      }
+    }
+  if (!vec) return;
+  __syncthreads();
+  constexpr int kVecs = kBM2 * TN / 8;
+#pragma unroll 4
+  for (int q = 0; q < kVecs / kGemmThreads; ++q) {
+    const int idx = tid + q * kGemmThreads;
+    const int rr = idx / (TN / 8), cv = idx % (TN / 8), col = c0 + cv * 8;
+    if (rr < rows && col < NO)
+      *reinterpret_cast<u32x4 *>(Y + (int64_t)(row0 + rr) * NO + col) =
+          *reinterpret_cast<const u32x4 *>(so + OSW(rr, cv));
+  }
+#undef OSW
+}
+
+// Which kernel: 256 x 256 tiles with at least 128 rows an expert on average
+// (and N of a column tile); the streaming kernel with at most 32, its waves
+// splitting K while the groups that can have rows, times their column tiles,
+// leave wave slots empty (four a compute unit); 128 x 128 tiles between.
+enum class I8Kernel { kStream, kSplit, kTiles, kWide };
+constexpr int64_t kStreamWaves = 1024;
+static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
+  if (g.n >= (int64_t)(kBM2 / 2) * g.E && N >= kBN2) return I8Kernel::kWide;
+  if (g.n > (int64_t)32 * g.E) return I8Kernel::kTiles;
+  const int64_t waves = (g.n < g.E ? g.n : g.E) * (((int64_t)N + kStreamCols - 1) / kStreamCols);
+  return waves < kStreamWaves ? I8Kernel::kSplit : I8Kernel::kStream;
+}
+
 bool gemm_int8_fits(const Geometry &g, int32_t K, int32_t N) {
-  // blocks * threads of a launch stay below 2^32
-  const int64_t ncol = (N + kBN - 1) / kBN;
+  // blocks * threads of a launch stay below 2^32, whichever the tiles
+  const int64_t ncol = ((int64_t)N + kStreamCols - 1) / kStreamCols;
   return K <= kI8MaxK && gemm_grid_blocks(gemm_max_tiles(g), 1) * ncol <= UINT32_MAX / kGemmThreads;
 }
 
@@ -178,19 +663,34 @@ hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, cons
                                     const float *sx, const uint8_t *w, const float *sw,
                                     const uint8_t *wslot, const float *swslot, int32_t K,
                                     int32_t N, uint16_t *y, bool glu, hipStream_t s) {
-  const int32_t max_tiles = gemm_max_tiles(g);
+  const I8Kernel kind = i8_kernel(g, N);
+  const bool wide = kind == I8Kernel::kWide;
+  const int32_t max_tiles = wide ? wide_max_tiles(g) : gemm_max_tiles(g);
   if (g.n == 0 || max_tiles == 0) return hipSuccess;
-  const hipError_t e = launch_gemm_tiles(g, ws, wslot != nullptr, false, max_tiles, s);
+  const hipError_t e = launch_gemm_tiles(g, ws, wslot != nullptr, wide ? kShortRows : 0, max_tiles, s);
   if (e != hipSuccess) return e;
-  const int32_t ncol = (N + kBN - 1) / kBN;
-  const unsigned grid = (unsigned)gemm_grid_blocks(max_tiles, ncol);
-#define I8_ARGS                                                                              \
-  dim3(grid), dim3(kGemmThreads), 0, s, reinterpret_cast<const u32x4 *>(x), sx,              \
-      reinterpret_cast<const u32x4 *>(w), sw, reinterpret_cast<const u32x4 *>(wslot), swslot, \
-      ws.gemm_tiles, ws.gemm_ntiles, max_tiles, K, N, g.E, ncol, y
-  if (glu) hipLaunchKernelGGL(k_grouped_gemm_i8<true>, I8_ARGS);
-  else hipLaunchKernelGGL(k_grouped_gemm_i8<false>, I8_ARGS);
-#undef I8_ARGS
+#define I8_LAUNCH(KERN, COLS, THREADS)                                                         \
+  do {                                                                                         \
+    const int32_t ncol = (N + (COLS)-1) / (COLS);                                              \
+    hipLaunchKernelGGL(KERN, dim3((unsigned)gemm_grid_blocks(max_tiles, ncol)), dim3(THREADS), 0, s, \
+                       reinterpret_cast<const u32x4 *>(x), sx, reinterpret_cast<const u32x4 *>(w), sw, \
+                       reinterpret_cast<const u32x4 *>(wslot), swslot, ws.gemm_tiles,          \
+                       ws.gemm_ntiles, max_tiles, K, N, g.E, ncol, y);                         \
+  } while (0)
+  if (kind == I8Kernel::kWide) {
+    if (glu) I8_LAUNCH(k_grouped_gemm_i8_256<true>, kBN2, kGemmThreads);
+    else I8_LAUNCH(k_grouped_gemm_i8_256<false>, kBN2, kGemmThreads);
+  } else if (kind == I8Kernel::kSplit) {
+    if (glu) I8_LAUNCH((k_grouped_gemm_i8_stream<true, true>), kStreamCols, 256);
+    else I8_LAUNCH((k_grouped_gemm_i8_stream<false, true>), kStreamCols, 256);
+  } else if (kind == I8Kernel::kStream) {
+    if (glu) I8_LAUNCH((k_grouped_gemm_i8_stream<true, false>), kStreamCols, 64);
+    else I8_LAUNCH((k_grouped_gemm_i8_stream<false, false>), kStreamCols, 64);
+  } else {
+    if (glu) I8_LAUNCH(k_grouped_gemm_i8<true>, kBN, kGemmThreads);
+    else I8_LAUNCH(k_grouped_gemm_i8<false>, kBN, kGemmThreads);
+  }
+#undef I8_LAUNCH
   return hipGetLastError();
 }
 

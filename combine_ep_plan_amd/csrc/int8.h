@@ -1,5 +1,5 @@
-// int8.h -- INT8 rows: one fp32 scale a row, scale = amax / 127 and code = the
-// integer nearest to value / scale (ties to even).
+// int8.h -- INT8 rows: one fp32 scale a row, scale = amax * fp32(1 / 127) and
+// code = the integer nearest to value / scale (ties to even).
 #pragma once
 
 #include "device.h"
@@ -12,14 +12,23 @@ namespace epk {
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Scale of a row (or of an FP8 block) whose largest magnitude is amax: 1 for
-// a row of zeros, NaN for one that holds a value that is not finite (its
-// codes are then 0, so what it stands for is NaN, not a plausible number).
-// The scale stays at 2^-126 or above, so that its reciprocal is finite.
-__device__ __forceinline__ float scale_of(uint32_t amax_bits, float most) {
+// Scale of a row (or of an FP8 block) whose largest magnitude is amax, from
+// the quotient of amax and the format's largest code: 1 for a row of zeros,
+// NaN for one that holds a value that is not finite (its codes are then 0, so
+// what it stands for is NaN, not a plausible number).  The scale stays at
+// 2^-126 or above, so that its reciprocal is finite.
+__device__ __forceinline__ float scale_of(uint32_t amax_bits, float quotient) {
   if (amax_bits >= kInfBits) return __uint_as_float(0x7FC00000u);
   if (amax_bits == 0u) return 1.0f;
-  return fmaxf(__uint_as_float(amax_bits) / most, 1.17549435e-38f);
+  return fmaxf(quotient, 1.17549435e-38f);
+}
+// INT8: times the rounded 1/127 -- a scale is free to be a last bit off, the
+// codes are decided against it -- FP8: the division its format is defined by.
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  return scale_of(amax_bits, __uint_as_float(amax_bits) * (1.0f / 127.0f));
+}
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
+  return scale_of(amax_bits, __uint_as_float(amax_bits) / 448.0f);
 }
 
 // The integer nearest to the exact quotient y / s, ties to even, at most 127

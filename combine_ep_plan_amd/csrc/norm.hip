@@ -95,7 +95,7 @@ __device__ __forceinline__ u32x2 fp8_codes(const float y[8], float *scale, bool 
     const uint32_t o = (uint32_t)__shfl_xor((int)a, d);
     a = o > a ? o : a;
   }
-  float s = scale_of(a, 448.0f);
+  float s = fp8_scale(a);
   if (pow2 && a != 0u && a < kInfBits) {
     const uint32_t b = __float_as_uint(s);
     if (b & 0x007FFFFFu) s = __uint_as_float((b & 0x7F800000u) + 0x00800000u);
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a) {
   }
   const float rstd = rstd_of(ss, a.V * 8, a.eps);
   const uint32_t am = magnitude_bits(__uint_as_float(m) * rstd);
-  const float s8 = scale_of(am, 127.0f), inv8 = 1.0f / s8;
+  const float s8 = int8_scale(am), inv8 = 1.0f / s8;
   if (a.quant == kQuantInt8 && tid == 0) a.scales[row] = s8;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(1024) void k_quantize_int8(const u32x4 *__restrict_
   __syncthreads();
   m = 0;
   for (int i = 0; i < nw; ++i) m = s_max[i] > m ? s_max[i] : m;
-  const float s = scale_of(m, 127.0f), inv = 1.0f / s;
+  const float s = int8_scale(m), inv = 1.0f / s;
   if (tid == 0) scales[row] = s;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {

@@ -652,7 +652,7 @@ typedef enum ep_quant {
   EP_QUANT_NONE = 0,
   EP_QUANT_FP8 = 1,      /* e4m3, one scale per 128 channels, amax / 448 */
   EP_QUANT_FP8_POW2 = 2, /* ... the power of two at or above it */
-  EP_QUANT_INT8 = 3      /* int8, one scale per row, amax / 127 */
+  EP_QUANT_INT8 = 3      /* int8, one scale per row, amax * fp32(1 / 127) */
 } ep_quant_t;
 
 typedef struct ep_norm_rule {
@@ -677,8 +677,8 @@ typedef struct ep_norm_rule {
  *               bits, quantised from the fp32 y.  FP8: e4m3 [T, H] and fp32
  *               [T, H/128] (tag FP8_SCALES), H % 128 == 0, the FP8 dispatch's
  *               recipe.  INT8: int8 [T, H] and fp32 [T] (tag ROW_SCALES):
- *               scale = amax / 127 (1 for a row of zeros, at least 2^-126),
- *               code = the integer nearest to y / scale, ties to even.  A row
+ *               scale = amax * fp32(1/127) (1 for a row of zeros, at least
+ *               2^-126), code = the integer nearest to y / scale, ties to even.  A row
  *               (FP8: a block) with a value that is not finite gets codes 0
  *               and a NaN scale.
  * At least one of y and codes is given.  Enqueues one kernel. */

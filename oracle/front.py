@@ -138,12 +138,12 @@ def rmsnorm_bwd(h, w, gy, gh, eps):
 
 
 def int8_rows(y32):
-    """Codes and fp32 scales of fp32 rows: scale = amax / 127, code = the
-    integer nearest to the quotient, ties to even."""
+    """Codes and fp32 scales of fp32 rows: scale = amax * fp32(1/127), code =
+    the integer nearest to the quotient, ties to even."""
     y = np.asarray(y32, np.float32)
     a = np.abs(y).max(-1)
     ok = np.isfinite(y).all(-1)
-    s = np.where(a > 0, np.maximum(a / np.float32(127), np.float32(2.0 ** -126)), np.float32(1))
+    s = np.where(a > 0, np.maximum(a * (np.float32(1) / np.float32(127)), np.float32(2.0 ** -126)), np.float32(1))
     s = np.where(ok, s, np.float32(np.nan)).astype(np.float32)
     # the double quotient of two floats is a tie only if the exact one is
     with np.errstate(invalid="ignore"):
