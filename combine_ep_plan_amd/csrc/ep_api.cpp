@@ -5,6 +5,7 @@
 // one stream synchronisation.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -909,7 +910,7 @@ static ep_status_t check_norm_weight(const ep_tensor_t *t, int64_t H, bool *fp32
 }
 
 static bool norm_rule_ok(const ep_norm_rule_t *r) {
-  return r && std::isfinite(r->eps) && r->eps > 0.0 && r->reserved == 0 &&
+  return r && std::isfinite(r->eps) && r->eps >= (double)FLT_MIN && r->reserved == 0 &&
          r->quant >= EP_QUANT_NONE && r->quant <= EP_QUANT_INT8;
 }
 
@@ -971,7 +972,7 @@ ep_status_t ep_add_rmsnorm(const ep_norm_rule_t *rule, const ep_tensor_t *x,
 ep_status_t ep_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes) {
   if (!bytes || rows < 0 || rows > INT32_MAX || H < 8 || H % 8 != 0 || H > epk::kRowMaxChannels)
     return EP_ERR_INVALID_ARG;
-  *bytes = sizeof(float) * (size_t)epk::norm_bwd_groups((int32_t)rows) * (size_t)H;
+  *bytes = sizeof(float) * (size_t)epk::norm_bwd_groups((int32_t)rows, H) * (size_t)H;
   return EP_OK;
 }
 
@@ -1004,7 +1005,7 @@ ep_status_t ep_add_rmsnorm_bwd(const ep_norm_rule_t *rule, const ep_tensor_t *hi
     st = check_tensor(grad_weight, EP_TAG_NORM_WEIGHT, EP_DTYPE_FP32);
     if (st != EP_OK) return st;
     if (grad_weight->ndim != 1 || grad_weight->sizes[0] != H) return EP_ERR_BAD_SHAPE;
-    const int64_t need = (int64_t)epk::norm_bwd_groups((int32_t)T) * H;
+    const int64_t need = (int64_t)epk::norm_bwd_groups((int32_t)T, (int32_t)H) * H;
     if (need > 0) {
       st = check_tensor(workspace, EP_TAG_WORKSPACE, EP_DTYPE_FP32);
       if (st != EP_OK) return st;

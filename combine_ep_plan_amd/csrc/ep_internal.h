@@ -157,7 +157,7 @@ struct RmsNormBwd {
   bool h_fp32, w_fp32;
   double eps;
 };
-int32_t norm_bwd_groups(int32_t T);  // partial rows of grad_weight in the workspace
+int32_t norm_bwd_groups(int32_t T, int32_t H);  // partial rows of grad_weight in the workspace
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s);
 hipError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int32_t K, uint8_t *codes,
                                 float *scales, hipStream_t s);

@@ -31,25 +31,40 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
   return scale_of(amax_bits, __uint_as_float(amax_bits) / 448.0f);
 }
 
-// The integer nearest to the exact quotient y / s, ties to even, at most 127
-// in magnitude; inv = 1 / s.  y * inv is within 2^-16 of the quotient, so its
-// rounding is at most one off, and only next to a tie; r = y - q*s is exact
-// there (q has 7 bits, and |r| <= s/2 up to that error), and comparing it with
-// s / 2 settles it.
-__device__ __forceinline__ int32_t int8_code(float y, float s, float inv) {
-  float q = rintf(y * inv);
-  const float r = __builtin_fmaf(-q, s, y), half = 0.5f * s, a = fabsf(r);
-  const int32_t qi = (int32_t)q;
-  const int32_t step = a > half || (a == half && (qi & 1)) ? (r > 0.0f ? 1 : -1) : 0;
-  const int32_t c = qi + step;
-  return c > 127 ? 127 : c < -127 ? -127 : c;
-}
-
-// Eight codes in memory order.
+// Eight codes in memory order: the integer nearest to the exact quotient y / s,
+// ties to even; inv = 1 / s.  Adding 1.5 * 2^23 to y * inv in one fma leaves the
+// rounded quotient in the low mantissa bits (its low byte is the code); it is
+// off by one at most, and only next to a tie, since y * inv is within 2^-16 of
+// the quotient.  r = y - q*s is exact (q has 7 bits and |r| stays near s/2), so
+// one comparison of the largest |r| of the eight with s / 2 tells whether any
+// needs the settling below: a few in ten thousand do.  |y| <= amax keeps q
+// within 127.
 __device__ __forceinline__ u32x2 int8_codes(const float y[8], float s, float inv) {
-  uint32_t w[2] = {0u, 0u};
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  const float half = 0.5f * s;
+  float t[8], worst = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) w[c >> 2] |= (uint32_t)(int8_code(y[c], s, inv) & 0xFF) << (8 * (c & 3));
+  for (int c = 0; c < 8; ++c) {
+    t[c] = __builtin_fmaf(y[c], inv, kMagic);
+    const float q = t[c] - kMagic;
+    worst = fmaxf(worst, fabsf(__builtin_fmaf(-q, s, y[c])));
+  }
+  if (worst >= half) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float q = t[c] - kMagic, r = __builtin_fmaf(-q, s, y[c]), a = fabsf(r);
+      const bool odd = (__float_as_uint(t[c]) & 1u) != 0u;
+      if (a > half || (a == half && odd)) t[c] += r > 0.0f ? 1.0f : -1.0f;
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // v_perm_b32: bytes 0 of two words, then the two halves
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 1]), __float_as_uint(t[4 * i]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 3]), __float_as_uint(t[4 * i + 2]), 0x04000c0cu);
+    w[i] = lo | hi;
+  }
   return u32x2{w[0], w[1]};
 }
 

@@ -13,12 +13,15 @@
 // formulas.  The largest |y| is (largest |h * w|) * rstd, so one reduction
 // over the row gives both rstd and the INT8 scale, and the row is read once and
 // stays in registers.
+//
+// Rows: up to 2048 channels go one to a wave (four to a workgroup, no barrier);
+// longer ones one to a workgroup.
 #include "ep_internal.h"
 #include "int8.h"
+#include "lanes.h"
 
 namespace epk {
 
-constexpr int kNormMaxVec = 4;  // 16-byte vectors of bf16 a thread holds
 enum Quant : int32_t { kQuantNone = 0, kQuantFp8 = 1, kQuantFp8Pow2 = 2, kQuantInt8 = 3 };
 
 struct NormArgs {
@@ -29,21 +32,45 @@ struct NormArgs {
   u32x4 *y;        // or null
   u32x2 *codes;    // or null
   float *scales;
-  int32_t T, V;    // rows, vectors of 8 per row
+  int64_t T;       // rows
+  int32_t V;       // vectors of 8 per row
   int32_t w_fp32, quant;
-  double eps;
+  double eps, inv_h;
 };
 
-// Eight values of a bf16 or fp32 row.
+// Eight values of a bf16 or fp32 row as they are stored.
+template <typename T>
+struct Raw8 {
+  u32x4 v[sizeof(T) / 2];
+};
+
+template <typename T, bool NT>
+__device__ __forceinline__ Raw8<T> load_raw(const void *p, int64_t v) {
+  Raw8<T> r;
+  const u32x4 *q = static_cast<const u32x4 *>(p) + v * (int)(sizeof(T) / 2);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.v[i] = NT ? load_stream(q + i) : q[i];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack_raw(const Raw8<T> &r, float f[8]) {
+  if constexpr (sizeof(T) == 2) {
+    unpack8(r.v[0], f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(r.v[i].x);
+      f[4 * i + 1] = __uint_as_float(r.v[i].y);
+      f[4 * i + 2] = __uint_as_float(r.v[i].z);
+      f[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void load8(const void *p, int64_t v, float f[8]) {
-  if constexpr (sizeof(T) == 2) {
-    unpack8(static_cast<const u32x4 *>(p)[v], f);
-  } else {
-    const f32x4 a = static_cast<const f32x4 *>(p)[2 * v], b = static_cast<const f32x4 *>(p)[2 * v + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
+  unpack_raw(load_raw<T, false>(p, v), f);
 }
 
 template <typename T>
@@ -61,40 +88,61 @@ __device__ __forceinline__ void load_weight8(const void *w, int32_t fp32, int64_
   else load8<uint16_t>(w, v, f);
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
+// rstd of a row from its sum of squares: the hardware's fp64 reciprocal square
+// root (about 2^-26) and two Newton steps, then one rounding to fp32.
+__device__ __forceinline__ float rstd_of(double ss, double inv_h, double eps) {
+  const double a = __builtin_fma(ss, inv_h, eps);
+  double r = __builtin_amdgcn_rsq(a);
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(0.5 * r, __builtin_fma(-a * r, r, 1.0), r);
+  // an infinite or NaN sum: 1 / sqrt of it
+  return a < 1e300 ? (float)r : (float)(1.0 / sqrt(a));
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
-    v = o > v ? o : v;
+// Maximum of m (and sum of v) over the workgroup (up to 16 waves) or, WAVE,
+// over the wave.
+template <bool WAVE>
+__device__ __forceinline__ void row_reduce(uint32_t &m) {
+  m = wave_max(m);
+  if constexpr (!WAVE) {
+    __shared__ uint32_t s_max[16];
+    const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+    if (lane == 0) s_max[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = row_max((lane & 15) < nw ? s_max[lane & 15] : 0u);
   }
-  return v;
 }
-
-// rstd of a row from its sum of squares.
-__device__ __forceinline__ float rstd_of(double ss, int32_t H, double eps) {
-  return (float)(1.0 / sqrt(ss / (double)H + eps));
+template <bool WAVE>
+__device__ __forceinline__ void row_reduce(double &v, uint32_t &m) {
+  v = wave_sum(v);
+  m = wave_max(m);
+  if constexpr (!WAVE) {
+    __shared__ double s_sum[16];
+    __shared__ uint32_t s_max[16];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    if (lane == 0) {
+      s_sum[wv] = v;
+      s_max[wv] = m;
+    }
+    __syncthreads();
+    const int i = lane & 15;  // every 16-lane row reduces the waves' results
+    v = row_sum(i < nw ? s_sum[i] : 0.0);
+    m = row_max(i < nw ? s_max[i] : 0u);
+  }
 }
 
 // FP8 codes of eight values of y whose 128-channel block spans 16 lanes; the
-// FP8 dispatch's recipe (quantize_fp8_vec in dispatch.hip) on fp32 values.
+// FP8 dispatch's recipe (quantize_fp8_vec in dispatch.hip) on fp32 values.  The
+// correctly rounded quotient y / s without a division each: with inv = 1 / s
+// correctly rounded, q = y * inv corrected once by its exact remainder is
+// y / s rounded (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990), where nothing underflows: blocks of tiny
+// values divide.
 __device__ __forceinline__ u32x2 fp8_codes(const float y[8], float *scale, bool pow2) {
   uint32_t a = 0;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t m = magnitude_bits(y[c]);
-    a = m > a ? m : a;
-  }
-#pragma unroll
-  for (int d = 8; d > 0; d >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)a, d);
-    a = o > a ? o : a;
-  }
+  for (int c = 0; c < 8; ++c) a = umax(a, magnitude_bits(y[c]));
+  a = row_max(a);
   float s = fp8_scale(a);
   if (pow2 && a != 0u && a < kInfBits) {
     const uint32_t b = __float_as_uint(s);
@@ -103,8 +151,20 @@ __device__ __forceinline__ u32x2 fp8_codes(const float y[8], float *scale, bool 
   *scale = s;
   if (a >= kInfBits) return u32x2{0u, 0u};
   float q[8];
+  if (s >= 0x1p-80f && s <= 0x1p80f) {
+    const float inv = 1.0f / s;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) q[c] = fminf(fmaxf(y[c] / s, -448.0f), 448.0f);
+    for (int c = 0; c < 8; ++c) {
+      const float q0 = y[c] * inv;
+      // (a quotient of -0 would come back +0)
+      q[c] = copysignf(__builtin_fmaf(__builtin_fmaf(-q0, s, y[c]), inv, q0), y[c]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) q[c] = y[c] / s;
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) q[c] = fminf(fmaxf(q[c], -448.0f), 448.0f);
   uint32_t w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
   w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
   uint32_t w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
@@ -112,35 +172,50 @@ __device__ __forceinline__ u32x2 fp8_codes(const float y[8], float *scale, bool 
   return u32x2{w0, w1};
 }
 
-// Row of a workgroup: a launch counts its threads in 32 bits, so many rows
-// spread over the grid's second dimension too.
-constexpr int64_t kGridRows = 1 << 20;
-__device__ __forceinline__ int64_t grid_row() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
-static dim3 row_grid(int64_t rows) {
-  const int64_t gx = rows < kGridRows ? rows : kGridRows;
-  return dim3((unsigned)gx, (unsigned)((rows + gx - 1) / gx));
+// Workgroups of a launch over rows, RPB rows each: a launch counts its threads
+// in 32 bits, so many rows spread over the grid's second dimension too.
+constexpr int kRowWaves4 = 4;  // rows of a workgroup with a wave to a row
+static dim3 row_grid(int64_t rows, bool wave) {
+  const int64_t blocks = wave ? (rows + kRowWaves4 - 1) / kRowWaves4 : rows;
+  const int64_t gx = blocks < (1 << 20) ? blocks : 1 << 20;
+  return dim3((unsigned)gx, (unsigned)((blocks + gx - 1) / gx));
+}
+// This thread's row, its place in it and the threads that share the row.
+template <bool WAVE>
+__device__ __forceinline__ int64_t my_row(int &sub, int &step) {
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  sub = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  step = WAVE ? 64 : blockDim.x;
+  return WAVE ? b * kRowWaves4 + (threadIdx.x >> 6) : b;
 }
 
-// One workgroup per row; a thread holds VPT vectors of it.
-template <typename RT, bool RES, int VPT>
-__global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a) {
-  __shared__ double s_sum[16];
-  __shared__ uint32_t s_max[16];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, nw = blockDim.x >> 6;
-  const int64_t row = grid_row(), base = row * a.V;
-  if (row >= a.T) return;
-  float p[VPT][8];  // h * w
+template <typename RT, bool RES, int VPT, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_add_rmsnorm(NormArgs a) {
+  int sub, step;
+  const int64_t row = my_row<WAVE>(sub, step), base = row * a.V;
+  if (row >= a.T) return;  // the whole wave (and, with barriers, the workgroup)
+  float p[VPT][8];  // h, then h * w
+  Raw8<uint16_t> xr[VPT];
+  Raw8<RT> rr[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int32_t v = sub + i * step;
+    if (v >= a.V) continue;
+    xr[i] = load_raw<uint16_t, true>(a.x, base + v);
+    if constexpr (RES) rr[i] = load_raw<RT, true>(a.residual, base + v);
+  }
   double ss = 0.0;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int32_t v = tid + i * blockDim.x;
+    const int32_t v = sub + i * step;
     if (v >= a.V) continue;
     float h[8], w[8];
-    load8<uint16_t>(a.x, base + v, h);
+    unpack_raw(xr[i], h);
+    load_weight8(a.w, a.w_fp32, v, w);
     if constexpr (RES) {
       float r[8];
-      load8<RT>(a.residual, base + v, r);
+      unpack_raw(rr[i], r);
 #pragma unroll
       for (int c = 0; c < 8; ++c) h[c] += r[c];
       if constexpr (sizeof(RT) == 2) {
@@ -151,35 +226,21 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a) {
         store8<RT>(a.hidden, base + v, h);
       }
     }
-    load_weight8(a.w, a.w_fp32, v, w);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      ss += (double)h[c] * (double)h[c];
+      ss = __builtin_fma((double)h[c], (double)h[c], ss);
       p[i][c] = h[c] * w[c];
-      const uint32_t b = magnitude_bits(p[i][c]);
-      m = b > m ? b : m;
+      m = umax(m, magnitude_bits(p[i][c]));
     }
   }
-  ss = wave_sum(ss);
-  m = wave_max(m);
-  if (lane == 0) {
-    s_sum[wv] = ss;
-    s_max[wv] = m;
-  }
-  __syncthreads();
-  ss = 0.0;
-  m = 0;
-  for (int i = 0; i < nw; ++i) {
-    ss += s_sum[i];
-    m = s_max[i] > m ? s_max[i] : m;
-  }
-  const float rstd = rstd_of(ss, a.V * 8, a.eps);
+  row_reduce<WAVE>(ss, m);
+  const float rstd = rstd_of(ss, a.inv_h, a.eps);
   const uint32_t am = magnitude_bits(__uint_as_float(m) * rstd);
   const float s8 = int8_scale(am), inv8 = 1.0f / s8;
-  if (a.quant == kQuantInt8 && tid == 0) a.scales[row] = s8;
+  if (a.quant == kQuantInt8 && sub == 0) a.scales[row] = s8;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int32_t v = tid + i * blockDim.x;
+    const int32_t v = sub + i * step;
     if (v >= a.V) continue;
     float y[8];
 #pragma unroll
@@ -195,33 +256,51 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(NormArgs a) {
   }
 }
 
-// Threads and vectors a thread for rows of V vectors (V <= 4096).
-static void row_shape(int32_t V, int &threads, int &vpt) {
-  threads = V <= 64 ? 64 : V <= 128 ? 128 : V <= 1024 ? 256 : V <= 2048 ? 512 : 1024;
-  const int n = (V + threads - 1) / threads;
-  vpt = n <= 1 ? 1 : n <= 2 ? 2 : 4;
+// Threads of a row of V vectors (V <= 4096) and vectors a thread.
+struct RowShape {
+  bool wave;
+  int threads, vpt;
+};
+// Few rows (latency counts) get a thread to a vector where 1024 threads allow
+// it: INT8 rows of 1024 x 2048 4.1 us against 5.0 with a wave to a row.  Many
+// rows: a wave each up to 2048 channels, 33 us against 47 with a workgroup each
+// for 32768 x 2048 (no barrier, more loads in flight).
+constexpr int64_t kFewRows = 4096;
+static RowShape row_shape(int64_t rows, int32_t V) {
+  if (rows < kFewRows && V <= 1024) return {false, (V + 63) / 64 * 64, 1};
+  if (V <= 256) return {true, 256, V <= 64 ? 1 : V <= 128 ? 2 : 4};
+  const int threads = V <= 512 ? 256 : V <= 1024 ? 512 : 1024;
+  return {false, threads, V <= 2 * threads ? 2 : 4};
 }
+// F(VPT, WAVE) for a shape
+#define EP_ROW_SWITCH(sh, F)                    \
+  do {                                          \
+    if (sh.wave && sh.vpt == 1) F(1, true);     \
+    else if (sh.wave && sh.vpt == 2) F(2, true); \
+    else if (sh.wave) F(4, true);               \
+    else if (sh.vpt == 1) F(1, false);          \
+    else if (sh.vpt == 2) F(2, false);          \
+    else F(4, false);                           \
+  } while (0)
 
 hipError_t launch_add_rmsnorm(const RmsNorm &n, hipStream_t s) {
   if (n.T == 0) return hipSuccess;
   const NormArgs a{reinterpret_cast<const u32x4 *>(n.x), n.residual, n.w, n.hidden,
                    reinterpret_cast<u32x4 *>(n.y), reinterpret_cast<u32x2 *>(n.codes), n.scales,
-                   n.T, n.H / 8, n.w_fp32 ? 1 : 0, n.quant, n.eps};
-  int threads, vpt;
-  row_shape(a.V, threads, vpt);
-#define L2(RT, RES, P) \
-  hipLaunchKernelGGL((k_add_rmsnorm<RT, RES, P>), row_grid(n.T), dim3(threads), 0, s, a)
-#define L(RT, RES)                  \
-  do {                              \
-    if (vpt == 1) L2(RT, RES, 1);   \
-    else if (vpt == 2) L2(RT, RES, 2); \
-    else L2(RT, RES, 4);            \
-  } while (0)
-  if (!n.residual) L(uint16_t, false);
-  else if (n.res_fp32) L(float, true);
-  else L(uint16_t, true);
-#undef L
-#undef L2
+                   n.T, n.H / 8, n.w_fp32 ? 1 : 0, n.quant, n.eps, 1.0 / n.H};
+  const RowShape sh = row_shape(n.T, a.V);
+#define L3(RT, RES, P, W) \
+  hipLaunchKernelGGL((k_add_rmsnorm<RT, RES, P, W>), row_grid(n.T, W), dim3(sh.threads), 0, s, a)
+#define LN(P, W) L3(uint16_t, false, P, W)
+#define LB(P, W) L3(uint16_t, true, P, W)
+#define LF(P, W) L3(float, true, P, W)
+  if (!n.residual) EP_ROW_SWITCH(sh, LN);
+  else if (n.res_fp32) EP_ROW_SWITCH(sh, LF);
+  else EP_ROW_SWITCH(sh, LB);
+#undef LF
+#undef LB
+#undef LN
+#undef L3
   return hipGetLastError();
 }
 
@@ -232,13 +311,26 @@ hipError_t launch_add_rmsnorm(const RmsNorm &n, hipStream_t s) {
 //   grad_h = rstd * (g - n * mean(g * n)) [+ grad_hidden]
 //   grad_w = sum over rows of grad_y * n
 // One reduction over a row gives sum h^2 and sum g * h.  A workgroup takes
-// every G-th row and keeps its share of grad_w in registers; the G partial
-// rows go to the workspace and a second kernel adds them in order, in fp64, so
-// the result does not depend on scheduling.
+// every G-th row, the next row's loads in flight while one is reduced, and
+// keeps its share of grad_w in registers; the G partial rows go to the
+// workspace and a second kernel adds them in order, in fp64, so the result
+// does not depend on scheduling.
 
-constexpr int32_t kNormBwdGroups = 512;
+// Threads and vectors a thread of a backward row.
+static void bwd_shape(int32_t V, int &threads, int &vpt) {
+  threads = V <= 1024 ? (V + 63) / 64 * 64 : 1024;
+  vpt = V <= threads ? 1 : V <= 2 * threads ? 2 : 4;
+}
 
-int32_t norm_bwd_groups(int32_t T) { return T < kNormBwdGroups ? T : kNormBwdGroups; }
+// Workgroups of the backward: about two of 512 threads a compute unit (and a
+// row each at least).
+constexpr int32_t kNormBwdThreads = 512 * 512;
+int32_t norm_bwd_groups(int32_t T, int32_t H) {
+  int threads, vpt;
+  bwd_shape(H / 8, threads, vpt);
+  const int32_t G = kNormBwdThreads / threads;
+  return T < G ? T : G;
+}
 
 struct NormBwdArgs {
   const void *hidden;
@@ -248,65 +340,91 @@ struct NormBwdArgs {
   void *gx;
   float *part;          // [G][H] partial grad_w, or null
   int32_t T, V, w_fp32;
-  double eps;
+  double eps, inv_h;
 };
 
 template <typename RT, int VPT>
 __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
-  __shared__ double s_sum[2][16][2];
+  __shared__ double s_sum[2][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, nw = blockDim.x >> 6;
+  // the next row's loads in flight under this row, and the weight in registers,
+  // where they fit
+  constexpr bool AHEAD = VPT == 1;
   float w[VPT][8], dw[VPT][8];
+  Raw8<RT> hr[VPT], rr[VPT];
+  u32x4 gr[VPT];
+  const auto load = [&](int64_t t) {
+    const int64_t base = t * a.V;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int32_t v = tid + i * blockDim.x;
+    for (int i = 0; i < VPT; ++i) {
+      const int32_t v = tid + i * blockDim.x;
+      if (v >= a.V) continue;
+      hr[i] = load_raw<RT, true>(a.hidden, base + v);
+      gr[i] = load_stream(a.gy + base + v);
+      if (a.ghidden) rr[i] = load_raw<RT, true>(a.ghidden, base + v);
+    }
+  };
+  const auto weight = [&] {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) w[i][c] = dw[i][c] = 0.0f;
-    if (v < a.V) load_weight8(a.w, a.w_fp32, v, w[i]);
+    for (int i = 0; i < VPT; ++i) {
+      const int32_t v = tid + i * blockDim.x;
+      if (v < a.V) load_weight8(a.w, a.w_fp32, v, w[i]);
+    }
+  };
+  if constexpr (AHEAD) {
+    load(blockIdx.x);
+    weight();
   }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) dw[i][c] = 0.0f;
   int buf = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
     const int64_t base = t * a.V;
-    float h[VPT][8], g[VPT][8];
+    float h[VPT][8], g[VPT][8], r[VPT][8];
     double ss = 0.0, sg = 0.0;
+    if constexpr (!AHEAD) {
+      load(t);
+      weight();
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int32_t v = tid + i * blockDim.x;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) h[i][c] = g[i][c] = 0.0f;
+      for (int c = 0; c < 8; ++c) h[i][c] = g[i][c] = r[i][c] = 0.0f;
       if (v >= a.V) continue;
-      load8<RT>(a.hidden, base + v, h[i]);
-      unpack8(a.gy[base + v], g[i]);
+      unpack_raw(hr[i], h[i]);
+      unpack8(gr[i], g[i]);
+      if (a.ghidden) unpack_raw(rr[i], r[i]);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        ss += (double)h[i][c] * (double)h[i][c];
-        sg += (double)(g[i][c] * w[i][c]) * (double)h[i][c];
+        ss = __builtin_fma((double)h[i][c], (double)h[i][c], ss);
+        sg = __builtin_fma((double)(g[i][c] * w[i][c]), (double)h[i][c], sg);
       }
     }
+    if constexpr (AHEAD)
+      if (t + gridDim.x < a.T) load(t + gridDim.x);
     ss = wave_sum(ss);
     sg = wave_sum(sg);
     if (lane == 0) {
-      s_sum[buf][wv][0] = ss;
-      s_sum[buf][wv][1] = sg;
+      s_sum[buf][0][wv] = ss;
+      s_sum[buf][1][wv] = sg;
     }
     __syncthreads();   // two buffers: the next row's sums do not meet this row's readers
-    ss = sg = 0.0;
-    for (int i = 0; i < nw; ++i) {
-      ss += s_sum[buf][i][0];
-      sg += s_sum[buf][i][1];
-    }
-    const float rstd = rstd_of(ss, a.V * 8, a.eps);
-    const float mean = (float)(sg * (double)rstd / (double)(a.V * 8));  // mean of g * n
+    ss = row_sum((lane & 15) < nw ? s_sum[buf][0][lane & 15] : 0.0);
+    sg = row_sum((lane & 15) < nw ? s_sum[buf][1][lane & 15] : 0.0);
+    const float rstd = rstd_of(ss, a.inv_h, a.eps);
+    const float mean = (float)(sg * (double)rstd * a.inv_h);  // mean of g * n
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int32_t v = tid + i * blockDim.x;
       if (v >= a.V) continue;
-      float o[8], r[8];
-      if (a.ghidden) load8<RT>(a.ghidden, base + v, r);
+      float o[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const float n = h[i][c] * rstd;
-        o[c] = rstd * (g[i][c] * w[i][c] - n * mean);
-        if (a.ghidden) o[c] += r[c];
+        o[c] = rstd * (g[i][c] * w[i][c] - n * mean) + r[i][c];
         dw[i][c] += g[i][c] * n;
       }
       store8<RT>(a.gx, base + v, o);
@@ -321,23 +439,44 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void k_rmsnorm_dw(const float *__restrict__ part, int32_t G,
-                                                    int32_t H, float *__restrict__ dw) {
-  const int32_t c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= H) return;
-  double s = 0.0;
-  for (int32_t i = 0; i < G; ++i) s += (double)part[(int64_t)i * H + c];
-  dw[c] = (float)s;
+// grad_w[c] = sum of the G partial rows: a workgroup takes 32 columns, its 32
+// thread rows every 32nd partial row each, all fp64, joined in order.
+constexpr int kDwCols = 32, kDwRows = 32;
+__global__ __launch_bounds__(kDwCols * kDwRows) void k_rmsnorm_dw(const float *__restrict__ part,
+                                                                  int32_t G, int32_t H,
+                                                                  float *__restrict__ dw) {
+  __shared__ double s[kDwRows][kDwCols];
+  const int cl = threadIdx.x % kDwCols, rl = threadIdx.x / kDwCols;
+  const int32_t c = blockIdx.x * kDwCols + cl;
+  double sum = 0.0;
+  if (c < H) {
+    int32_t i = rl;
+    for (; i + 7 * kDwRows < G; i += 8 * kDwRows) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kDwRows) * H + c];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += (double)v[u];
+    }
+    for (; i < G; i += kDwRows) sum += (double)part[(int64_t)i * H + c];
+  }
+  s[rl][cl] = sum;
+  __syncthreads();
+  if (rl == 0 && c < H) {
+    for (int i = 1; i < kDwRows; ++i) sum += s[i][cl];
+    dw[c] = (float)sum;
+  }
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
+  const int32_t G = norm_bwd_groups(n.T, n.H);
   if (n.T > 0) {
     const NormBwdArgs a{n.hidden, n.w, reinterpret_cast<const u32x4 *>(n.gy), n.ghidden, n.gx,
-                        n.gw ? n.part : nullptr, n.T, n.H / 8, n.w_fp32 ? 1 : 0, n.eps};
+                        n.gw ? n.part : nullptr, n.T, n.H / 8, n.w_fp32 ? 1 : 0, n.eps, 1.0 / n.H};
     int threads, vpt;
-    row_shape(a.V, threads, vpt);
-    const unsigned G = (unsigned)norm_bwd_groups(n.T);
-#define L2(RT, P) hipLaunchKernelGGL((k_rmsnorm_bwd<RT, P>), dim3(G), dim3(threads), 0, s, a)
+    bwd_shape(a.V, threads, vpt);
+#define L2(RT, P) \
+  hipLaunchKernelGGL((k_rmsnorm_bwd<RT, P>), dim3((unsigned)G), dim3(threads), 0, s, a)
 #define L(RT)                    \
   do {                           \
     if (vpt == 1) L2(RT, 1);     \
@@ -352,49 +491,51 @@ hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!n.gw) return hipSuccess;
-  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((n.H + 255) / 256)), dim3(256), 0, s, n.part,
-                     norm_bwd_groups(n.T), n.H, n.gw);   // T == 0: zeros
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((n.H + kDwCols - 1) / kDwCols)),
+                     dim3(kDwCols * kDwRows), 0, s, n.part, G, n.H, n.gw);   // T == 0: zeros
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // INT8 rows from bf16 rows (the activation between an expert FFN's two INT8
-// products): one workgroup per row, the row in registers between the
-// reduction of its amax and its codes.
+// products): the row in registers between the reduction of its amax and its
+// codes.
 
-template <int VPT>
-__global__ __launch_bounds__(1024) void k_quantize_int8(const u32x4 *__restrict__ x,
-                                                        u32x2 *__restrict__ codes,
-                                                        float *__restrict__ scales, int64_t rows,
-                                                        int32_t V) {
-  __shared__ uint32_t s_max[16];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, nw = blockDim.x >> 6;
-  const int64_t row = grid_row(), base = row * V;
+template <int VPT, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_quantize_int8(const u32x4 *__restrict__ x,
+                                                                     u32x2 *__restrict__ codes,
+                                                                     float *__restrict__ scales,
+                                                                     int64_t rows, int32_t V) {
+  int sub, step;
+  const int64_t row = my_row<WAVE>(sub, step), base = row * V;
   if (row >= rows) return;
-  float f[VPT][8];
-  uint32_t m = 0;
+  u32x4 r[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int32_t v = tid + i * blockDim.x;
-    if (v >= V) continue;
-    unpack8(x[base + v], f[i]);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t b = magnitude_bits(f[i][c]);
-      m = b > m ? b : m;
-    }
+    const int32_t v = sub + i * step;
+    r[i] = v < V ? load_stream(x + base + v) : u32x4{0u, 0u, 0u, 0u};
   }
-  m = wave_max(m);
-  if (lane == 0) s_max[wv] = m;
-  __syncthreads();
-  m = 0;
-  for (int i = 0; i < nw; ++i) m = s_max[i] > m ? s_max[i] : m;
+  // bf16 magnitudes order like their bits: two at a time in the halves of a word
+  uint32_t hi = 0, lo = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t b = r[i][c] & 0x7FFF7FFFu;
+      hi = umax(hi, b);
+      lo = umax(lo, b << 16);
+    }
+  uint32_t m = umax(hi & 0xFFFF0000u, lo);
+  row_reduce<WAVE>(m);
   const float s = int8_scale(m), inv = 1.0f / s;
-  if (tid == 0) scales[row] = s;
+  if (sub == 0) scales[row] = s;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int32_t v = tid + i * blockDim.x;
-    if (v < V) codes[base + v] = m >= kInfBits ? u32x2{0u, 0u} : int8_codes(f[i], s, inv);
+    const int32_t v = sub + i * step;
+    if (v >= V) continue;
+    float f[8];
+    unpack8(r[i], f);
+    codes[base + v] = m >= kInfBits ? u32x2{0u, 0u} : int8_codes(f, s, inv);
   }
 }
 
@@ -402,15 +543,12 @@ hipError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int32_t K, uint
                                 float *scales, hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const int32_t V = K / 8;
-  int threads, vpt;
-  row_shape(V, threads, vpt);
-#define L(P)                                                                              \
-  hipLaunchKernelGGL((k_quantize_int8<P>), row_grid(rows), dim3(threads), 0, s,           \
+  const RowShape sh = row_shape(rows, V);
+#define L(P, W)                                                                            \
+  hipLaunchKernelGGL((k_quantize_int8<P, W>), row_grid(rows, W), dim3(sh.threads), 0, s,   \
                      reinterpret_cast<const u32x4 *>(x), reinterpret_cast<u32x2 *>(codes), \
                      scales, rows, V)
-  if (vpt == 1) L(1);
-  else if (vpt == 2) L(2);
-  else L(4);
+  EP_ROW_SWITCH(sh, L);
 #undef L
   return hipGetLastError();
 }

@@ -656,7 +656,7 @@ typedef enum ep_quant {
 } ep_quant_t;
 
 typedef struct ep_norm_rule {
-  double eps;    /* added to the mean square; positive and finite */
+  double eps;    /* added to the mean square; finite, at least 2^-126 */
   int32_t quant; /* ep_quant_t (0 for the backward) */
   int32_t reserved; /* must be 0 */
 } ep_norm_rule_t;

@@ -82,7 +82,7 @@ def test_norm_refusals(lib):  # noqa: F811
     q8, s8 = view(I8, T_, 4, 256), view(FP32, RS, 4)
     qf, sf = view(FP8, T_, 4, 256), view(FP32, F8S, 4, 2)
     f = lib.ep_add_rmsnorm
-    for bad in (norm_rule(0.0), norm_rule(-1.0), norm_rule(float("nan")), norm_rule(float("inf")),
+    for bad in (norm_rule(0.0), norm_rule(-1.0), norm_rule(float("nan")), norm_rule(float("inf")), norm_rule(1e-39),
                 norm_rule(quant=4), norm_rule(quant=-1), norm_rule(reserved=1), None):
         assert f(bad, x, None, w, None, y, None, None, None) == INVALID
     r = norm_rule()
