@@ -34,17 +34,29 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 }
 
 // Across the four rows: a swap of a register with itself leaves, in its two
-// results, the values of the even and odd rows (halves), so adding or comparing
-// them needs no selection.
+// results, the values of the even and odd rows (halves), so combining the two
+// needs no selection.
+__device__ __forceinline__ void swap16(double v, double &a, double &b) {
+  const uint64_t w = (uint64_t)__double_as_longlong(v);
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)w, (uint32_t)w, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(w >> 32), (uint32_t)(w >> 32), false, false);
+  a = __longlong_as_double((int64_t)join(lo[0], hi[0]));
+  b = __longlong_as_double((int64_t)join(lo[1], hi[1]));
+}
+__device__ __forceinline__ void swap32(double v, double &a, double &b) {
+  const uint64_t w = (uint64_t)__double_as_longlong(v);
+  const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)w, (uint32_t)w, false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(w >> 32), (uint32_t)(w >> 32), false, false);
+  a = __longlong_as_double((int64_t)join(lo[0], hi[0]));
+  b = __longlong_as_double((int64_t)join(lo[1], hi[1]));
+}
+
 __device__ __forceinline__ double join_rows_sum(double v) {
-  uint64_t b = (uint64_t)__double_as_longlong(v);
-  auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
-  auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
-  v = __longlong_as_double((int64_t)join(lo[0], hi[0])) + __longlong_as_double((int64_t)join(lo[1], hi[1]));
-  b = (uint64_t)__double_as_longlong(v);
-  lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
-  hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
-  return __longlong_as_double((int64_t)join(lo[0], hi[0])) + __longlong_as_double((int64_t)join(lo[1], hi[1]));
+  double a, b;
+  swap16(v, a, b);
+  v = a + b;
+  swap32(v, a, b);
+  return a + b;
 }
 
 __device__ __forceinline__ uint32_t join_rows_max(uint32_t v) {

@@ -15,39 +15,121 @@
 // chosen one (by exponents, before anything can underflow), so they sum to
 // scale whatever the logits.
 //
-// One wave per token; lane i holds experts i*PER .. i*PER + PER - 1, so the
-// first lane among equals holds the lowest expert.  Each of the k rounds: the
-// lane's best choice left, the wave's maximum, a ballot for its first lane.
+// G lanes per token: a wave (64) for few tokens, a 16-lane row for many, as in
+// route.hip; lane i holds experts i, i + G, ...  Each of the k rounds: the
+// lane's best choice left, the token's maximum by lane moves, then the lowest
+// expert that has it.  A few thousand instructions a wave on a few KB: the
+// kernel is bound by their latency for few tokens and their number for many.
 #include <math.h>
 
 #include "ep_internal.h"
-#include "route_impl.h"
+#include "lanes.h"
 
 namespace epk {
 
 constexpr int kScoreWaves = 4;       // waves per workgroup
-constexpr int kMaxGroups = 64;       // expert groups: at least one lane each
+constexpr int kMaxGroups = 64;       // expert groups
 
 struct ScoreRule {
   int32_t sigmoid, groups, kept, top2, renorm;
   float scale;
 };
 
-__device__ __forceinline__ double shfl_xor_max(double v, int d) {
-  const double o = __shfl_xor(v, d);
-  return o > v ? o : v;
+// e^x for x <= 0 in fp64 to about an ulp: x = n ln 2 + r, |r| <= ln 2 / 2, the
+// Taylor series of e^r to r^13 (the next term is below 2^-57), times 2^n.
+__device__ __forceinline__ double exp_neg(double x) {
+  x = fmax(x, -800.0);  // below: 0 (the scaling underflows)
+  const double n = rint(x * 1.4426950408889634);
+  const double r = __builtin_fma(-n, 2.3190468138462996e-17, __builtin_fma(-n, 0.6931471805599453, x));
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return ldexp(p, (int)n);
 }
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = shfl_xor_max(v, d);
+// 1 / x for x in [1, 2048]: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double recip(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+}
+
+__device__ __forceinline__ double sigmoid_of(double l) {
+  const double e = exp_neg(-fabs(l)), r = recip(1.0 + e);
+  return l >= 0.0 ? r : e * r;
+}
+
+__device__ __forceinline__ double max_d(double a, double b) { return a > b ? a : b; }
+
+// Reductions over a token's G lanes (a 16-lane row or the wave); every lane
+// gets the result.
+template <int G>
+__device__ __forceinline__ double token_max(double v) {
+  v = max_d(v, dpp_d<kDppXor1>(v));
+  v = max_d(v, dpp_d<kDppXor2>(v));
+  v = max_d(v, dpp_d<kDppHalfMirror>(v));
+  v = max_d(v, dpp_d<kDppMirror>(v));
+  if constexpr (G == 64) {
+    double a, b;
+    swap16(v, a, b);
+    v = max_d(a, b);
+    swap32(v, a, b);
+    v = max_d(a, b);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ double token_sum(double v) {
+  return G == 64 ? wave_sum(v) : row_sum(v);
+}
+template <int G>
+__device__ __forceinline__ uint32_t token_min(uint32_t v) {
+  return ~(G == 64 ? wave_max(~v) : row_max(~v));
+}
+template <int G>
+__device__ __forceinline__ float token_sum_f(float v) {
+  v += __uint_as_float(dpp<kDppXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppMirror>(__float_as_uint(v)));
+  if constexpr (G == 64) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float token_max_f(float v) {
+  v = fmaxf(v, __uint_as_float(dpp<kDppXor1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kDppXor2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kDppHalfMirror>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<kDppMirror>(__float_as_uint(v))));
+  if constexpr (G == 64) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
 }
 
-__device__ __forceinline__ double wave_add(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// The value of lane J of each 16-lane row (J < 16).
+template <int J>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return dpp<0x150 + J>(v);  // row_newbcast
 }
 
 // A logit as the routing reads it: NaN masks like -inf, +inf is the largest float.
@@ -55,140 +137,203 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
 }
 
-__device__ __forceinline__ float load_logit(const void *p, int64_t i, bool bf16) {
-  return clean_logit(bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16)
-                          : static_cast<const float *>(p)[i]);
+// LT: float, or uint16_t for bf16
+template <typename LT>
+__device__ __forceinline__ float logit_value(LT v) {
+  if constexpr (sizeof(LT) == 2) return clean_logit(__uint_as_float((uint32_t)v << 16));
+  else return clean_logit(v);
 }
 
 __device__ __forceinline__ bool masked(float l) { return l == -INFINITY; }
 
-template <int PER>
+// Top two of two disjoint sets.
+__device__ __forceinline__ void join2(double &m1, double &m2, double o1, double o2) {
+  m2 = max_d(m1 < o1 ? m1 : o1, max_d(m2, o2));
+  m1 = max_d(m1, o1);
+}
+
+// Masks the experts of the groups a token may not choose from.  The choices go
+// through LDS (sv, the token's own part): `per` lanes share a group, each
+// scanning every per-th member, then join; more groups than lanes take several
+// passes, which leave their values in gv.
+template <int G, int PER>
+__device__ __forceinline__ void keep_groups(double (&v)[PER], const ScoreRule &rule, int32_t E,
+                                            int sub, double *sv, double *gv) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sv[sub + G * i] = v[i];
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  int per = G;
+  while (per > 1 && per * rule.groups > G) per >>= 1;
+  const int gs = E / rule.groups;
+  for (int q0 = 0; q0 < rule.groups; q0 += G / per) {
+    const int q = q0 + sub / per;
+    double m1 = -INFINITY, m2 = -INFINITY;
+    if (q < rule.groups) {
+      for (int i = sub & (per - 1); i < gs; i += per) {
+        const double c = sv[q * gs + i];
+        m2 = max_d(m2, m1 < c ? m1 : c);
+        m1 = max_d(m1, c);
+      }
+    }
+    if (per > 1) join2(m1, m2, dpp_d<kDppXor1>(m1), dpp_d<kDppXor1>(m2));
+    if (per > 2) join2(m1, m2, dpp_d<kDppXor2>(m1), dpp_d<kDppXor2>(m2));
+    if (per > 4) join2(m1, m2, dpp_d<kDppHalfMirror>(m1), dpp_d<kDppHalfMirror>(m2));
+    if (per > 8) join2(m1, m2, dpp_d<kDppMirror>(m1), dpp_d<kDppMirror>(m2));
+    if constexpr (G == 64) {
+      double a1, b1, a2, b2;
+      if (per > 16) {
+        swap16(m1, a1, b1);
+        swap16(m2, a2, b2);
+        m1 = a1, m2 = a2;
+        join2(m1, m2, b1, b2);
+      }
+      if (per > 32) {
+        swap32(m1, a1, b1);
+        swap32(m2, a2, b2);
+        m1 = a1, m2 = a2;
+        join2(m1, m2, b1, b2);
+      }
+    }
+    if (q < rule.groups) gv[q] = rule.top2 && m2 > -INFINITY ? m1 + m2 : m1;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  // a group stays if fewer than `kept` come before it; lane `sub` ranks groups
+  // sub, sub + G, ...
+  uint64_t kept = 0;  // bit g
+  for (int q0 = 0; q0 < rule.groups; q0 += G) {
+    const int q = q0 + sub;
+    const double mine = q < rule.groups ? gv[q] : -INFINITY;
+    int rank = 0;
+    for (int p = 0; p < rule.groups; ++p) {
+      const double o = gv[p];
+      rank += o > mine || (o == mine && p < q) ? 1 : 0;
+    }
+    const uint64_t b = __ballot(q < rule.groups && rank < rule.kept);
+    if constexpr (G == 64) kept = b;  // at most 64 groups
+    else kept |= ((b >> (threadIdx.x & 48)) & 0xFFFFull) << q0;
+  }
+  const float inv = 1.0f / (float)gs;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = sub + G * i;
+    const int g = (int)(((float)e + 0.5f) * inv);  // e / gs, exact for E <= 1024
+    if (e < E && !((kept >> g) & 1)) v[i] = -INFINITY;
+  }
+}
+
+template <typename LT, int G, int PER>
 __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route(
-    const void *__restrict__ logits, int32_t bf16, const float *__restrict__ bias, ScoreRule rule,
-    int32_t T, int32_t E, int32_t k, int32_t *__restrict__ idx_out, float *__restrict__ w_out,
+    const LT *__restrict__ logits, const float *__restrict__ bias, ScoreRule rule, int32_t T,
+    int32_t E, int32_t k, int32_t *__restrict__ idx_out, float *__restrict__ w_out,
     float *__restrict__ scores) {
-  __shared__ double s_choice[kScoreWaves][64 * PER];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kScoreWaves + wv;
-  if (t >= T) return;  // the whole wave; no workgroup barrier below
-  const int e0 = lane * PER;
+  constexpr int kTokens = 64 / G;  // of a wave
+  __shared__ double s_choice[kScoreWaves * kTokens][G * PER];
+  __shared__ double s_group[kScoreWaves * kTokens][kMaxGroups];
+  const int lane = threadIdx.x & 63, sub = lane & (G - 1), tok = threadIdx.x / G;
+  const int64_t t0 = (int64_t)blockIdx.x * (kScoreWaves * kTokens) + tok;
+  const bool live = t0 < T;
+  if (G == 64 && !live) return;  // the whole wave; no workgroup barrier below
+  const int64_t t = live ? t0 : T - 1;  // (G = 16) idle rows keep in step on the last token
+  // all loads first, none behind a branch of its own
+  LT raw[PER];
+  float be[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) raw[i] = logits[t * E + min(sub + G * i, E - 1)];
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) be[i] = bias[min(sub + G * i, E - 1)];
+  }
   float l[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? load_logit(logits, t * E + e0 + i, bf16) : -INFINITY;
+  for (int i = 0; i < PER; ++i) l[i] = sub + G * i < E ? logit_value(raw[i]) : -INFINITY;
 
   const bool grouped = rule.groups > 1;
   const bool by_logit = !bias && !(grouped && rule.top2);
-  double lmax = -INFINITY, z = 1.0;
-  if (!rule.sigmoid) {
+  const bool want_scores = scores || !by_logit;
+  double lmax = 0.0, zinv = 0.0;
+  double v[PER];  // scores (a masked expert's come out 0), then choices
+  if (rule.sigmoid) {
+    if (want_scores) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = sigmoid_of((double)l[i]);
+    }
+  } else if (want_scores || !rule.renorm) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = fmaxf(m, l[i]);
-    lmax = wave_max((double)m);
-    if (scores || !rule.renorm || !by_logit) {
-      z = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) z += masked(l[i]) ? 0.0 : exp((double)l[i] - lmax);
-      z = wave_add(z);
-    }
-  }
-  double v[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const bool in = e0 + i < E, dead = masked(l[i]);
-    v[i] = (double)l[i];
-    if (scores || !by_logit) {
-      const double s = dead ? 0.0
-                       : rule.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i]))
-                                      : exp((double)l[i] - lmax) / z;
-      if (scores && in) scores[t * E + e0 + i] = (float)s;
-      if (!by_logit) v[i] = dead ? -INFINITY : bias && in ? s + (double)bias[e0 + i] : s;
-    }
-    if (!(v[i] > -INFINITY)) v[i] = -INFINITY;  // a bias that is NaN masks too
-  }
-
-  if (grouped) {
-    double *sv = s_choice[wv];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sv[e0 + i] = v[i];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    // `per` lanes (a power of two) share a group: each scans every per-th member
-    int per = 64;
-    while (per * rule.groups > 64) per >>= 1;
-    const int gs = E / rule.groups, q = lane / per;
-    double m1 = -INFINITY, m2 = -INFINITY;
-    if (q < rule.groups) {
-      for (int i = lane % per; i < gs; i += per) {
-        const double c = sv[q * gs + i];
-        m2 = fmax(m2, fmin(m1, c));
-        m1 = fmax(m1, c);
-      }
-    }
-    for (int d = 1; d < per; d <<= 1) {
-      const double o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
-      m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-      m1 = fmax(m1, o1);
-    }
-    const double value = rule.top2 && m2 > -INFINITY ? m1 + m2 : m1;
-    int rank = 0;
-    for (int p = 0; p < rule.groups; ++p) {
-      const double o = __shfl(value, p * per);
-      rank += o > value || (o == value && p < q) ? 1 : 0;
-    }
-    // bit q * per: group q stays
-    const uint64_t kept = __ballot(q < rule.groups && rank < rule.kept);
-    const float inv = 1.0f / (float)gs;
+    m = token_max_f<G>(m);
+    lmax = masked(m) ? 0.0 : (double)m;
+    double z = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int g = (int)(((float)(e0 + i) + 0.5f) * inv);  // (e0 + i) / gs, exact for E <= 1024
-      if (e0 + i < E && !((kept >> (g * per)) & 1)) v[i] = -INFINITY;
+      v[i] = exp_neg((double)l[i] - lmax);
+      z += v[i];
     }
+    z = token_sum<G>(z);
+    zinv = z > 0.0 ? recip(z) : 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] *= zinv;
   }
+  if (scores) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (sub + G * i < E && live) scores[t * E + sub + G * i] = (float)v[i];
+  }
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = (double)l[i];
+  } else if (bias) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] += (double)be[i];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)  // a bias that is NaN masks too
+    v[i] = !masked(l[i]) && v[i] > -INFINITY ? v[i] : -INFINITY;
+  if (grouped) keep_groups<G, PER>(v, rule, E, sub, s_choice[tok], s_group[tok]);
 
   int32_t my_e = -1;
-  float my_l = -INFINITY;
   for (int j = 0; j < k; ++j) {
     double b = v[0];
     int bi = 0;
-    float bl = l[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) {
       const bool g = v[i] > b;
       b = g ? v[i] : b;
       bi = g ? i : bi;
-      bl = g ? l[i] : bl;
     }
-    const double top = wave_max(b);
-    if (!(top > -INFINITY)) break;  // wave-uniform: nothing left to choose
-    const int src = __builtin_ctzll(__ballot(b == top));
-    const int e = __shfl(e0 + bi, src);
-    const float el = __shfl(bl, src);
+    const double top = token_max<G>(b);
+    const bool any = top > -INFINITY;
+    if (!__any(any)) break;  // nothing left to choose for any token of the wave
+    const uint32_t e = token_min<G>(any && b == top ? (uint32_t)(sub + G * bi) : 0xFFFFFFFFu);
+    const int pos = (e & (G - 1)) == (uint32_t)sub ? (int)(e / G) : -1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = lane == src && i == bi ? -INFINITY : v[i];
-    my_e = lane == j ? e : my_e;
-    my_l = lane == j ? el : my_l;
+    for (int i = 0; i < PER; ++i) v[i] = any && i == pos ? -INFINITY : v[i];
+    my_e = sub == j && any ? (int32_t)e : my_e;
   }
 
   const bool chosen = my_e >= 0;
+  const double my_l = chosen ? (double)logit_value(logits[t * E + my_e]) : 0.0;
   double w = 0.0;
   if (rule.renorm) {
     // exponents of the scores, up to a common factor: l, or min(l, 0) with 1 + e^-|l| beside it
-    const double u = !chosen ? -INFINITY : rule.sigmoid ? fmin((double)my_l, 0.0) : (double)my_l;
-    const double um = wave_max(u);
+    const double u = !chosen ? -INFINITY : rule.sigmoid ? fmin(my_l, 0.0) : my_l;
+    const double um = token_max<G>(u);
     if (chosen) {
-      w = exp(u - um);
-      if (rule.sigmoid) w /= 1.0 + exp(-fabs((double)my_l));
+      w = exp_neg(u - um);
+      if (rule.sigmoid) w *= recip(1.0 + exp_neg(-fabs(my_l)));
     }
-    const double sum = wave_add(w);
-    if (chosen) w = w / sum * (double)rule.scale;
+    const double sum = token_sum<G>(w);
+    if (chosen) w = w / sum;
   } else if (chosen) {
-    w = (rule.sigmoid ? 1.0 / (1.0 + exp(-(double)my_l)) : exp((double)my_l - lmax) / z) *
-        (double)rule.scale;
+    w = rule.sigmoid ? sigmoid_of(my_l) : exp_neg(my_l - lmax) * zinv;
   }
-  if (lane < k) {
-    idx_out[t * k + lane] = my_e;
-    w_out[t * k + lane] = (float)w;
+  if (live && sub < k) {
+    idx_out[t * k + sub] = my_e;
+    w_out[t * k + sub] = (float)(w * (double)rule.scale);
   }
 }
 
@@ -203,92 +348,113 @@ __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route(
 // The choice itself has no gradient (nor has the bias).  Entries of -1, ids out
 // of range and masked experts carry none; an expert named twice gets the sum.
 // DENSE: every expert has a gradient, so all logits are read; otherwise only
-// the chosen ones are, and the rest of the row is zeros.
+// the chosen ones are, and the rest of the row is zeros.  Lanes as in the
+// forward: bound by memory for many tokens.
 
-template <bool DENSE, int PER>
+// r[i] += the part of each entry that names expert sub + G * i.
+template <int G, int PER, int J>
+__device__ __forceinline__ void add_entries(float (&r)[PER], int32_t e, float part, int sub, int k) {
+  if constexpr (J < kMaxTopK) {
+    if (J < k) {  // wave-uniform
+      // entry J sits in lane J of the token's lanes
+      uint32_t ej, pj;
+      if constexpr (G == 16) {
+        ej = row_lane<J>((uint32_t)e);
+        pj = row_lane<J>(__float_as_uint(part));
+      } else {
+        ej = __builtin_amdgcn_readlane((uint32_t)e, J);
+        pj = __builtin_amdgcn_readlane(__float_as_uint(part), J);
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) r[i] += (uint32_t)(sub + G * i) == ej ? __uint_as_float(pj) : 0.0f;
+      add_entries<G, PER, J + 1>(r, e, part, sub, k);
+    }
+  }
+}
+
+template <typename LT, bool DENSE, int G, int PER>
 __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route_bwd(
-    const void *__restrict__ logits, int32_t bf16, const int32_t *__restrict__ idx,
+    const LT *__restrict__ logits, const int32_t *__restrict__ idx,
     const float *__restrict__ gw, const float *__restrict__ gs, ScoreRule rule, int32_t T,
-    int32_t E, int32_t k, void *__restrict__ gl, uint32_t *__restrict__ status) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kScoreWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
+    int32_t E, int32_t k, LT *__restrict__ gl, uint32_t *__restrict__ status) {
+  const int lane = threadIdx.x & 63, sub = lane & (G - 1);
+  const int64_t t0 = (int64_t)blockIdx.x * (kScoreWaves * 64 / G) + threadIdx.x / G;
+  const bool live = t0 < T;
+  if (G == 64 && !live) return;
+  const int64_t t = live ? t0 : T - 1;
+  // every load that depends on nothing first
+  LT raw[PER];
+  float l[PER], ds[PER];
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) raw[i] = logits[t * E + min(sub + G * i, E - 1)];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ds[i] = 0.0f;
+    if (gs) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) ds[i] = gs[t * E + min(sub + G * i, E - 1)];
+    }
+  }
   // lane j < k: entry j
-  int32_t e = lane < k ? idx[t * k + lane] : -1;
+  int32_t e = sub < k ? idx[t * k + sub] : -1;
+  float g = sub < k ? gw[t * k + sub] * rule.scale : 0.0f;
   const bool out_of_range = e >= E || e < -1;
-  if (__ballot(out_of_range) != 0 && lane == 0) atomicOr(status, kFlagIndexRange);
-  if (e >= E) e = -1;
-  float el = e >= 0 ? load_logit(logits, t * E + e, bf16) : -INFINITY;
+  if (__any(out_of_range) && lane == 0) atomicOr(status, kFlagIndexRange);
+  if (e >= E || e < 0) e = -1;
+  const float el = e >= 0 ? logit_value(logits[t * E + e]) : -INFINITY;
   if (masked(el)) e = -1;
-  const float g = e >= 0 ? gw[t * k + lane] * rule.scale : 0.0f;
+  if (e < 0) g = 0.0f;
 
-  float l[PER], lmax = -INFINITY, z = 0.0f;
+  float lmax = -INFINITY, zinv = 0.0f;
   if constexpr (DENSE) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = lane + 64 * i;
-      l[i] = c < E ? load_logit(logits, t * E + c, bf16) : -INFINITY;
+      l[i] = sub + G * i < E ? logit_value(raw[i]) : -INFINITY;
+      ds[i] = masked(l[i]) ? 0.0f : ds[i];
       lmax = fmaxf(lmax, l[i]);
     }
     if (!rule.sigmoid) {
+      lmax = token_max_f<G>(lmax);
+      float z = 0.0f;
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) lmax = fmaxf(lmax, __shfl_xor(lmax, d));
-#pragma unroll
-      for (int i = 0; i < PER; ++i) z += masked(l[i]) ? 0.0f : expf(l[i] - lmax);
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) z += __shfl_xor(z, d);
+      for (int i = 0; i < PER; ++i) {
+        l[i] = masked(l[i]) ? 0.0f : expf(l[i] - lmax);  // the score's numerator from here on
+        z += l[i];
+      }
+      z = token_sum_f<G>(z);
+      zinv = z > 0.0f ? 1.0f / z : 0.0f;
     }
   }
 
   float part = g;  // what expert e gets: of ds (DENSE without renorm) or of dl
   if (rule.renorm) {
-    float um = e < 0 ? -INFINITY : rule.sigmoid ? fminf(el, 0.0f) : el;
-    const float u = um;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) um = fmaxf(um, __shfl_xor(um, d));  // k <= 16 lanes
+    const float u = e < 0 ? -INFINITY : rule.sigmoid ? fminf(el, 0.0f) : el;
+    const float um = token_max_f<G>(u);
     float p = e < 0 ? 0.0f : expf(u - um);
     if (rule.sigmoid && e >= 0) p /= 1.0f + expf(-fabsf(el));
-    float sum = p;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    const float sum = token_sum_f<G>(p);
     p = e >= 0 ? p / sum : 0.0f;
-    float a = g * p;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) a += __shfl_xor(a, d);
-    part = p * (g - a);
+    part = p * (g - token_sum_f<G>(g * p));
     if (rule.sigmoid && e >= 0) part /= 1.0f + expf(el);
   } else if (!DENSE && e >= 0) {  // sigmoid
-    const float s = 1.0f / (1.0f + expf(-el));
-    part = g * s / (1.0f + expf(el));
+    part = g / ((1.0f + expf(-el)) * (1.0f + expf(el)));
   }
 
-  float r[PER];  // dl of the chosen (renorm or sparse), or ds
+  float r[PER];  // dl of the chosen (renorm or sparse), or their ds
 #pragma unroll
   for (int i = 0; i < PER; ++i) r[i] = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int ej = __shfl(e, j);
-    const float pj = __shfl(part, j);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) r[i] += lane + 64 * i == ej ? pj : 0.0f;
-  }
+  add_entries<G, PER, 0>(r, e, part, sub, k);
   if constexpr (DENSE) {
-    float ds[PER], dot = 0.0f;
+    float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = lane + 64 * i;
-      ds[i] = gs && c < E && !masked(l[i]) ? gs[t * E + c] : 0.0f;
       if (!rule.renorm) ds[i] += r[i];
-      if (!rule.sigmoid && !masked(l[i])) {
-        l[i] = expf(l[i] - lmax) / z;  // the score from here on
+      if (!rule.sigmoid) {
+        l[i] *= zinv;
         dot += ds[i] * l[i];
-      } else if (!rule.sigmoid) {
-        l[i] = 0.0f;
       }
     }
-    if (!rule.sigmoid) {
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
-    }
+    if (!rule.sigmoid) dot = token_sum_f<G>(dot);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       float v;
@@ -299,21 +465,35 @@ __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route_bwd(
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = lane + 64 * i;
-    if (c >= E) continue;
-    if (bf16) static_cast<uint16_t *>(gl)[t * E + c] = (uint16_t)(pack_bf16x2(r[i], 0.0f) & 0xFFFFu);
-    else static_cast<float *>(gl)[t * E + c] = r[i];
+    const int c = sub + G * i;
+    if (c >= E || !live) continue;
+    if constexpr (sizeof(LT) == 2) gl[t * E + c] = (uint16_t)(pack_bf16x2(r[i], 0.0f) & 0xFFFFu);
+    else gl[t * E + c] = r[i];
   }
 }
 
-#define EP_PER_SWITCH(E, F)          \
-  do {                               \
-    const int per_ = ((E) + 63) / 64; \
-    if (per_ <= 1) F(1);             \
-    else if (per_ <= 2) F(2);        \
-    else if (per_ <= 4) F(4);        \
-    else if (per_ <= 8) F(8);        \
-    else F(16);                      \
+// F(G, PER): a wave per token for few tokens and for more than 256 experts
+// (their choices would not fit a row's registers and LDS); a 16-lane row
+// otherwise.  Forward with E = 256, 8 groups: 6.7 us with a wave and 11.1 with
+// a row at 128 tokens, 11.4 and 11.5 at 4096, 33 and 22 at 16384; E = 128,
+// softmax: 4.6 and 5.5 at 1024, 7.5 and 5.7 at 4096.
+static bool wave_per_token(int32_t T, int32_t E) { return E > 256 || T <= (E > 128 ? 4096 : 2048); }
+#define EP_SCORE_SWITCH(T, E, F)                                 \
+  do {                                                           \
+    if (wave_per_token(T, E)) {                                  \
+      const int per_ = ((E) + 63) / 64;                          \
+      if (per_ <= 1) F(64, 1);                                   \
+      else if (per_ <= 2) F(64, 2);                              \
+      else if (per_ <= 4) F(64, 4);                              \
+      else if (per_ <= 8) F(64, 8);                              \
+      else F(64, 16);                                            \
+    } else {                                                     \
+      const int per_ = ((E) + 15) / 16;                          \
+      if (per_ <= 2) F(16, 2);                                   \
+      else if (per_ <= 4) F(16, 4);                              \
+      else if (per_ <= 8) F(16, 8);                              \
+      else F(16, 16);                                            \
+    }                                                            \
   } while (0)
 
 static ScoreRule score_rule(const ep_route_rule_t &r) {
@@ -321,16 +501,27 @@ static ScoreRule score_rule(const ep_route_rule_t &r) {
                    r.group_score == EP_GROUP_TOP2, r.renormalise, r.scale};
 }
 
+static unsigned score_blocks(int32_t T, int G) {
+  const int64_t per = kScoreWaves * 64 / G;
+  return (unsigned)((T + per - 1) / per);
+}
+
 hipError_t launch_route_scored(const Geometry &g, const ep_route_rule_t &r, const void *logits,
                                bool bf16, const float *bias, int32_t *idx, float *w, float *scores,
                                hipStream_t s) {
   if (g.T == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)((g.T + kScoreWaves - 1) / kScoreWaves);
-#define L(P)                                                                                   \
-  hipLaunchKernelGGL((k_score_route<P>), dim3(blocks), dim3(64 * kScoreWaves), 0, s, logits,   \
-                     bf16 ? 1 : 0, bias, score_rule(r), g.T, g.E, g.k, idx, w, scores)
-  EP_PER_SWITCH(g.E, L);
+#define L1(LT, G, P)                                                                            \
+  hipLaunchKernelGGL((k_score_route<LT, G, P>), dim3(score_blocks(g.T, G)),                     \
+                     dim3(64 * kScoreWaves), 0, s, static_cast<const LT *>(logits), bias,       \
+                     score_rule(r), g.T, g.E, g.k, idx, w, scores)
+#define L(G, P)                   \
+  do {                            \
+    if (bf16) L1(uint16_t, G, P); \
+    else L1(float, G, P);         \
+  } while (0)
+  EP_SCORE_SWITCH(g.T, g.E, L);
 #undef L
+#undef L1
   return hipGetLastError();
 }
 
@@ -339,17 +530,19 @@ hipError_t launch_route_scored_bwd(const Geometry &g, const Workspace &ws,
                                    const int32_t *idx, const float *gw, const float *gs, void *gl,
                                    hipStream_t s) {
   if (g.T == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)((g.T + kScoreWaves - 1) / kScoreWaves);
   const bool dense = gs || (r.score == EP_SCORE_SOFTMAX && !r.renormalise);
-#define L1(D, P)                                                                                 \
-  hipLaunchKernelGGL((k_score_route_bwd<D, P>), dim3(blocks), dim3(64 * kScoreWaves), 0, s, logits, \
-                     bf16 ? 1 : 0, idx, gw, gs, score_rule(r), g.T, g.E, g.k, gl, ws.status)
-#define L(P)                \
-  do {                      \
-    if (dense) L1(true, P); \
-    else L1(false, P);      \
+#define L1(LT, D, G, P)                                                                          \
+  hipLaunchKernelGGL((k_score_route_bwd<LT, D, G, P>), dim3(score_blocks(g.T, G)),               \
+                     dim3(64 * kScoreWaves), 0, s, static_cast<const LT *>(logits), idx, gw, gs, \
+                     score_rule(r), g.T, g.E, g.k, static_cast<LT *>(gl), ws.status)
+#define L(G, P)                                \
+  do {                                         \
+    if (bf16 && dense) L1(uint16_t, true, G, P); \
+    else if (bf16) L1(uint16_t, false, G, P);  \
+    else if (dense) L1(float, true, G, P);     \
+    else L1(float, false, G, P);               \
   } while (0)
-  EP_PER_SWITCH(g.E, L);
+  EP_SCORE_SWITCH(g.T, g.E, L);
 #undef L
 #undef L1
   return hipGetLastError();

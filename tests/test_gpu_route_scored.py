@@ -45,7 +45,10 @@ def _rule(c):
 CASES = [dict(T=T, E=E, k=k, groups=g, kept=kept) for T, E, k, g, kept in [
     (1, 256, 8, 8, 4), (3, 8, 2, 1, 1), (129, 65, 3, 5, 2), (64, 60, 6, 10, 3), (50, 5, 7, 1, 1),
     (17, 1024, 16, 64, 33), (33, 1024, 16, 1, 1), (40, 384, 8, 8, 3), (257, 128, 8, 4, 4), (5, 1, 1, 1, 1),
-    (70, 64, 1, 64, 7), (31, 100, 16, 4, 1), (1500, 256, 8, 8, 4), (2049, 384, 6, 1, 1), (1025, 130, 4, 2, 1)]]
+    (70, 64, 1, 64, 7), (31, 100, 16, 4, 1), (1500, 256, 8, 8, 4), (2049, 384, 6, 1, 1), (1025, 130, 4, 2, 1),
+    (1030, 64, 8, 16, 5), (1100, 8, 2, 4, 2), (1201, 100, 8, 20, 7), (1301, 192, 16, 48, 9), (1026, 30, 3, 3, 2),
+    (1027, 1, 1, 1, 1), (2050, 100, 8, 20, 7), (2050, 96, 16, 48, 9), (4100, 192, 8, 6, 2), (2100, 8, 2, 4, 2),
+    (2100, 30, 3, 1, 1)]]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -123,7 +126,8 @@ def _bwd_bound(l, mag, bf16, ref):
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("with_scores", [True, False])
 @pytest.mark.parametrize("T,E,k,bf16", [(1, 256, 8, False), (300, 128, 8, True), (65, 65, 3, False),
-                                        (20, 1024, 16, True), (7, 5, 7, False), (4100, 60, 6, False)])
+                                        (20, 1024, 16, True), (7, 5, 7, False), (4100, 60, 6, False),
+                                        (1025, 256, 16, False), (2051, 128, 8, True), (1030, 17, 3, False)])
 def test_route_scored_bwd(score, renorm, with_scores, T, E, k, bf16):
     rng = np.random.default_rng(T + E + 2 * renorm + with_scores)
     l, lt = _logits(rng, T, E, bf16=bf16, masked=0.1)
