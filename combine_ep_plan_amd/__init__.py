@@ -121,6 +121,8 @@ class ep_handle_view_t(ctypes.Structure):
 
 
 _lib = None
+_marshal_call = None             # the C++ marshalling (csrc/marshal.cpp) and the addresses it calls
+_entry: dict[str, int] = {}
 _T = POINTER(ep_tensor_t)
 
 
@@ -131,14 +133,16 @@ def library_path() -> str:
 
 
 def load_library():
-    """Load libep_mi355x.so (raises if it has not been built)."""
-    global _lib
+    """Load libep_mi355x.so and the marshalling module (raises if they have
+    not been built)."""
+    global _lib, _marshal_call
     if _lib is not None:
         return _lib
     path = library_path()
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m combine_ep_plan_amd.build`"
-                           " (there is no fallback path)")
+    for f in (path, os.path.join(_HERE, "_marshal.so")):
+        if not os.path.exists(f):
+            raise RuntimeError(f"{f} is missing: build it with `python -m combine_ep_plan_amd.build`"
+                               " (there is no fallback path)")
     lib = ctypes.CDLL(path)
     S = c_int32
     sig = {
@@ -181,6 +185,9 @@ def load_library():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+        _entry[name] = ctypes.cast(fn, c_void_p).value
+    from . import _marshal
+    _marshal_call = _marshal.call
     _lib = lib
     return lib
 
@@ -195,13 +202,6 @@ _VIEWS_MAX = 4096
 _RECORDING = threading.local()   # prepare(): the calls being recorded and what they use
 _recorders = 0                   # threads inside prepare(): the thread-local is only asked if any
 _recorders_lock = threading.Lock()
-
-
-def _device(stream) -> int:
-    """The device a call runs on: its stream's, or the current one."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.device_index
-    return torch._C._cuda_getDevice()
 
 
 def _tensor(t: torch.Tensor | None, tag: int, dev: int | None = None):
@@ -254,6 +254,13 @@ def _stream(stream):
     return c_void_p(int(stream))
 
 
+def _hold(obj) -> None:
+    """A prepared call holds on to what it points to."""
+    keep = getattr(_RECORDING, "keep", None)
+    if keep is not None:
+        keep.append(obj)
+
+
 # Compute entry points only enqueue work, so a call is fully described by the
 # C function and its marshalled arguments.  prepare() records them once; its
 # result makes the same C calls again without marshalling anything in Python
@@ -268,7 +275,6 @@ def _enqueue(name: str, *args) -> None:
         calls = getattr(_RECORDING, "calls", None)
         if calls is not None:
             calls.append((fn, args, name))
-            _RECORDING.keep.extend(args)   # rules live as long as the recorded call
             return
     code = fn(*args)
     if code:
@@ -528,54 +534,85 @@ class RouteRule:
             _GROUP_SCORES[group_score] if isinstance(group_score, str) else int(group_score),
             int(renormalise), scale)
         self.ptr = ctypes.pointer(self.c)
+        self.addr = ctypes.addressof(self.c)
 
 
 _NORM_RULES: dict = {}
 
 
-def _norm_rule(eps: float, quant: str | int):
-    p = _NORM_RULES.get((eps, quant))
-    if p is None:
+def _norm_rule(eps: float, quant: str | int) -> int:
+    """Address of the ep_norm_rule_t of these values (kept for the process's life)."""
+    r = _NORM_RULES.get((eps, quant))
+    if r is None:
         q = _QUANTS[quant] if isinstance(quant, str) else int(quant)
-        if len(_NORM_RULES) >= _VIEWS_MAX:
-            _NORM_RULES.clear()
-        p = _NORM_RULES[(eps, quant)] = ctypes.pointer(ep_norm_rule_t(eps, q, 0))
-    return p
+        r = _NORM_RULES[(eps, quant)] = ep_norm_rule_t(eps, q, 0)
+    return ctypes.addressof(r)
+
+
+# Entry points that take pointers only are marshalled in C++ (csrc/marshal.cpp):
+# one byte per argument, a tensor's tag or 0xFF for an address.  Recorded calls
+# are described with the ctypes views above, which outlive the call.
+_ADDR = 0xFF
+
+
+def _call(name: str, tags: bytes, stream, *args) -> None:
+    if _marshal_call is None:
+        load_library()
+    if _recorders and getattr(_RECORDING, "calls", None) is not None:
+        dev = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
+        _enqueue(name, *(a if tag == _ADDR else _tensor(a, tag, dev) for a, tag in zip(args, tags)),
+                 _stream(stream))
+        return
+    if stream is not None:
+        stream = ((stream.device_index, stream.cuda_stream) if isinstance(stream, torch.cuda.Stream)
+                  else (torch.cuda.current_device(), int(stream)))
+    code = _marshal_call(_entry[name], tags, stream, *args)
+    if code:
+        raise EpError(code, name)
+
+
+_TAGS_ROUTE = bytes((_ADDR, _ADDR, TAG_ROUTER_LOGITS, TAG_ROUTER_BIAS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS,
+                     TAG_ROUTER_LOGITS))
+_TAGS_ROUTE_BWD = bytes((_ADDR, _ADDR, TAG_ROUTER_LOGITS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS,
+                         TAG_ROUTER_LOGITS, TAG_ROUTER_LOGITS))
+_TAGS_NORM_BWD = bytes((_ADDR, TAG_TOKENS, TAG_NORM_WEIGHT, TAG_TOKENS, TAG_TOKENS, TAG_TOKENS,
+                        TAG_NORM_WEIGHT, TAG_WORKSPACE))
+_TAGS_QUANTIZE = bytes((TAG_TOKENS, TAG_TOKENS, TAG_ROW_SCALES))
+_TAGS_GEMM_INT8 = bytes((_ADDR, TAG_TOKENS, TAG_ROW_SCALES, TAG_EXPERT_WEIGHTS, TAG_ROW_SCALES,
+                         TAG_EXPERT_WEIGHTS, TAG_ROW_SCALES, TAG_TOKENS))
+# with the scales of INT8 (True) or FP8 rows
+_TAGS_NORM = {i8: bytes((_ADDR, TAG_TOKENS, TAG_TOKENS, TAG_NORM_WEIGHT, TAG_TOKENS, TAG_TOKENS,
+                         TAG_TOKENS, TAG_ROW_SCALES if i8 else TAG_FP8_SCALES)) for i8 in (True, False)}
+_TAGS_DISPATCH = {i8: bytes((_ADDR, TAG_TOKENS, t, TAG_TOPK_WEIGHTS, TAG_TOKENS, t, TAG_TOPK_IDX,
+                             TAG_TOPK_WEIGHTS))
+                  for i8, t in ((True, TAG_ROW_SCALES), (False, TAG_FP8_SCALES))}
 
 
 def ep_route_scored(h: int, rule: RouteRule, logits: torch.Tensor, bias: torch.Tensor | None,
                     topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                     scores: torch.Tensor | None = None, stream=None) -> None:
-    d = _device(stream)
-    _enqueue("ep_route_scored", h, rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS, d),
-             _tensor(bias, TAG_ROUTER_BIAS, d), _tensor(topk_idx, TAG_TOPK_IDX, d),
-             _tensor(topk_weights, TAG_TOPK_WEIGHTS, d), _tensor(scores, TAG_ROUTER_LOGITS, d),
-             _stream(stream))
+    _call("ep_route_scored", _TAGS_ROUTE, stream, h, rule.addr, logits, bias, topk_idx, topk_weights,
+          scores)
+    if _recorders:
+        _hold(rule)
 
 
 def ep_route_scored_bwd(h: int, rule: RouteRule, logits: torch.Tensor, topk_idx: torch.Tensor,
                         grad_topk_weights: torch.Tensor, grad_scores: torch.Tensor | None,
                         grad_logits: torch.Tensor, stream=None) -> None:
-    d = _device(stream)
-    _enqueue("ep_route_scored_bwd", h, rule.ptr, _tensor(logits, TAG_ROUTER_LOGITS, d),
-             _tensor(topk_idx, TAG_TOPK_IDX, d), _tensor(grad_topk_weights, TAG_TOPK_WEIGHTS, d),
-             _tensor(grad_scores, TAG_ROUTER_LOGITS, d), _tensor(grad_logits, TAG_ROUTER_LOGITS, d),
-             _stream(stream))
-
-
-def _scale_tag(codes: torch.Tensor | None) -> int:
-    return TAG_ROW_SCALES if codes is not None and codes.dtype == torch.int8 else TAG_FP8_SCALES
+    _call("ep_route_scored_bwd", _TAGS_ROUTE_BWD, stream, h, rule.addr, logits, topk_idx,
+          grad_topk_weights, grad_scores, grad_logits)
+    if _recorders:
+        _hold(rule)
 
 
 def ep_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
                    residual_out: torch.Tensor | None, y: torch.Tensor | None,
                    codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                    eps: float = 1e-6, quant: str | int = "none", stream=None) -> None:
-    d = _device(stream)
-    _enqueue("ep_add_rmsnorm", _norm_rule(eps, quant), _tensor(x, TAG_TOKENS, d),
-             _tensor(residual, TAG_TOKENS, d), _tensor(weight, TAG_NORM_WEIGHT, d),
-             _tensor(residual_out, TAG_TOKENS, d), _tensor(y, TAG_TOKENS, d), _tensor(codes, TAG_TOKENS, d),
-             _tensor(scales, _scale_tag(codes), d), _stream(stream))
+    i8 = codes is not None and codes.dtype == torch.int8
+    _call("ep_add_rmsnorm", _TAGS_NORM[i8], stream, _norm_rule(eps, quant), x, residual, weight,
+          residual_out, y, codes, scales)
 
 
 def ep_add_rmsnorm_bwd_workspace_bytes(rows: int, hidden: int) -> int:
@@ -589,44 +626,29 @@ def ep_add_rmsnorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch
                        grad_residual_out: torch.Tensor | None, grad: torch.Tensor,
                        grad_weight: torch.Tensor | None, workspace: torch.Tensor | None,
                        eps: float = 1e-6, stream=None) -> None:
-    d = _device(stream)
-    _enqueue("ep_add_rmsnorm_bwd", _norm_rule(eps, QUANT_NONE), _tensor(hidden, TAG_TOKENS, d),
-             _tensor(weight, TAG_NORM_WEIGHT, d), _tensor(grad_y, TAG_TOKENS, d),
-             _tensor(grad_residual_out, TAG_TOKENS, d), _tensor(grad, TAG_TOKENS, d),
-             _tensor(grad_weight, TAG_NORM_WEIGHT, d), _tensor(workspace, TAG_WORKSPACE, d),
-             _stream(stream))
+    _call("ep_add_rmsnorm_bwd", _TAGS_NORM_BWD, stream, _norm_rule(eps, QUANT_NONE), hidden, weight,
+          grad_y, grad_residual_out, grad, grad_weight, workspace)
 
 
 def ep_quantize_int8(tokens: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                      stream=None) -> None:
-    d = _device(stream)
-    _enqueue("ep_quantize_int8", _tensor(tokens, TAG_TOKENS, d), _tensor(codes, TAG_TOKENS, d),
-             _tensor(scales, TAG_ROW_SCALES, d), _stream(stream))
+    _call("ep_quantize_int8", _TAGS_QUANTIZE, stream, tokens, codes, scales)
 
 
 def ep_dispatch_quantized(h: int, tokens: torch.Tensor, token_scales: torch.Tensor,
                           topk_weights: torch.Tensor | None, recv_tokens: torch.Tensor,
                           recv_scales: torch.Tensor, recv_topk_idx: torch.Tensor | None = None,
                           recv_topk_weights: torch.Tensor | None = None, stream=None) -> None:
-    d = _device(stream)
-    tag = _scale_tag(tokens)
-    _enqueue("ep_dispatch_quantized", h, _tensor(tokens, TAG_TOKENS, d),
-             _tensor(token_scales, tag, d), _tensor(topk_weights, TAG_TOPK_WEIGHTS, d),
-             _tensor(recv_tokens, TAG_TOKENS, d), _tensor(recv_scales, tag, d),
-             _tensor(recv_topk_idx, TAG_TOPK_IDX, d), _tensor(recv_topk_weights, TAG_TOPK_WEIGHTS, d),
-             _stream(stream))
+    _call("ep_dispatch_quantized", _TAGS_DISPATCH[tokens.dtype == torch.int8], stream, h, tokens,
+          token_scales, topk_weights, recv_tokens, recv_scales, recv_topk_idx, recv_topk_weights)
 
 
 def ep_expert_gemm_int8(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,
                         expert_weights: torch.Tensor, expert_scales: torch.Tensor,
                         slot_weights: torch.Tensor | None, slot_scales: torch.Tensor | None,
                         out: torch.Tensor, stream=None, swiglu: bool = False) -> None:
-    d = _device(stream)
-    name = "ep_expert_gemm_int8_swiglu" if swiglu else "ep_expert_gemm_int8"
-    _enqueue(name, h, _tensor(recv_tokens, TAG_TOKENS, d),
-             _tensor(recv_scales, TAG_ROW_SCALES, d), _tensor(expert_weights, TAG_EXPERT_WEIGHTS, d),
-             _tensor(expert_scales, TAG_ROW_SCALES, d), _tensor(slot_weights, TAG_EXPERT_WEIGHTS, d),
-             _tensor(slot_scales, TAG_ROW_SCALES, d), _tensor(out, TAG_TOKENS, d), _stream(stream))
+    _call("ep_expert_gemm_int8_swiglu" if swiglu else "ep_expert_gemm_int8", _TAGS_GEMM_INT8, stream,
+          h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights, slot_scales, out)
 
 
 def ep_expert_gemm_int8_swiglu(h: int, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,

@@ -1,5 +1,7 @@
 """Build libep_mi355x.so (HIP kernels for gfx950 + the C ABI) in the package
-directory with hipcc.  Usage: ``python -m combine_ep_plan_amd.build``.
+directory with hipcc, and _marshal.so (the binding's argument marshalling, host
+code against torch's headers) with g++.  Usage:
+``python -m combine_ep_plan_amd.build``.
 
 ``--host-sanitize`` builds libep_mi355x_hostsan.so instead: the kernels as
 usual, the host runtime (ep_api.cpp, host code only) compiled by g++ with
@@ -67,13 +69,39 @@ def _compile_host_sanitized(src: str) -> str:
     return obj
 
 
+OUT_MARSHAL = os.path.join(PKG, "_marshal.so")
+
+
+def _build_marshal() -> str:
+    """The Python extension module: no device code, so the host compiler alone."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = OUT_MARSHAL + ".tmp"
+    libs = cpp_extension.library_paths()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           *(f"-isystem{p}" for p in cpp_extension.include_paths()), f"-isystem{ROCM}/include",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "marshal.cpp"),
+           *(f"-L{p}" for p in libs), *(f"-Wl,-rpath,{p}" for p in libs),
+           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, OUT_MARSHAL)
+    return OUT_MARSHAL
+
+
 def build(verbose: bool = False, host_sanitize: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     device_srcs = [s for s in SOURCES if s.endswith(".hip")]
     host_srcs = [s for s in SOURCES if not s.endswith(".hip")]
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(_compile, device_srcs))
         objs += list(ex.map(_compile_host_sanitized if host_sanitize else _compile, host_srcs))
+        marshal.result()
     out = OUT_HOSTSAN if host_sanitize else OUT
     tmp = out + ".tmp"
     if host_sanitize:   # the sanitizer runtimes come from the host compiler's link

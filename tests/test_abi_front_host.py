@@ -7,6 +7,7 @@ from __future__ import annotations
 import ctypes
 
 import pytest
+import torch
 
 import combine_ep_plan_amd as ep
 from tests.test_abi_host import FAKE, create, lib  # noqa: F401  (lib: fixture)
@@ -234,3 +235,20 @@ def test_recorded_front_calls_check_like_their_entry_points(lib):  # noqa: F811
         for m, a in enumerate(args):
             c.p[m] = None if a is None else ctypes.cast(a, ctypes.c_void_p).value
         assert lib.ep_run_calls(ctypes.byref(c), 1, None) == want, op
+
+
+def test_marshalling_refuses_what_the_library_cannot_take(lib):  # noqa: F811
+    """The C++ marshalling: CPU tensors, non-tensors, a wrong number of
+    arguments -- Python errors, nothing called."""
+    fn = ep._entry["ep_quantize_int8"]
+    x, q, s = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(ValueError, match="on the GPU"):
+        ep._marshal_call(fn, ep._TAGS_QUANTIZE, (0, 0), x, q, s)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        ep._marshal_call(fn, ep._TAGS_QUANTIZE, (0, 0), 5, q, s)
+    with pytest.raises(TypeError, match="one tag"):
+        ep._marshal_call(fn, ep._TAGS_QUANTIZE, (0, 0), x, q)
+    with pytest.raises(TypeError, match="stream"):
+        ep._marshal_call(fn, ep._TAGS_QUANTIZE, 7, x, q, s)
+    # NULL arguments reach the entry point's own checks
+    assert ep._marshal_call(fn, ep._TAGS_QUANTIZE, (0, 0), None, None, None) == INVALID

@@ -251,3 +251,27 @@ def test_gemm_int8_silu_extremes():
     ref = front.swiglu(ref64)
     tol = (UB + (24 + 8 * np.abs(ref64[:, 0::2])) * U) * np.abs(ref) + 2.0 ** -133   # bf16's smallest step
     assert np.all(np.abs(host(out.float()).astype(np.float64) - ref) <= tol)
+
+
+def test_calls_refuse_tensors_they_cannot_take():
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty(8, 64, dtype=torch.int8, device="cuda"), torch.empty(8, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        ep.ep_quantize_int8(x[:, ::2], q[:, :32].contiguous(), s)
+    with pytest.raises(ValueError, match="on the GPU"):
+        ep.ep_quantize_int8(x, q, s.cpu())
+    with pytest.raises(TypeError, match="dtype"):
+        ep.ep_quantize_int8(x.half(), q, s)
+    with pytest.raises(ep.EpError, match="BAD_SHAPE"):
+        ep.ep_quantize_int8(x, q, s[:7])
+    with pytest.raises(ep.EpError, match="INVALID_ARG"):   # rows start at 16-byte boundaries
+        ep.ep_quantize_int8(x.view(-1)[4:4 + 7 * 64].view(7, 64), q[:7], s[:7])
+    # a stream by object and by address; recorded
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for st in (side, side.cuda_stream):
+        s.fill_(-1)
+        side.wait_stream(torch.cuda.current_stream())
+        ep.ep_quantize_int8(x, q, s, stream=st)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.all(s == 1)
