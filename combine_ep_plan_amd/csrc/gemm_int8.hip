@@ -402,18 +402,62 @@ __global__ __launch_bounds__(SPLIT ? 256 : 64) void k_grouped_gemm_i8_stream(
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles (large groups): waves, LDS geometry and pipeline of the
-// power-of-two FP8 kernel (gemm.hip, k_grouped_gemm_fp8_256) -- 4 x 4
-// accumulators of 32 x 32 a wave, 128-byte slabs straight from global memory
-// into two LDS buffers, the slab after next issued as soon as its buffer is
-// free -- with two 32-deep v_mfma_i32_32x32x32_i8 in place of each 64-deep FP8
-// step and no scales in the loop.
+// 256 x 256 tiles (large groups): four waves in 2 x 2, each 4 x 4 accumulators
+// of 32 x 32 in the 256 accumulation registers; 128-byte slabs straight from
+// global memory into LDS, rows of X in two buffers and of W in three (all 160
+// KB).  A slab's two halves are multiplied one after the other; the one barrier
+// a slab stands between them, where the slab's last fragments are in
+// registers.  It publishes the next slab and frees this one's buffers, whose
+// loads (X two slabs ahead, W, which misses the L2 more often, three) then go
+// out under the second half's MFMAs.  Row tiles of at most kShortRows rows are
+// streamed instead (above).
 
 // A lane's fragments of half a slab: chunks 2s + lane / 32 of its row, s = 0, 1
 // (within the half).
 struct Frag2 {
   i32x4 s0, s1;
 };
+
+// Work of workgroup blockIdx.x.  Its XCD's work comes in chunks of 16
+// workgroups: a block of 4 full row tiles by 4 column tiles, which run at about
+// the same time on the XCD's compute units and share their row and weight slabs
+// in its L2, or 16 column tiles of short row tiles, which stream weights; the two
+// kinds merged in proportion, XCD x taking the blocks and the short tiles x, x +
+// 8, ...  Against every XCD walking one row tile's column tiles at a time:
+// 1010 -> 972 us on even groups (4096 tokens, 16 experts, top-8, K = 7168, N =
+// 4096), 1711 -> 1663 us on the skewed prefill batch; other block shapes and
+// chunk sizes (1 x 16 to 4 x 8, 8 to 64) fell between.
+constexpr int kBlock = 4, kChunk = kBlock * kBlock;
+__device__ __forceinline__ bool blocked_tile(const int32_t *__restrict__ ntiles, int32_t max_tiles,
+                                             int32_t n_col_tiles, int32_t &tile, int32_t &col) {
+  const int32_t nf = ntiles[1], ns = ntiles[0] - nf;
+  const int32_t x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+  const int32_t cg = (n_col_tiles + kBlock - 1) / kBlock;
+  const int32_t nb = (nf + kBlock - 1) / kBlock * cg;
+  const int32_t fx = x < nb ? (nb - x + kXcds - 1) / kXcds : 0;   // this XCD's blocks ...
+  const int32_t sx = x < ns ? (ns - x + kXcds - 1) / kXcds : 0;   // ... and short tiles
+  const int32_t n = fx + (sx * n_col_tiles + kChunk - 1) / kChunk;
+  const int32_t p = slot / kChunk, i = slot % kChunk;
+  if (p >= n) return false;
+  const int32_t f = (int32_t)((int64_t)p * fx / n);
+  if ((int32_t)((int64_t)(p + 1) * fx / n) > f) {
+    const int32_t b = x + kXcds * f;
+    tile = b / cg * kBlock + i % kBlock;
+    col = b % cg * kBlock + i / kBlock;
+    return tile < nf && col < n_col_tiles;
+  }
+  const int32_t q = (p - f) * kChunk + i, t = q / n_col_tiles;
+  tile = max_tiles - 1 - (x + kXcds * t);
+  col = q - t * n_col_tiles;
+  return t < sx;
+}
+// Workgroups that cover it for any split of max_tiles row tiles into kinds: per
+// XCD an eighth of the blocks, rounded up, and of the short tiles' chunks.
+static int64_t blocked_grid(int32_t max_tiles, int64_t ncol) {
+  const int64_t blocks = ((int64_t)max_tiles / kBlock + 1) * ((ncol + kBlock - 1) / kBlock);
+  const int64_t chunks = (((int64_t)max_tiles / kXcds + 1) * ncol + kChunk - 1) / kChunk;
+  return kXcds * kChunk * (blocks / kXcds + 1 + chunks);
+}
 
 template <int I, int NB>
 __device__ __forceinline__ void mfma_i8_rows(i32x16 (&acc)[kFM2][kFN2], const Frag2 (&fa)[kFM2],
@@ -436,14 +480,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
     const float *__restrict__ SWslot, const int32_t *__restrict__ tiles,
     const int32_t *__restrict__ ntiles, int32_t max_tiles, int32_t K, int32_t N, int32_t E,
     int32_t n_col_tiles, uint16_t *__restrict__ Y) {
-  // two slabs of X and W (128 KB), later the bf16 output tile; the row scales
-  __shared__ u32x4 lds[2 * kSlabA2 + 2 * kSlabB2];
-  __shared__ float ssx[kBM2];
-  static_assert(kBM2 * kBN2 * 2 <= (int)sizeof(lds), "output tile fits the slab buffers");
+  // two slabs of X and three of W; later the bf16 output tile and the row scales
+  __shared__ u32x4 lds[2 * kSlabA2 + 3 * kSlabB2];
+  static_assert(kBM2 * kBN2 * 2 + kBM2 * 4 <= (int)sizeof(lds), "output tile and scales fit the buffers");
   static_assert(kBM2 == kGemmThreads, "one row scale per thread");
   u32x4 *const sa = lds, *const sb = lds + 2 * kSlabA2;
   int32_t tile, ctile;
-  if (!balanced_tile(ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
+  if (!blocked_tile(ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
   const int32_t n0 = ctile * kBN2;
   const int32_t row0 = tiles[tile * 4 + 0], rows = tiles[tile * 4 + 1], widx = tiles[tile * 4 + 2];
   const int32_t KV = K / 16;
@@ -453,10 +496,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
   const float *SWt = (own ? SW : SWslot) + wsel * N + n0;
   // every offset is in range by construction: rows past the end read the last
   // row, and 256 rows of K <= 131071 bytes span less than 2^31
-  const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(X + (int64_t)row0 * KV), (short)0, rows * K, kBufDword3);
-  const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)((own ? W : Wslot) + (wsel * N + n0) * KV), (short)0, wrows * K, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rX = uniform_rsrc(X + (int64_t)row0 * KV, rows * K);
+  const __amdgpu_buffer_rsrc_t rW = uniform_rsrc((own ? W : Wslot) + (wsel * N + n0) * KV, wrows * K);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
@@ -465,13 +506,12 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
     const StreamTile t = stream_tile<GLU>(X, SX, (own ? W : Wslot) + wsel * N * KV,
                                           (own ? SW : SWslot) + wsel * N, Y, row0, rows,
                                           n0 + wv * kStreamCols, N, K);
-    constexpr int kRing = (2 * kSlabA2 + 2 * kSlabB2) / 4;   // a wave's quarter of LDS
-    static_assert(stream_slots(1, 3) <= kRing && stream_slots(4, 2) <= kRing && stream_slots(8, 2) <= kRing, "");
-    stream_all<GLU, 3, 2, 2, false>(t, wv, lane, lds + wv * kRing, nullptr);
+    constexpr int kRing = (2 * kSlabA2 + 3 * kSlabB2) / 4;   // a wave's quarter of LDS
+    static_assert(kStreamSlots <= kRing, "one wave's ring");
+    stream_all<GLU, kStreamD1, kStreamD4, kStreamD8, false>(t, wv, lane, lds + wv * kRing, nullptr);
     return;
   }
   const int wm = wv >> 1, wn = wv & 1;
-  ssx[tid] = SX[row0 + (tid < rows ? tid : rows - 1)];
   // load i of wave wv fills the 64 slots i*256 + wv*64 + lane, slot q holding
   // chunk (q % 8) ^ ((r / 2) % 8) of LDS row r = q / 8
   uint32_t oa[kLoads2], ob[kLoadsB2];
@@ -490,28 +530,29 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
   const bool half = K % kI8Slab != 0;  // the last slab: only its upper half is new (see k_grouped_gemm_i8)
   const int last = K > kI8Slab ? K - kI8Slab : 0;
 #define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
-#define I8W_ISSUE(kt, buf)                                                                     \
-  {                                                                                            \
-    const int so_ = (kt) + 1 < KT ? (kt) * kI8Slab : last;                                     \
-    _Pragma("unroll") for (int i = 0; i < kLoads2; ++i) lds_load16(                            \
-        rX, LDS_ADDR(&sa[(buf) * kSlabA2 + i * kGemmThreads + wv * 64]), oa[i], so_);          \
-    _Pragma("unroll") for (int i = 0; i < kLoadsB2; ++i) lds_load16(                           \
-        rW, LDS_ADDR(&sb[(buf) * kSlabB2 + i * kGemmThreads + wv * 64]), ob[i], so_);          \
-  }
-  static_assert(kLoads2 + kLoadsB2 == 16, "the waits below count 16 loads per slab");
+#define I8W_OFF(kt) ((kt) + 1 < KT ? (kt) * kI8Slab : last)
+#define I8W_LOAD_X(i, kt, buf)                                                                 \
+  lds_load16(rX, LDS_ADDR(&sa[(buf) * kSlabA2 + (i) * kGemmThreads + wv * 64]), oa[i], I8W_OFF(kt));
+#define I8W_LOAD_W(i, kt, buf)                                                                 \
+  lds_load16(rW, LDS_ADDR(&sb[(buf) * kSlabB2 + (i) * kGemmThreads + wv * 64]), ob[i], I8W_OFF(kt));
+#define I8W_ISSUE_X(kt, buf)                                                                   \
+  _Pragma("unroll") for (int i = 0; i < kLoads2; ++i) I8W_LOAD_X(i, kt, buf)
+#define I8W_ISSUE_W(kt, buf)                                                                   \
+  _Pragma("unroll") for (int i = 0; i < kLoadsB2; ++i) I8W_LOAD_W(i, kt, buf)
+  static_assert(kLoads2 == 8 && kLoadsB2 == 8, "the waits below count 8 loads of X and 8 of W per slab");
 // half h (0 or 1) of a slab: chunks h*4 + lane/32 and h*4 + 2 + lane/32 of the lane's row
-#define READ8(FA, FB, buf, h, NBK)                                                             \
+#define READ8(FA, FB, bufa, bufb, h, NBK)                                                             \
   {                                                                                            \
     const int c_ = (h) * 4 + (lane >> 5);                                                      \
     _Pragma("unroll") for (int i = 0; i < (NBK); ++i) {                                        \
       const int r_ = wm * kWTM2 + i * 32 + (lane & 31);                                        \
-      FA[i].s0 = __builtin_bit_cast(i32x4, sa[(buf) * kSlabA2 + swz(r_, c_)]);                 \
-      FA[i].s1 = __builtin_bit_cast(i32x4, sa[(buf) * kSlabA2 + swz(r_, c_ + 2)]);             \
+      FA[i].s0 = __builtin_bit_cast(i32x4, sa[(bufa) * kSlabA2 + swz(r_, c_)]);                 \
+      FA[i].s1 = __builtin_bit_cast(i32x4, sa[(bufa) * kSlabA2 + swz(r_, c_ + 2)]);             \
     }                                                                                          \
     _Pragma("unroll") for (int j = 0; j < kFN2; ++j) {                                         \
       const int r_ = wn * kWTN2 + j * 32 + (lane & 31);                                        \
-      FB[j].s0 = __builtin_bit_cast(i32x4, sb[(buf) * kSlabB2 + swz(r_, c_)]);                 \
-      FB[j].s1 = __builtin_bit_cast(i32x4, sb[(buf) * kSlabB2 + swz(r_, c_ + 2)]);             \
+      FB[j].s0 = __builtin_bit_cast(i32x4, sb[(bufb) * kSlabB2 + swz(r_, c_)]);                 \
+      FB[j].s1 = __builtin_bit_cast(i32x4, sb[(bufb) * kSlabB2 + swz(r_, c_ + 2)]);             \
     }                                                                                          \
   }
 
@@ -535,10 +576,18 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
                   "a"(acc[3][0][0]), "a"(acc[3][1][0]), "a"(acc[3][2][0]), "a"(acc[3][3][0])   \
                : "memory")
   static_assert(kFM2 == 4 && kFN2 == 4, "the barrier names each of the 16 accumulators");
-  I8W_ISSUE(0, 0);
+  // the order of issue is the order the waits count: X0 W0 W1 X1 W2, then X W a slab
+  I8W_ISSUE_X(0, 0);
+  I8W_ISSUE_W(0, 0);
   if (KT > 1) {
-    I8W_ISSUE(1, 1);
-    I8W_SYNC(16);   // slab 0 landed
+    I8W_ISSUE_W(1, 1);
+    I8W_ISSUE_X(1, 1);
+  }
+  if (KT > 2) {
+    I8W_ISSUE_W(2, 2);
+    I8W_SYNC(24);   // slab 0 landed
+  } else if (KT > 1) {
+    I8W_SYNC(16);
   } else {
     I8W_SYNC(0);
   }
@@ -548,29 +597,69 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
   if constexpr ((NBK) == kFM2) {                                                               \
     _Pragma("unroll") for (int q_ = 0; q_ < 16; ++q_) { SGB8(0x008, 2); SGB8(0x100, 1); }      \
   }
-#define I8W_SLAB(NBK, ISSUE)                                                                   \
+// The second half of a slab: X of slab kt + 2 and W of slab kt + 3 go out.  A
+// load occupies the address path for 16 cycles and a wave issues in order: all
+// 16 at once would leave the matrix cores idle behind them, so one goes
+// between every two MFMAs, with one LDS read (the chunks pinned by
+// sched_barrier).
+#define I8W_STEP(q_)                                                                           \
   {                                                                                            \
-    const int buf = kt & 1;                                                                    \
-    READ8(fa1, fb1, buf, 1, NBK);                                                              \
+    constexpr int i_ = (q_) / 4, s_ = ((q_) / 2) & 1, j_ = ((q_) & 1) * 2;                     \
+    acc[i_][j_] = __builtin_amdgcn_mfma_i32_32x32x32_i8(                                       \
+        s_ ? fa1[i_].s1 : fa1[i_].s0, s_ ? fb1[j_].s1 : fb1[j_].s0, acc[i_][j_], 0, 0, 0);     \
+    acc[i_][j_ + 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(                                   \
+        s_ ? fa1[i_].s1 : fa1[i_].s0, s_ ? fb1[j_ + 1].s1 : fb1[j_ + 1].s0, acc[i_][j_ + 1],   \
+        0, 0, 0);                                                                              \
+    /* reads: column fragments first, then the rows' */                                        \
+    constexpr int f_ = ((q_) & 7) / 2, h_ = (q_) & 1;                                          \
+    const int c_ = (lane >> 5) + 2 * h_;                                                       \
+    if constexpr ((q_) < 8) {                                                                  \
+      const i32x4 v_ = __builtin_bit_cast(                                                     \
+          i32x4, sb[nb * kSlabB2 + swz(wn * kWTN2 + f_ * 32 + (lane & 31), c_)]);              \
+      if constexpr (h_ == 0) fb0[f_].s0 = v_; else fb0[f_].s1 = v_;                            \
+      I8W_LOAD_X((q_) & 7, kt + 2, ba)                                                         \
+    } else {                                                                                   \
+      const i32x4 v_ = __builtin_bit_cast(                                                     \
+          i32x4, sa[(ba ^ 1) * kSlabA2 + swz(wm * kWTM2 + f_ * 32 + (lane & 31), c_)]);        \
+      if constexpr (h_ == 0) fa0[f_].s0 = v_; else fa0[f_].s1 = v_;                            \
+      I8W_LOAD_W((q_) & 7, kt + 3, bb)                                                         \
+    }                                                                                          \
+    __builtin_amdgcn_sched_barrier(0);                                                         \
+  }
+// slab kt is in buffers ba of X and bb of W, slab kt + 1 in ba ^ 1 and nb; VM: the
+// loads that may still be on their way when slab kt + 1 is published
+#define I8W_SLAB(NBK, DX, DW, VM)                                                              \
+  {                                                                                            \
+    const int nb = bb == 2 ? 0 : bb + 1;                                                       \
+    READ8(fa1, fb1, ba, bb, 1, NBK);                                                           \
     mfma_i8_rows<0, NBK>(acc, fa0, fb0);                                                       \
     I8W_INTERLEAVE(NBK);                                                                       \
-    I8W_SYNC(0);                                                                               \
+    I8W_SYNC(VM);                                                                              \
     __builtin_amdgcn_sched_barrier(0);                                                         \
-    if (ISSUE) I8W_ISSUE(kt + 2, buf);                                                         \
-    READ8(fa0, fb0, buf ^ 1, 0, NBK);                                                          \
-    mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                       \
-    I8W_INTERLEAVE(NBK);                                                                       \
+    if constexpr ((DX) && (DW) && (NBK) == kFM2) {                                             \
+      I8W_STEP(0) I8W_STEP(1) I8W_STEP(2) I8W_STEP(3) I8W_STEP(4) I8W_STEP(5) I8W_STEP(6)      \
+      I8W_STEP(7) I8W_STEP(8) I8W_STEP(9) I8W_STEP(10) I8W_STEP(11) I8W_STEP(12) I8W_STEP(13)  \
+      I8W_STEP(14) I8W_STEP(15)                                                                \
+    } else {                                                                                   \
+      if (DX) { I8W_ISSUE_X(kt + 2, ba); }                                                     \
+      if (DW) { I8W_ISSUE_W(kt + 3, bb); }                                                     \
+      READ8(fa0, fb0, ba ^ 1, nb, 0, NBK);                                                     \
+      mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                     \
+      I8W_INTERLEAVE(NBK);                                                                     \
+    }                                                                                          \
+    ba ^= 1;                                                                                   \
+    bb = nb;                                                                                   \
+    ++kt;                                                                                      \
   }
+// (the last three slabs peeled: fewer loads are on their way)
 #define I8W_LOOP(NBK)                                                                          \
   {                                                                                            \
-    READ8(fa0, fb0, 0, 0, NBK);                                                                \
-    int kt = 0;                                                                                \
-    for (; kt + 2 < KT; ++kt) I8W_SLAB(NBK, true)                                              \
-    if (kt + 1 < KT) {                                                                         \
-      I8W_SLAB(NBK, false)                                                                     \
-      ++kt;                                                                                    \
-    }                                                                                          \
-    READ8(fa1, fb1, kt & 1, 1, NBK);                                                           \
+    int kt = 0, ba = 0, bb = 0;                                                                \
+    READ8(fa0, fb0, 0, 0, 0, NBK);                                                             \
+    while (kt + 3 < KT) I8W_SLAB(NBK, true, true, 8)                                           \
+    if (kt + 2 < KT) I8W_SLAB(NBK, true, false, 8)                                             \
+    if (kt + 1 < KT) I8W_SLAB(NBK, false, false, 0)                                            \
+    READ8(fa1, fb1, ba, bb, 1, NBK);                                                           \
     if (!half) mfma_i8_rows<0, NBK>(acc, fa0, fb0);                                            \
     mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                       \
   }
@@ -582,11 +671,16 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
   else I8W_LOOP(0)
 #undef I8W_LOOP
 #undef I8W_SLAB
+#undef I8W_STEP
 #undef I8W_INTERLEAVE
 #undef SGB8
 #undef I8W_SYNC
 #undef READ8
-#undef I8W_ISSUE
+#undef I8W_ISSUE_X
+#undef I8W_ISSUE_W
+#undef I8W_LOAD_X
+#undef I8W_LOAD_W
+#undef I8W_OFF
 #undef LDS_ADDR
 
   float sw[kFN2];
@@ -604,7 +698,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
   const bool vec = (NO & 7) == 0;
   const int32_t c0 = GLU ? n0 / 2 : n0;
   uint16_t *so = reinterpret_cast<uint16_t *>(lds);
+  float *const ssx = reinterpret_cast<float *>(lds + kBM2 * kBN2 * 2 / 16);
   __syncthreads();   // every wave is done with the slab buffers
+  ssx[tid] = SX[row0 + (tid < rows ? tid : rows - 1)];
+  __syncthreads();
 #define OSW(r_, cv_) ((r_) * TN + (((cv_) ^ ((((r_) >> 2) & 3) << 2)) << 3))
 #pragma unroll
   for (int i = 0; i < kFM2; ++i)
@@ -656,7 +753,9 @@ static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
 bool gemm_int8_fits(const Geometry &g, int32_t K, int32_t N) {
   // blocks * threads of a launch stay below 2^32, whichever the tiles
   const int64_t ncol = ((int64_t)N + kStreamCols - 1) / kStreamCols;
-  return K <= kI8MaxK && gemm_grid_blocks(gemm_max_tiles(g), 1) * ncol <= UINT32_MAX / kGemmThreads;
+  const int64_t most = UINT32_MAX / kGemmThreads;
+  return K <= kI8MaxK && gemm_grid_blocks(gemm_max_tiles(g), 1) * ncol <= most &&
+         blocked_grid(wide_max_tiles(g), ((int64_t)N + kBN2 - 1) / kBN2) <= most;
 }
 
 hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, const uint8_t *x,
@@ -672,7 +771,9 @@ hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, cons
 #define I8_LAUNCH(KERN, COLS, THREADS)                                                         \
   do {                                                                                         \
     const int32_t ncol = (N + (COLS)-1) / (COLS);                                              \
-    hipLaunchKernelGGL(KERN, dim3((unsigned)gemm_grid_blocks(max_tiles, ncol)), dim3(THREADS), 0, s, \
+    const int64_t blocks = kind == I8Kernel::kWide ? blocked_grid(max_tiles, ncol)             \
+                                                   : gemm_grid_blocks(max_tiles, ncol);        \
+    hipLaunchKernelGGL(KERN, dim3((unsigned)blocks), dim3(THREADS), 0, s,                      \
                        reinterpret_cast<const u32x4 *>(x), sx, reinterpret_cast<const u32x4 *>(w), sw, \
                        reinterpret_cast<const u32x4 *>(wslot), swslot, ws.gemm_tiles,          \
                        ws.gemm_ntiles, max_tiles, K, N, g.E, ncol, y);                         \

@@ -218,12 +218,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_add_rmsnorm(NormArgs a) {
       unpack_raw(rr[i], r);
 #pragma unroll
       for (int c = 0; c < 8; ++c) h[c] += r[c];
+      // the stream is next read behind the whole MoE layer: its rows leave no
+      // lines behind (prefill 4096 x 7168, FP8: 49.5 us against 54)
       if constexpr (sizeof(RT) == 2) {
         const u32x4 b = pack8(h);
-        static_cast<u32x4 *>(a.hidden)[base + v] = b;
+        store_stream(static_cast<u32x4 *>(a.hidden) + base + v, b);
         unpack8(b, h);
       } else {
-        store8<RT>(a.hidden, base + v, h);
+        f32x4 *o = static_cast<f32x4 *>(a.hidden) + 2 * (base + v);
+        store_stream(o, f32x4{h[0], h[1], h[2], h[3]});
+        store_stream(o + 1, f32x4{h[4], h[5], h[6], h[7]});
       }
     }
 #pragma unroll
@@ -427,6 +431,8 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
         o[c] = rstd * (g[i][c] * w[i][c] - n * mean) + r[i][c];
         dw[i][c] += g[i][c] * n;
       }
+      // cached: the next backward reads it (a chain of these calls on 16384 x
+      // 4096 takes 85 us a call, 95 with streaming stores)
       store8<RT>(a.gx, base + v, o);
     }
   }
