@@ -64,41 +64,6 @@ namespace epk {
 // ---------------------------------------------------------------------------
 // tile table
 
-struct TileArgs {
-  Geometry g;
-  Workspace ws;
-  int32_t use_slots;  // STATIC segments with a slot read weights from the slot
-};
-
-// Group q of the current plan: first receive row, rows, weight index
-// (< E: owner expert; E + r*S + s: slot s of rank r).
-__device__ __forceinline__ void group_of(const TileArgs &a, int32_t q, int32_t &row0,
-                                         int32_t &rows, int32_t &widx) {
-  const Geometry &g = a.g;
-  const Workspace &ws = a.ws;
-  if (g.layout == kHT) {
-    row0 = ws.offsets[q];
-    rows = ws.offsets[q + 1] - row0;
-    widx = q;
-  } else if (g.layout == kLL) {
-    const int32_t c = ws.counts[q];
-    row0 = q * g.cap;
-    rows = c < g.cap ? c : g.cap;
-    widx = q;
-  } else if (q < g.E) {  // kept rows of expert q on its home rank
-    const int32_t m = g.E / g.R;
-    row0 = (q / m) * g.C + ws.native_row[q];
-    rows = ws.keep[q];
-    widx = q;
-  } else {  // segment q - E on its receiving rank
-    const int32_t *s = ws.segments + (int64_t)(q - g.E) * 5;
-    const int32_t slot = ws.seg_slot[q - g.E];
-    row0 = s[1] * g.C + s[4];
-    rows = s[3];
-    widx = (a.use_slots && slot >= 0) ? g.E + s[1] * g.S + slot : s[0];
-  }
-}
-
 // PART: row tiles come in two kinds, full ones (more than short_rows rows), whose
 // time is MFMA work, and short ones (a group's tail or a small group), whose
 // time is streaming their weight slice.  The table then holds the full tiles
@@ -1178,7 +1143,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_fp8_256(
 
 // Row tiles of kTileM rows the plan can produce; the 256-row tiling needs no more.
 int32_t gemm_max_tiles(const Geometry &g) {
-  const int64_t groups = g.layout == kStatic ? 2 * (int64_t)g.E + g.R : g.E;
+  const int64_t groups = gemm_groups(g);
   return (int32_t)((g.n + kTileM - 1) / kTileM + groups);
 }
 

@@ -33,6 +33,42 @@ constexpr int kLoadsB2 = kBN2 * kChunks / kGemmThreads;   // ... and of W
 constexpr int kSlabA2 = kBM2 * kChunks, kSlabB2 = kBN2 * kChunks;
 constexpr int kBufDword3 = 0x00020000;                    // buffer resource word 3 (raw, 32-bit data)
 
+// What a kernel reads of the current plan's groups.
+struct TileArgs {
+  Geometry g;
+  Workspace ws;
+  int32_t use_slots;  // STATIC segments with a slot read weights from the slot
+};
+
+// Group q of the current plan: first receive row, rows, weight index
+// (< E: owner expert; E + r*S + s: slot s of rank r).
+__device__ __forceinline__ void group_of(const TileArgs &a, int32_t q, int32_t &row0,
+                                         int32_t &rows, int32_t &widx) {
+  const Geometry &g = a.g;
+  const Workspace &ws = a.ws;
+  if (g.layout == kHT) {
+    row0 = ws.offsets[q];
+    rows = ws.offsets[q + 1] - row0;
+    widx = q;
+  } else if (g.layout == kLL) {
+    const int32_t c = ws.counts[q];
+    row0 = q * g.cap;
+    rows = c < g.cap ? c : g.cap;
+    widx = q;
+  } else if (q < g.E) {  // kept rows of expert q on its home rank
+    const int32_t m = g.E / g.R;
+    row0 = (q / m) * g.C + ws.native_row[q];
+    rows = ws.keep[q];
+    widx = q;
+  } else {  // segment q - E on its receiving rank
+    const int32_t *s = ws.segments + (int64_t)(q - g.E) * 5;
+    const int32_t slot = ws.seg_slot[q - g.E];
+    row0 = s[1] * g.C + s[4];
+    rows = s[3];
+    widx = (a.use_slots && slot >= 0) ? g.E + s[1] * g.S + slot : s[0];
+  }
+}
+
 // Work of workgroup blockIdx.x: its row tile (an index into the table) and
 // column tile.  Workgroup b runs on XCD b % 8; XCD x takes full tiles x,
 // x + 8, x + 16, ... and short tiles x, x + 8, ..., each in group order,
@@ -97,9 +133,14 @@ inline int64_t gemm_grid_blocks(int32_t max_tiles, int32_t ncol) {
   return (int64_t)kXcds * (max_tiles / kXcds + 2) * ncol;
 }
 
+// Groups a plan can have (those of the current one are counted on the device).
+inline int64_t gemm_groups(const Geometry &g) {
+  return g.layout == kStatic ? 2 * (int64_t)g.E + g.R : g.E;
+}
+
 // At most as many 256-row tiles as the table holds 128-row ones.
 inline int32_t wide_max_tiles(const Geometry &g) {
-  const int64_t groups = g.layout == kStatic ? 2 * (int64_t)g.E + g.R : g.E;
+  const int64_t groups = gemm_groups(g);
   return (int32_t)((g.n + kBM2 - 1) / kBM2 + groups);
 }
 

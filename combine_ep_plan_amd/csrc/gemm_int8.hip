@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_grouped_gemm_i8(
 // bytes a lane) the same bytes take four times the address slots and the
 // kernel stops at 6.1 TB/s of weights.  The weights are loaded non-temporally:
 // plain loads of them stop at 6.2 TB/s on this card, non-temporal ones at 7.1.
-// Decode (1024 rows, 256 experts, K = 7168, N = 2048): 582 us, 6.5 TB/s.
+// Decode (1024 rows, 256 experts, K = 7168, N = 2048): 560 us, 6.6 TB/s.
 // SPLIT: the four waves of a workgroup share 64 columns and take a quarter of K
 // each, so that a batch of few experts still fills the GPU; their integer
 // partial sums are joined through LDS, exactly.
@@ -220,7 +220,7 @@ __device__ __forceinline__ StreamTile stream_tile(const u32x4 *X, const float *S
   t.NO = NO;
   t.cols = GLU ? t.wrows / 2 : t.wrows;
   // every offset is in range by construction (rows past the end read the last
-  // row); 128 rows of K <= 131071 bytes span less than 2^31
+  // row); the rows span less than 2^31 bytes
   t.rX = uniform_rsrc(X + (int64_t)row0 * KV, rows * K);
   t.rW = uniform_rsrc(Wm + (int64_t)n0 * KV, t.wrows * K);
   t.SX = SX + row0;
@@ -232,7 +232,7 @@ __device__ __forceinline__ StreamTile stream_tile(const u32x4 *X, const float *S
 // 16-byte slots of a wave's ring: D slabs of 64 weight rows and 8 NX token rows.
 constexpr int stream_slots(int NX, int D) { return D * (kStreamCols + 8 * NX) * kChunks; }
 
-// Rows [m0, m0 + 8 NX) of the tile, NX in 1, 2, 4, 8; ring: the wave's
+// Rows [m0, m0 + 8 NX) of the tile, NX 1, 2, 4 or 8; ring: the wave's
 // stream_slots(NX, D).
 template <bool GLU, int NX, int D, bool SPLIT>
 __device__ __forceinline__ void stream_rows(const StreamTile &t, int32_t m0, int wv, int lane,
@@ -361,35 +361,67 @@ __device__ __forceinline__ void stream_rows(const StreamTile &t, int32_t m0, int
   if constexpr (SPLIT) __syncthreads();   // before the next rows' loads land in the rings
 }
 
-// All rows of a tile, in passes of 64 over its weights (one, unless a busier
-// expert stands among few rows); the smallest ring row count that holds them.
-template <bool GLU, int D1, int D4, int D8, bool SPLIT>
-__device__ __forceinline__ void stream_all(const StreamTile &t, int wv, int lane, u32x4 *ring,
-                                           int32_t *part) {
-  int32_t m0 = 0;
-  for (; m0 + 32 < t.rows; m0 += 64) stream_rows<GLU, 8, D8, SPLIT>(t, m0, wv, lane, ring, part);
-  const int32_t left = t.rows - m0;
-  if (left > 8) stream_rows<GLU, 4, D4, SPLIT>(t, m0, wv, lane, ring, part);
-  else if (left > 0) stream_rows<GLU, 1, D1, SPLIT>(t, m0, wv, lane, ring, part);
+// Slabs in the ring by its token rows (8, 16, 32, 64).  A wave by itself idles
+// when its slab is late and while it starts and ends, so more waves a compute
+// unit beat deeper rings: kRingFew, 20 KB, eight waves (1024 rows on 256
+// experts, K = 7168, N = 2048: 563 us against 602 with 36 KB rings of four
+// slabs); kRingMore, 24 KB, six waves, where groups have some 16 rows or more.
+// kRingWide: a wave's quarter of the 256 x 256 kernel's LDS.
+struct RingDepth {
+  int d1, d2, d4, d8;
+};
+constexpr RingDepth kRingFew = {2, 2, 1, 1}, kRingMore = {2, 2, 2, 1}, kRingWide = {4, 4, 3, 2};
+constexpr int max_i(int a, int b) { return a > b ? a : b; }
+constexpr int ring_slots(RingDepth d) {
+  return max_i(max_i(stream_slots(1, d.d1), stream_slots(2, d.d2)),
+               max_i(stream_slots(4, d.d4), stream_slots(8, d.d8)));
+}
+template <bool FEW, bool WIDE>
+constexpr RingDepth ring_depth() {
+  return WIDE ? kRingWide : FEW ? kRingFew : kRingMore;
 }
 
-constexpr int kStreamD1 = 4, kStreamD4 = 3, kStreamD8 = 2;
-constexpr int kStreamSlots = stream_slots(1, kStreamD1);
-static_assert(stream_slots(4, kStreamD4) <= kStreamSlots && stream_slots(8, kStreamD8) <= kStreamSlots,
-              "one wave's ring");
+// All rows of a tile, in passes of 64 over its weights (one, unless a busier
+// expert stands among few rows); the smallest ring row count that holds them.
+template <bool GLU, bool FEW, bool WIDE, bool SPLIT>
+__device__ __forceinline__ void stream_all(const StreamTile &t, int wv, int lane, u32x4 *ring,
+                                           int32_t *part) {
+  constexpr RingDepth d = ring_depth<FEW, WIDE>();
+  int32_t m0 = 0;
+  for (; m0 + 32 < t.rows; m0 += 64) stream_rows<GLU, 8, d.d8, SPLIT>(t, m0, wv, lane, ring, part);
+  const int32_t left = t.rows - m0;
+  if (left > 16) stream_rows<GLU, 4, d.d4, SPLIT>(t, m0, wv, lane, ring, part);
+  else if (left > 8) stream_rows<GLU, 2, d.d2, SPLIT>(t, m0, wv, lane, ring, part);
+  else if (left > 0) stream_rows<GLU, 1, d.d1, SPLIT>(t, m0, wv, lane, ring, part);
+}
 
-template <bool GLU, bool SPLIT>
+// TABLE: 128-row tiles of the tile table; otherwise workgroup b takes a whole
+// group (b / column tiles) of the plan, with no table to wait for -- for batches
+// whose groups are small for certain.
+template <bool GLU, bool FEW, bool SPLIT, bool TABLE>
 __global__ __launch_bounds__(SPLIT ? 256 : 64) void k_grouped_gemm_i8_stream(
     const u32x4 *__restrict__ X, const float *__restrict__ SX, const u32x4 *__restrict__ W,
     const float *__restrict__ SW, const u32x4 *__restrict__ Wslot,
-    const float *__restrict__ SWslot, const int32_t *__restrict__ tiles,
-    const int32_t *__restrict__ ntiles, int32_t max_tiles, int32_t K, int32_t N, int32_t E,
-    int32_t n_col_tiles, uint16_t *__restrict__ Y) {
-  __shared__ u32x4 ring[(SPLIT ? 4 : 1) * kStreamSlots];   // 36 KB a wave
-  static_assert(4 * 2 * 16 * 64 * 4 <= 4 * kStreamSlots * 16, "the partial sums fit the rings");
-  int32_t tile, ctile;
-  if (!balanced_tile(ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
-  const int32_t row0 = tiles[tile * 4 + 0], rows = tiles[tile * 4 + 1], widx = tiles[tile * 4 + 2];
+    const float *__restrict__ SWslot, TileArgs a, int32_t max_tiles, int32_t K, int32_t N,
+    int32_t E, int32_t n_col_tiles, uint16_t *__restrict__ Y) {
+  constexpr int kSlots = ring_slots(ring_depth<FEW, false>());
+  __shared__ u32x4 ring[(SPLIT ? 4 : 1) * kSlots];
+  static_assert(4 * 2 * 16 * 64 * 4 <= 4 * kSlots * 16, "the partial sums fit the rings");
+  int32_t ctile, row0, rows, widx;
+  if constexpr (TABLE) {
+    int32_t tile;
+    if (!balanced_tile(a.ws.gemm_ntiles, max_tiles, n_col_tiles, tile, ctile)) return;
+    const int32_t *t = a.ws.gemm_tiles + (int64_t)tile * 4;
+    row0 = t[0];
+    rows = t[1];
+    widx = t[2];
+  } else {
+    const int32_t q = blockIdx.x / n_col_tiles;
+    ctile = blockIdx.x % n_col_tiles;
+    if (a.g.layout == kStatic && q >= a.g.E + *a.ws.n_segments) return;
+    group_of(a, q, row0, rows, widx);
+    if (rows <= 0) return;
+  }
   const bool own = widx < E;
   const int64_t wsel = own ? widx : widx - E;
   const StreamTile t = stream_tile<GLU>(X, SX, (own ? W : Wslot) + wsel * N * (K / 16),
@@ -397,8 +429,7 @@ __global__ __launch_bounds__(SPLIT ? 256 : 64) void k_grouped_gemm_i8_stream(
                                         ctile * kStreamCols, N, K);
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  stream_all<GLU, kStreamD1, kStreamD4, kStreamD8, SPLIT>(
-      t, wv, lane, ring + wv * kStreamSlots, reinterpret_cast<int32_t *>(ring));
+  stream_all<GLU, FEW, false, SPLIT>(t, wv, lane, ring + wv * kSlots, reinterpret_cast<int32_t *>(ring));
 }
 
 // ---------------------------------------------------------------------------
@@ -507,8 +538,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
                                           (own ? SW : SWslot) + wsel * N, Y, row0, rows,
                                           n0 + wv * kStreamCols, N, K);
     constexpr int kRing = (2 * kSlabA2 + 3 * kSlabB2) / 4;   // a wave's quarter of LDS
-    static_assert(kStreamSlots <= kRing, "one wave's ring");
-    stream_all<GLU, kStreamD1, kStreamD4, kStreamD8, false>(t, wv, lane, lds + wv * kRing, nullptr);
+    static_assert(ring_slots(kRingWide) <= kRing, "one wave's ring");
+    stream_all<GLU, false, true, false>(t, wv, lane, lds + wv * kRing, nullptr);
     return;
   }
   const int wm = wv >> 1, wn = wv & 1;
@@ -738,16 +769,29 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
 }
 
 // Which kernel: 256 x 256 tiles with at least 128 rows an expert on average
-// (and N of a column tile); the streaming kernel with at most 32, its waves
-// splitting K while the groups that can have rows, times their column tiles,
-// leave wave slots empty (four a compute unit); 128 x 128 tiles between.
-enum class I8Kernel { kStream, kSplit, kTiles, kWide };
-constexpr int64_t kStreamWaves = 1024;
+// (and N of a column tile); the streaming kernel with at most 32; 128 x 128
+// tiles between.
+enum class I8Kernel { kStream, kTiles, kWide };
 static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
   if (g.n >= (int64_t)(kBM2 / 2) * g.E && N >= kBN2) return I8Kernel::kWide;
-  if (g.n > (int64_t)32 * g.E) return I8Kernel::kTiles;
-  const int64_t waves = (g.n < g.E ? g.n : g.E) * (((int64_t)N + kStreamCols - 1) / kStreamCols);
-  return waves < kStreamWaves ? I8Kernel::kSplit : I8Kernel::kStream;
+  return g.n <= (int64_t)32 * g.E ? I8Kernel::kStream : I8Kernel::kTiles;
+}
+// The streaming kernel splits K while the groups that can have rows, times
+// their column tiles, are few units for the 1024 waves the GPU holds of it.
+constexpr int64_t kStreamWaves = 512;
+static bool stream_split(const Geometry &g, int64_t ncol) {
+  return (g.n < g.E ? g.n : g.E) * ncol < kStreamWaves;
+}
+// Small rings (kRingFew) up to this many rows an expert on average (560 us
+// against 582 at 4, 403 against 384 at 8).
+constexpr int64_t kFewRowsPerExpert = 6;
+// ... and goes without the tile table where no group can have many rows (two
+// passes over the weights, or a few more where a token names an expert twice):
+// the table's launch is most of a small batch's time.
+constexpr int32_t kDirectRows = 128;
+static bool stream_direct(const Geometry &g, int32_t K) {
+  const int32_t most = g.layout == kLL && g.cap < g.T ? g.cap : g.T;
+  return most <= kDirectRows && g.n * K <= INT32_MAX;   // 32-bit offsets over a group's rows
 }
 
 bool gemm_int8_fits(const Geometry &g, int32_t K, int32_t N) {
@@ -755,6 +799,7 @@ bool gemm_int8_fits(const Geometry &g, int32_t K, int32_t N) {
   const int64_t ncol = ((int64_t)N + kStreamCols - 1) / kStreamCols;
   const int64_t most = UINT32_MAX / kGemmThreads;
   return K <= kI8MaxK && gemm_grid_blocks(gemm_max_tiles(g), 1) * ncol <= most &&
+         gemm_groups(g) * ncol <= most &&
          blocked_grid(wide_max_tiles(g), ((int64_t)N + kBN2 - 1) / kBN2) <= most;
 }
 
@@ -764,34 +809,51 @@ hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, cons
                                     int32_t N, uint16_t *y, bool glu, hipStream_t s) {
   const I8Kernel kind = i8_kernel(g, N);
   const bool wide = kind == I8Kernel::kWide;
+  const bool direct = kind == I8Kernel::kStream && stream_direct(g, K);
   const int32_t max_tiles = wide ? wide_max_tiles(g) : gemm_max_tiles(g);
   if (g.n == 0 || max_tiles == 0) return hipSuccess;
-  const hipError_t e = launch_gemm_tiles(g, ws, wslot != nullptr, wide ? kShortRows : 0, max_tiles, s);
-  if (e != hipSuccess) return e;
-#define I8_LAUNCH(KERN, COLS, THREADS)                                                         \
-  do {                                                                                         \
-    const int32_t ncol = (N + (COLS)-1) / (COLS);                                              \
-    const int64_t blocks = kind == I8Kernel::kWide ? blocked_grid(max_tiles, ncol)             \
-                                                   : gemm_grid_blocks(max_tiles, ncol);        \
-    hipLaunchKernelGGL(KERN, dim3((unsigned)blocks), dim3(THREADS), 0, s,                      \
-                       reinterpret_cast<const u32x4 *>(x), sx, reinterpret_cast<const u32x4 *>(w), sw, \
-                       reinterpret_cast<const u32x4 *>(wslot), swslot, ws.gemm_tiles,          \
-                       ws.gemm_ntiles, max_tiles, K, N, g.E, ncol, y);                         \
-  } while (0)
-  if (kind == I8Kernel::kWide) {
-    if (glu) I8_LAUNCH(k_grouped_gemm_i8_256<true>, kBN2, kGemmThreads);
-    else I8_LAUNCH(k_grouped_gemm_i8_256<false>, kBN2, kGemmThreads);
-  } else if (kind == I8Kernel::kSplit) {
-    if (glu) I8_LAUNCH((k_grouped_gemm_i8_stream<true, true>), kStreamCols, 256);
-    else I8_LAUNCH((k_grouped_gemm_i8_stream<false, true>), kStreamCols, 256);
-  } else if (kind == I8Kernel::kStream) {
-    if (glu) I8_LAUNCH((k_grouped_gemm_i8_stream<true, false>), kStreamCols, 64);
-    else I8_LAUNCH((k_grouped_gemm_i8_stream<false, false>), kStreamCols, 64);
-  } else {
-    if (glu) I8_LAUNCH(k_grouped_gemm_i8<true>, kBN, kGemmThreads);
-    else I8_LAUNCH(k_grouped_gemm_i8<false>, kBN, kGemmThreads);
+  if (!direct) {
+    const hipError_t e = launch_gemm_tiles(g, ws, wslot != nullptr, wide ? kShortRows : 0, max_tiles, s);
+    if (e != hipSuccess) return e;
   }
+  const int32_t cols = wide ? kBN2 : kind == I8Kernel::kStream ? kStreamCols : kBN;
+  const int32_t ncol = (N + cols - 1) / cols;
+  const TileArgs ta{g, ws, wslot != nullptr ? 1 : 0};
+  const bool few = g.n <= kFewRowsPerExpert * g.E;
+#define I8_OPERANDS                                                                         \
+  reinterpret_cast<const u32x4 *>(x), sx, reinterpret_cast<const u32x4 *>(w), sw,           \
+      reinterpret_cast<const u32x4 *>(wslot), swslot
+#define I8_LAUNCH(KERN, BLOCKS)                                                             \
+  hipLaunchKernelGGL(KERN, dim3((unsigned)(BLOCKS)), dim3(kGemmThreads), 0, s, I8_OPERANDS, \
+                     ws.gemm_tiles, ws.gemm_ntiles, max_tiles, K, N, g.E, ncol, y)
+#define I8_STREAM1(GLU, FEW, SPLIT, TABLE, BLOCKS)                                          \
+  hipLaunchKernelGGL((k_grouped_gemm_i8_stream<GLU, FEW, SPLIT, TABLE>),                    \
+                     dim3((unsigned)(BLOCKS)), dim3(SPLIT ? 256 : 64), 0, s, I8_OPERANDS, ta, \
+                     max_tiles, K, N, g.E, ncol, y)
+#define I8_STREAM(SPLIT, TABLE, BLOCKS)                          \
+  do {                                                           \
+    if (glu && few) I8_STREAM1(true, true, SPLIT, TABLE, BLOCKS); \
+    else if (glu) I8_STREAM1(true, false, SPLIT, TABLE, BLOCKS); \
+    else if (few) I8_STREAM1(false, true, SPLIT, TABLE, BLOCKS); \
+    else I8_STREAM1(false, false, SPLIT, TABLE, BLOCKS);         \
+  } while (0)
+  if (wide) {
+    if (glu) I8_LAUNCH(k_grouped_gemm_i8_256<true>, blocked_grid(max_tiles, ncol));
+    else I8_LAUNCH(k_grouped_gemm_i8_256<false>, blocked_grid(max_tiles, ncol));
+  } else if (kind == I8Kernel::kTiles) {
+    if (glu) I8_LAUNCH(k_grouped_gemm_i8<true>, gemm_grid_blocks(max_tiles, ncol));
+    else I8_LAUNCH(k_grouped_gemm_i8<false>, gemm_grid_blocks(max_tiles, ncol));
+  } else if (direct) {
+    if (stream_split(g, ncol)) I8_STREAM(true, false, gemm_groups(g) * ncol);
+    else I8_STREAM(false, false, gemm_groups(g) * ncol);
+  } else {
+    if (stream_split(g, ncol)) I8_STREAM(true, true, gemm_grid_blocks(max_tiles, ncol));
+    else I8_STREAM(false, true, gemm_grid_blocks(max_tiles, ncol));
+  }
+#undef I8_STREAM
+#undef I8_STREAM1
 #undef I8_LAUNCH
+#undef I8_OPERANDS
   return hipGetLastError();
 }
 

@@ -328,11 +328,12 @@ static void bwd_shape(int32_t V, int &threads, int &vpt) {
 
 // Workgroups of the backward: about two of 512 threads a compute unit (and a
 // row each at least).
-constexpr int32_t kNormBwdThreads = 512 * 512;
+constexpr int32_t kNormBwdThreads = 512 * 512, kNormBwdMost = 2048;
 int32_t norm_bwd_groups(int32_t T, int32_t H) {
   int threads, vpt;
   bwd_shape(H / 8, threads, vpt);
-  const int32_t G = kNormBwdThreads / threads;
+  int32_t G = kNormBwdThreads / threads;
+  if (G > kNormBwdMost) G = kNormBwdMost;
   return T < G ? T : G;
 }
 
@@ -445,33 +446,38 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
   }
 }
 
-// grad_w[c] = sum of the G partial rows: a workgroup takes 32 columns, its 32
-// thread rows every 32nd partial row each, all fp64, joined in order.
-constexpr int kDwCols = 32, kDwRows = 32;
-__global__ __launch_bounds__(kDwCols * kDwRows) void k_rmsnorm_dw(const float *__restrict__ part,
-                                                                  int32_t G, int32_t H,
-                                                                  float *__restrict__ dw) {
-  __shared__ double s[kDwRows][kDwCols];
-  const int cl = threadIdx.x % kDwCols, rl = threadIdx.x / kDwCols;
-  const int32_t c = blockIdx.x * kDwCols + cl;
+// grad_w[c] = sum of the G partial rows: a workgroup takes COLS columns, its
+// 1024 / COLS thread rows every (1024 / COLS)th partial row each, all fp64, joined
+// in order.  Narrow rows take 8 columns a workgroup, so that more of them share
+// the partial rows.
+constexpr int kDwThreads = 1024;
+template <int COLS>
+__global__ __launch_bounds__(kDwThreads) void k_rmsnorm_dw(const float *__restrict__ part, int32_t G,
+                                                           int32_t H, float *__restrict__ dw) {
+  constexpr int kRows = kDwThreads / COLS;
+  __shared__ double s[kRows][COLS];
+  const int cl = threadIdx.x % COLS, rl = threadIdx.x / COLS;
+  const int32_t c = blockIdx.x * COLS + cl;
   double sum = 0.0;
   if (c < H) {
     int32_t i = rl;
-    for (; i + 7 * kDwRows < G; i += 8 * kDwRows) {
+    for (; i + 7 * kRows < G; i += 8 * kRows) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kDwRows) * H + c];
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kRows) * H + c];
 #pragma unroll
       for (int u = 0; u < 8; ++u) sum += (double)v[u];
     }
-    for (; i < G; i += kDwRows) sum += (double)part[(int64_t)i * H + c];
+    for (; i < G; i += kRows) sum += (double)part[(int64_t)i * H + c];
   }
   s[rl][cl] = sum;
   __syncthreads();
-  if (rl == 0 && c < H) {
-    for (int i = 1; i < kDwRows; ++i) sum += s[i][cl];
-    dw[c] = (float)sum;
+  // halves: thread row r adds row r + n's sum, for n = kRows / 2, ..., 1
+  for (int n = kRows / 2; n > 0; n >>= 1) {
+    if (rl < n) s[rl][cl] += s[rl + n][cl];
+    __syncthreads();
   }
+  if (rl == 0 && c < H) dw[c] = (float)s[0][cl];
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
@@ -497,8 +503,13 @@ hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!n.gw) return hipSuccess;
-  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((n.H + kDwCols - 1) / kDwCols)),
-                     dim3(kDwCols * kDwRows), 0, s, n.part, G, n.H, n.gw);   // T == 0: zeros
+  // T == 0: zeros
+  if (n.H <= 1024)
+    hipLaunchKernelGGL(k_rmsnorm_dw<8>, dim3((unsigned)((n.H + 7) / 8)), dim3(kDwThreads), 0, s,
+                       n.part, G, n.H, n.gw);
+  else
+    hipLaunchKernelGGL(k_rmsnorm_dw<32>, dim3((unsigned)((n.H + 31) / 32)), dim3(kDwThreads), 0, s,
+                       n.part, G, n.H, n.gw);
   return hipGetLastError();
 }
 
