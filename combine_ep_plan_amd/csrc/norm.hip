@@ -315,26 +315,34 @@ hipError_t launch_add_rmsnorm(const RmsNorm &n, hipStream_t s) {
 //   grad_h = rstd * (g - n * mean(g * n)) [+ grad_hidden]
 //   grad_w = sum over rows of grad_y * n
 // One reduction over a row gives sum h^2 and sum g * h.  A workgroup takes
-// every G-th row, the next row's loads in flight while one is reduced, and
-// keeps its share of grad_w in registers; the G partial rows go to the
-// workspace and a second kernel adds them in order, in fp64, so the result
-// does not depend on scheduling.
+// every G-th row (or group of narrow rows), the next row's loads in flight while
+// one is reduced, and keeps its share of grad_w in registers; the G partial rows
+// go to the workspace and a second kernel adds them in order, in fp64, so the
+// result does not depend on scheduling.  16384 x 4096: 90 + 5 us, 5.9 TB/s.
 
-// Threads and vectors a thread of a backward row.
-static void bwd_shape(int32_t V, int &threads, int &vpt) {
-  threads = V <= 1024 ? (V + 63) / 64 * 64 : 1024;
-  vpt = V <= threads ? 1 : V <= 2 * threads ? 2 : 4;
+// Threads of a backward row, vectors a thread, rows a workgroup takes at a time
+// (narrow rows share one, so that there are few partial rows of grad_w).
+struct BwdShape {
+  int threads, vpt, rows;
+};
+static BwdShape bwd_shape(int32_t V) {
+  BwdShape b;
+  b.threads = V <= 1024 ? (V + 63) / 64 * 64 : 1024;
+  b.vpt = V <= b.threads ? 1 : V <= 2 * b.threads ? 2 : 4;
+  b.rows = b.threads <= 256 ? 512 / b.threads : 1;
+  return b;
 }
 
-// Workgroups of the backward: about two of 512 threads a compute unit (and a
-// row each at least).
-constexpr int32_t kNormBwdThreads = 512 * 512, kNormBwdMost = 2048;
+// Workgroups of the backward: up to 512 (two of 512 threads a compute unit),
+// each with as many passes as the others, and at least two where there are rows
+// enough for 256 of them: a partial row costs as much to write and read as half
+// a row of the inputs.
 int32_t norm_bwd_groups(int32_t T, int32_t H) {
-  int threads, vpt;
-  bwd_shape(H / 8, threads, vpt);
-  int32_t G = kNormBwdThreads / threads;
-  if (G > kNormBwdMost) G = kNormBwdMost;
-  return T < G ? T : G;
+  if (T == 0) return 0;
+  const int64_t units = ((int64_t)T + bwd_shape(H / 8).rows - 1) / bwd_shape(H / 8).rows;
+  int64_t passes = (units + 511) / 512;
+  if (passes < 2 && units > 256) passes = 2;
+  return (int32_t)((units + passes - 1) / passes);
 }
 
 struct NormBwdArgs {
@@ -344,14 +352,16 @@ struct NormBwdArgs {
   const void *ghidden;  // or null
   void *gx;
   float *part;          // [G][H] partial grad_w, or null
-  int32_t T, V, w_fp32;
+  int32_t T, V, w_fp32, rows;
   double eps, inv_h;
 };
 
 template <typename RT, int VPT>
 __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
   __shared__ double s_sum[2][2][16];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, nw = blockDim.x >> 6;
+  extern __shared__ double s_dw[];  // [rows - 1][H]
+  const int tpr = blockDim.x / a.rows, slot = threadIdx.x / tpr, sub = threadIdx.x - slot * tpr;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = tpr >> 6, w0 = slot * nw;
   // the next row's loads in flight under this row, and the weight in registers,
   // where they fit
   constexpr bool AHEAD = VPT == 1;
@@ -362,8 +372,8 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
     const int64_t base = t * a.V;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int32_t v = tid + i * blockDim.x;
-      if (v >= a.V) continue;
+      const int32_t v = sub + i * tpr;
+      if (v >= a.V || t >= a.T) continue;
       hr[i] = load_raw<RT, true>(a.hidden, base + v);
       gr[i] = load_stream(a.gy + base + v);
       if (a.ghidden) rr[i] = load_raw<RT, true>(a.ghidden, base + v);
@@ -372,12 +382,14 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
   const auto weight = [&] {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int32_t v = tid + i * blockDim.x;
+      const int32_t v = sub + i * tpr;
       if (v < a.V) load_weight8(a.w, a.w_fp32, v, w[i]);
     }
   };
+  const int64_t step = (int64_t)gridDim.x * a.rows;
+  int64_t t = (int64_t)blockIdx.x * a.rows + slot;
   if constexpr (AHEAD) {
-    load(blockIdx.x);
+    load(t);
     weight();
   }
 #pragma unroll
@@ -385,8 +397,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) dw[i][c] = 0.0f;
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
+  // (all rows of the workgroup go through the same passes: the barrier)
+  for (; t - slot < a.T; t += step, buf ^= 1) {
     const int64_t base = t * a.V;
+    const bool live = t < a.T;
     float h[VPT][8], g[VPT][8], r[VPT][8];
     double ss = 0.0, sg = 0.0;
     if constexpr (!AHEAD) {
@@ -395,10 +409,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int32_t v = tid + i * blockDim.x;
+      const int32_t v = sub + i * tpr;
 #pragma unroll
       for (int c = 0; c < 8; ++c) h[i][c] = g[i][c] = r[i][c] = 0.0f;
-      if (v >= a.V) continue;
+      if (v >= a.V || !live) continue;
       unpack_raw(hr[i], h[i]);
       unpack8(gr[i], g[i]);
       if (a.ghidden) unpack_raw(rr[i], r[i]);
@@ -408,23 +422,25 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
         sg = __builtin_fma((double)(g[i][c] * w[i][c]), (double)h[i][c], sg);
       }
     }
-    if constexpr (AHEAD)
-      if (t + gridDim.x < a.T) load(t + gridDim.x);
+    if constexpr (AHEAD) load(t + step);
     ss = wave_sum(ss);
     sg = wave_sum(sg);
-    if (lane == 0) {
-      s_sum[buf][0][wv] = ss;
-      s_sum[buf][1][wv] = sg;
+    if (nw > 1) {
+      if (lane == 0) {
+        s_sum[buf][0][wv] = ss;
+        s_sum[buf][1][wv] = sg;
+      }
+      __syncthreads();   // two buffers: the next row's sums do not meet this row's readers
+      const int i = lane & 15;
+      ss = row_sum(i < nw ? s_sum[buf][0][w0 + i] : 0.0);
+      sg = row_sum(i < nw ? s_sum[buf][1][w0 + i] : 0.0);
     }
-    __syncthreads();   // two buffers: the next row's sums do not meet this row's readers
-    ss = row_sum((lane & 15) < nw ? s_sum[buf][0][lane & 15] : 0.0);
-    sg = row_sum((lane & 15) < nw ? s_sum[buf][1][lane & 15] : 0.0);
     const float rstd = rstd_of(ss, a.inv_h, a.eps);
     const float mean = (float)(sg * (double)rstd * a.inv_h);  // mean of g * n
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int32_t v = tid + i * blockDim.x;
-      if (v >= a.V) continue;
+      const int32_t v = sub + i * tpr;
+      if (v >= a.V || !live) continue;
       float o[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -437,43 +453,58 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_bwd(NormBwdArgs a) {
       store8<RT>(a.gx, base + v, o);
     }
   }
-  if (a.part) {
+  if (!a.part) return;
+  if constexpr (VPT == 1) {   // several rows only with one vector a thread; joined in fp64
+    if (a.rows > 1) {
+      const int32_t H = a.V * 8;
+      if (slot > 0 && sub < a.V) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int32_t v = tid + i * blockDim.x;
-      if (v < a.V) store8<float>(a.part, (int64_t)blockIdx.x * a.V + v, dw[i]);
+        for (int c = 0; c < 8; ++c) s_dw[(slot - 1) * H + c * a.V + sub] = (double)dw[0][c];
+      }
+      __syncthreads();
+      if (slot > 0) return;
+      if (sub < a.V) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          double sum = (double)dw[0][c];
+          for (int i = 0; i < a.rows - 1; ++i) sum += s_dw[i * H + c * a.V + sub];
+          dw[0][c] = (float)sum;
+        }
+      }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int32_t v = sub + i * tpr;
+    if (v < a.V) store8<float>(a.part, (int64_t)blockIdx.x * a.V + v, dw[i]);
   }
 }
 
-// grad_w[c] = sum of the G partial rows: a workgroup takes COLS columns, its
-// 1024 / COLS thread rows every (1024 / COLS)th partial row each, all fp64, joined
-// in order.  Narrow rows take 8 columns a workgroup, so that more of them share
-// the partial rows.
-constexpr int kDwThreads = 1024;
-template <int COLS>
+// grad_w[c] = sum of the G partial rows: a workgroup takes 32 columns, its 32
+// thread rows every 32nd partial row each, all fp64, joined
+// in order.
+constexpr int kDwThreads = 1024, kDwCols = 32, kDwRows = kDwThreads / kDwCols;
 __global__ __launch_bounds__(kDwThreads) void k_rmsnorm_dw(const float *__restrict__ part, int32_t G,
                                                            int32_t H, float *__restrict__ dw) {
-  constexpr int kRows = kDwThreads / COLS;
-  __shared__ double s[kRows][COLS];
-  const int cl = threadIdx.x % COLS, rl = threadIdx.x / COLS;
-  const int32_t c = blockIdx.x * COLS + cl;
+  __shared__ double s[kDwRows][kDwCols];
+  const int cl = threadIdx.x % kDwCols, rl = threadIdx.x / kDwCols;
+  const int32_t c = blockIdx.x * kDwCols + cl;
   double sum = 0.0;
   if (c < H) {
     int32_t i = rl;
-    for (; i + 7 * kRows < G; i += 8 * kRows) {
+    for (; i + 7 * kDwRows < G; i += 8 * kDwRows) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kRows) * H + c];
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kDwRows) * H + c];
 #pragma unroll
       for (int u = 0; u < 8; ++u) sum += (double)v[u];
     }
-    for (; i < G; i += kRows) sum += (double)part[(int64_t)i * H + c];
+    for (; i < G; i += kDwRows) sum += (double)part[(int64_t)i * H + c];
   }
   s[rl][cl] = sum;
   __syncthreads();
-  // halves: thread row r adds row r + n's sum, for n = kRows / 2, ..., 1
-  for (int n = kRows / 2; n > 0; n >>= 1) {
+  // halves: thread row r adds row r + n's sum, for n = kDwRows / 2, ..., 1
+  for (int n = kDwRows / 2; n > 0; n >>= 1) {
     if (rl < n) s[rl][cl] += s[rl + n][cl];
     __syncthreads();
   }
@@ -483,17 +514,19 @@ __global__ __launch_bounds__(kDwThreads) void k_rmsnorm_dw(const float *__restri
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
   const int32_t G = norm_bwd_groups(n.T, n.H);
   if (n.T > 0) {
+    const BwdShape sh = bwd_shape(n.H / 8);
     const NormBwdArgs a{n.hidden, n.w, reinterpret_cast<const u32x4 *>(n.gy), n.ghidden, n.gx,
-                        n.gw ? n.part : nullptr, n.T, n.H / 8, n.w_fp32 ? 1 : 0, n.eps, 1.0 / n.H};
-    int threads, vpt;
-    bwd_shape(a.V, threads, vpt);
-#define L2(RT, P) \
-  hipLaunchKernelGGL((k_rmsnorm_bwd<RT, P>), dim3((unsigned)G), dim3(threads), 0, s, a)
-#define L(RT)                    \
-  do {                           \
-    if (vpt == 1) L2(RT, 1);     \
-    else if (vpt == 2) L2(RT, 2); \
-    else L2(RT, 4);              \
+                        n.gw ? n.part : nullptr, n.T, n.H / 8, n.w_fp32 ? 1 : 0, sh.rows, n.eps,
+                        1.0 / n.H};
+    const size_t lds = sizeof(double) * (size_t)(sh.rows - 1) * n.H;   // 28 KB at most
+#define L2(RT, P)                                                                             \
+  hipLaunchKernelGGL((k_rmsnorm_bwd<RT, P>), dim3((unsigned)G), dim3(sh.threads * sh.rows), lds, \
+                     s, a)
+#define L(RT)                       \
+  do {                              \
+    if (sh.vpt == 1) L2(RT, 1);     \
+    else if (sh.vpt == 2) L2(RT, 2); \
+    else L2(RT, 4);                 \
   } while (0)
     if (n.h_fp32) L(float);
     else L(uint16_t);
@@ -503,13 +536,8 @@ hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!n.gw) return hipSuccess;
-  // T == 0: zeros
-  if (n.H <= 1024)
-    hipLaunchKernelGGL(k_rmsnorm_dw<8>, dim3((unsigned)((n.H + 7) / 8)), dim3(kDwThreads), 0, s,
-                       n.part, G, n.H, n.gw);
-  else
-    hipLaunchKernelGGL(k_rmsnorm_dw<32>, dim3((unsigned)((n.H + 31) / 32)), dim3(kDwThreads), 0, s,
-                       n.part, G, n.H, n.gw);
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((n.H + kDwCols - 1) / kDwCols)), dim3(kDwThreads),
+                     0, s, n.part, G, n.H, n.gw);   // T == 0: zeros
   return hipGetLastError();
 }
 

@@ -74,6 +74,17 @@ def test_route_refusals(lib):  # noqa: F811
     assert lib.ep_route_scored_bwd(h, r, bf, good[2], good[3], bf, bf, None) == DTYPE
 
 
+def test_route_refuses_launches_past_32_bits(lib):  # noqa: F811
+    T = 1 << 26
+    rc, g = create(lib, hidden=64, max_tokens=T)
+    assert rc == OK
+    h = ctypes.c_void_p()
+    assert lib.ep_handle_create(g, T, FAKE, 1 << 36, ctypes.byref(h)) == OK
+    lg, i, w = view(FP32, LOG, T, 8), view(I32, IDX, T, 2), view(FP32, WTS, T, 2)
+    assert lib.ep_route_scored(h, rule(), lg, None, i, w, None, None) == UNSUPPORTED
+    assert lib.ep_route_scored_bwd(h, rule(), lg, i, w, None, lg, None) == UNSUPPORTED
+
+
 def norm_rule(eps=1e-6, quant=0, reserved=0):
     return ctypes.pointer(ep.ep_norm_rule_t(eps, quant, reserved))
 
@@ -120,10 +131,11 @@ def test_norm_bwd_refusals(lib):  # noqa: F811
     f, r = lib.ep_add_rmsnorm_bwd, norm_rule()
     h, w, gw = view(BF16, T_, 4, 256), view(BF16, NW, 256), view(FP32, NW, 256)
     need = ctypes.c_size_t()
-    assert lib.ep_add_rmsnorm_bwd_workspace_bytes(4, 256, ctypes.byref(need)) == OK and need.value == 4 * 256 * 4
+    assert lib.ep_add_rmsnorm_bwd_workspace_bytes(4, 256, ctypes.byref(need)) == OK
+    assert 256 * 4 <= need.value <= 4 * 256 * 4   # at least one partial row, at most one a row
+    n = need.value // 4
     for rows, H in ((-1, 256), (4, 0), (4, 12), (4, 32776), (1 << 31, 256)):
         assert lib.ep_add_rmsnorm_bwd_workspace_bytes(rows, H, ctypes.byref(need)) == INVALID
-    n = 4 * 256
     ws = view(FP32, WS, n)
     assert f(norm_rule(quant=1), h, w, h, None, h, gw, ws, None) == INVALID
     assert f(r, None, w, h, None, h, gw, ws, None) == INVALID
