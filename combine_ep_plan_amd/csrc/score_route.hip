@@ -97,6 +97,13 @@ template <int G>
 __device__ __forceinline__ uint32_t token_min(uint32_t v) {
   return ~(G == 64 ? wave_max(~v) : row_max(~v));
 }
+// Integers in the order of floats (-0 as 0); kNoChoice is that of -inf.
+__device__ __forceinline__ uint32_t choice_key(float f) {
+  const int32_t b = __float_as_int(f + 0.0f);
+  return (uint32_t)(b ^ (b >> 31 | (int32_t)0x80000000));
+}
+constexpr uint32_t kNoChoice = 0x007FFFFFu;
+
 template <int G>
 __device__ __forceinline__ float token_sum_f(float v) {
   v += __uint_as_float(dpp<kDppXor1>(__float_as_uint(v)));
@@ -152,6 +159,13 @@ __device__ __forceinline__ void join2(double &m1, double &m2, double o1, double 
   m1 = max_d(m1, o1);
 }
 
+// LDS written by lanes of this wave is read by others.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Masks the experts of the groups a token may not choose from.  The choices go
 // through LDS (sv, the token's own part): `per` lanes share a group, each
 // scanning every per-th member, then join; more groups than lanes take several
@@ -159,20 +173,26 @@ __device__ __forceinline__ void join2(double &m1, double &m2, double o1, double 
 template <int G, int PER>
 __device__ __forceinline__ void keep_groups(double (&v)[PER], const ScoreRule &rule, int32_t E,
                                             int sub, double *sv, double *gv) {
-#pragma unroll
-  for (int i = 0; i < PER; ++i) sv[sub + G * i] = v[i];
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   int per = G;
   while (per > 1 && per * rule.groups > G) per >>= 1;
-  const int gs = E / rule.groups;
+  const int gs = E / rule.groups, pitch = G == 64 ? gs + per : gs;   // (four tokens' LDS has no room for the gap
+  // that keeps lanes on other banks: four workgroups a compute unit are worth more)
+  const float inv = 1.0f / (float)gs;
+  int grp[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = sub + G * i;
+    grp[i] = (int)(((float)e + 0.5f) * inv);  // e / gs, exact for E <= 1024
+    if (e < E) sv[grp[i] * pitch + e - grp[i] * gs] = v[i];
+  }
+  wave_fence();
   for (int q0 = 0; q0 < rule.groups; q0 += G / per) {
     const int q = q0 + sub / per;
     double m1 = -INFINITY, m2 = -INFINITY;
     if (q < rule.groups) {
+#pragma unroll 4
       for (int i = sub & (per - 1); i < gs; i += per) {
-        const double c = sv[q * gs + i];
+        const double c = sv[q * pitch + i];
         m2 = max_d(m2, m1 < c ? m1 : c);
         m1 = max_d(m1, c);
       }
@@ -198,9 +218,7 @@ __device__ __forceinline__ void keep_groups(double (&v)[PER], const ScoreRule &r
     }
     if (q < rule.groups) gv[q] = rule.top2 && m2 > -INFINITY ? m1 + m2 : m1;
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_fence();
   // a group stays if fewer than `kept` come before it; lane `sub` ranks groups
   // sub, sub + G, ...
   uint64_t kept = 0;  // bit g
@@ -208,6 +226,7 @@ __device__ __forceinline__ void keep_groups(double (&v)[PER], const ScoreRule &r
     const int q = q0 + sub;
     const double mine = q < rule.groups ? gv[q] : -INFINITY;
     int rank = 0;
+#pragma unroll 8
     for (int p = 0; p < rule.groups; ++p) {
       const double o = gv[p];
       rank += o > mine || (o == mine && p < q) ? 1 : 0;
@@ -216,13 +235,9 @@ __device__ __forceinline__ void keep_groups(double (&v)[PER], const ScoreRule &r
     if constexpr (G == 64) kept = b;  // at most 64 groups
     else kept |= ((b >> (threadIdx.x & 48)) & 0xFFFFull) << q0;
   }
-  const float inv = 1.0f / (float)gs;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = sub + G * i;
-    const int g = (int)(((float)e + 0.5f) * inv);  // e / gs, exact for E <= 1024
-    if (e < E && !((kept >> g) & 1)) v[i] = -INFINITY;
-  }
+  for (int i = 0; i < PER; ++i)
+    if (sub + G * i < E && !((kept >> grp[i]) & 1)) v[i] = -INFINITY;
 }
 
 template <typename LT, int G, int PER>
@@ -231,7 +246,7 @@ __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route(
     int32_t E, int32_t k, int32_t *__restrict__ idx_out, float *__restrict__ w_out,
     float *__restrict__ scores) {
   constexpr int kTokens = 64 / G;  // of a wave
-  __shared__ double s_choice[kScoreWaves * kTokens][G * PER];
+  __shared__ double s_choice[kScoreWaves * kTokens][G * (PER + (G == 64 ? 1 : 0))];
   __shared__ double s_group[kScoreWaves * kTokens][kMaxGroups];
   const int lane = threadIdx.x & 63, sub = lane & (G - 1), tok = threadIdx.x / G;
   const int64_t t0 = (int64_t)blockIdx.x * (kScoreWaves * kTokens) + tok;
@@ -295,28 +310,70 @@ __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route(
     v[i] = !masked(l[i]) && v[i] > -INFINITY ? v[i] : -INFINITY;
   if (grouped) keep_groups<G, PER>(v, rule, E, sub, s_choice[tok], s_group[tok]);
 
+  // A round: the lane's best choice left, then the token's, then the lowest
+  // expert that has it.  A wave on one token compares choices rounded to fp32
+  // first, which keeps their order: one lane alone with the largest has the
+  // token's choice, and fp64 and the ids decide only where several have it
+  // (4096 tokens, 256 experts: 8.1 -> 6.4 us; four tokens a wave gain nothing).
   int32_t my_e = -1;
-  for (int j = 0; j < k; ++j) {
-    double b = v[0];
-    int bi = 0;
+  float my_logit = 0.0f;
+  if constexpr (G == 64) {
+    int2 *const pick = reinterpret_cast<int2 *>(s_group[tok]);   // expert and logit of each choice
+    static_assert(kMaxTopK <= kMaxGroups, "the choices fit the groups' values");
+    int found = 0;
+    for (; found < k; ++found) {
+      double b = v[0];
+      float bl = l[0];
+      int bi = 0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) {
-      const bool g = v[i] > b;
-      b = g ? v[i] : b;
-      bi = g ? i : bi;
+      for (int i = 1; i < PER; ++i) {
+        const bool g = v[i] > b;
+        b = g ? v[i] : b;
+        bl = g ? l[i] : bl;
+        bi = g ? i : bi;
+      }
+      const uint32_t key = choice_key((float)b), top = wave_max(key);
+      if (__builtin_amdgcn_readfirstlane(top) <= kNoChoice) break;  // nothing left to choose
+      bool mine = key == top;
+      const uint64_t have = __ballot(mine);
+      if ((have & (have - 1)) != 0) {
+        const double best = token_max<G>(mine ? b : -INFINITY);
+        const uint32_t e = token_min<G>(mine && b == best ? (uint32_t)(sub + G * bi) : 0xFFFFFFFFu);
+        mine = (e & (G - 1)) == (uint32_t)sub;
+      }
+      if (mine) pick[found] = make_int2(sub + G * bi, __float_as_int(bl));
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = mine && i == bi ? -INFINITY : v[i];
     }
-    const double top = token_max<G>(b);
-    const bool any = top > -INFINITY;
-    if (!__any(any)) break;  // nothing left to choose for any token of the wave
-    const uint32_t e = token_min<G>(any && b == top ? (uint32_t)(sub + G * bi) : 0xFFFFFFFFu);
-    const int pos = (e & (G - 1)) == (uint32_t)sub ? (int)(e / G) : -1;
+    wave_fence();
+    if (sub < found) {
+      my_e = pick[sub].x;
+      my_logit = __int_as_float(pick[sub].y);
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      double b = v[0];
+      int bi = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = any && i == pos ? -INFINITY : v[i];
-    my_e = sub == j && any ? (int32_t)e : my_e;
+      for (int i = 1; i < PER; ++i) {
+        const bool g = v[i] > b;
+        b = g ? v[i] : b;
+        bi = g ? i : bi;
+      }
+      const double top = token_max<G>(b);
+      const bool any = top > -INFINITY;
+      if (!__any(any)) break;  // nothing left to choose for any token of the wave
+      const uint32_t e = token_min<G>(any && b == top ? (uint32_t)(sub + G * bi) : 0xFFFFFFFFu);
+      const int pos = (e & (G - 1)) == (uint32_t)sub ? (int)(e / G) : -1;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = any && i == pos ? -INFINITY : v[i];
+      my_e = sub == j && any ? (int32_t)e : my_e;
+    }
+    if (my_e >= 0) my_logit = logit_value(logits[t * E + my_e]);
   }
 
   const bool chosen = my_e >= 0;
-  const double my_l = chosen ? (double)logit_value(logits[t * E + my_e]) : 0.0;
+  const double my_l = (double)my_logit;
   double w = 0.0;
   if (rule.renorm) {
     // exponents of the scores, up to a common factor: l, or min(l, 0) with 1 + e^-|l| beside it
@@ -474,13 +531,18 @@ __global__ __launch_bounds__(64 * kScoreWaves) void k_score_route_bwd(
 
 // F(G, PER): a wave per token for few tokens and for more than 256 experts
 // (their choices would not fit a row's registers and LDS); a 16-lane row
-// otherwise.  Forward with E = 256, 8 groups: 6.7 us with a wave and 11.1 with
-// a row at 128 tokens, 11.4 and 11.5 at 4096, 33 and 22 at 16384; E = 128,
-// softmax: 4.6 and 5.5 at 1024, 7.5 and 5.7 at 4096.
-static bool wave_per_token(int32_t T, int32_t E) { return E > 256 || T <= (E > 128 ? 4096 : 2048); }
-#define EP_SCORE_SWITCH(T, E, F)                                 \
+// otherwise.  "Few" is up to 4096 with more than `many` experts, up to 2048
+// below.  Forward, a wave against a row: E = 256 in 8 groups 5.9 and 11.1 us at
+// 128 tokens, 9.8 and 11.5 at 4096, 16.3 and 14.4 at 8192; E = 128, softmax: 4.9
+// and 5.6 at 4096, 7.4 and 6.2 at 8192; E = 64: 5.2 and 4.9 at 4096.  Backward,
+// E = 128: 4.3 and 3.8 at 4096, E = 256: 7.9 and 7.2 at 8192.
+constexpr int kManyForward = 64, kManyBackward = 128;
+static bool wave_per_token(int32_t T, int32_t E, int many) {
+  return E > 256 || T <= (E > many ? 4096 : 2048);
+}
+#define EP_SCORE_SWITCH(T, E, MANY, F)                           \
   do {                                                           \
-    if (wave_per_token(T, E)) {                                  \
+    if (wave_per_token(T, E, MANY)) {                            \
       const int per_ = ((E) + 63) / 64;                          \
       if (per_ <= 1) F(64, 1);                                   \
       else if (per_ <= 2) F(64, 2);                              \
@@ -519,7 +581,7 @@ hipError_t launch_route_scored(const Geometry &g, const ep_route_rule_t &r, cons
     if (bf16) L1(uint16_t, G, P); \
     else L1(float, G, P);         \
   } while (0)
-  EP_SCORE_SWITCH(g.T, g.E, L);
+  EP_SCORE_SWITCH(g.T, g.E, kManyForward, L);
 #undef L
 #undef L1
   return hipGetLastError();
@@ -542,7 +604,7 @@ hipError_t launch_route_scored_bwd(const Geometry &g, const Workspace &ws,
     else if (dense) L1(float, true, G, P);     \
     else L1(float, false, G, P);               \
   } while (0)
-  EP_SCORE_SWITCH(g.T, g.E, L);
+  EP_SCORE_SWITCH(g.T, g.E, kManyBackward, L);
 #undef L
 #undef L1
   return hipGetLastError();
