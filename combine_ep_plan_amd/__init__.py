@@ -961,7 +961,9 @@ class Buffer:
         gw = torch.empty(H, dtype=torch.float32, device=hidden.device)
         if workspace is None:
             n = ep_add_rmsnorm_bwd_workspace_bytes(hidden.numel() // H, H) // 4
-            workspace = torch.empty(n, dtype=torch.float32, device=hidden.device)
+            on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+            with torch.cuda.stream(on):   # let go of on return: the memory is the call's stream's
+                workspace = torch.empty(n, dtype=torch.float32, device=hidden.device)
         ep_add_rmsnorm_bwd(hidden, weight, grad_y, grad_residual_out, grad, gw, workspace, eps, stream)
         return grad, gw
 

@@ -165,3 +165,24 @@ def test_bwd_without_weight_gradient_and_in_place():
     grad, _ = ep.Buffer.add_rmsnorm_bwd(h, w, gy, gh)
     ep.ep_add_rmsnorm_bwd(h, w, gy, gh, gh, None, None)
     assert torch.equal(grad, gh)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_bwd_workspace_belongs_to_the_call_stream(raw):
+    """The workspace a call makes for itself on another stream is not handed
+    to the current stream while the call still waits to run."""
+    rng = np.random.default_rng(9)
+    T, H = 512, 1024
+    h, gy = (_rows(rng, T, H, torch.bfloat16) for _ in range(2))
+    w = torch.ones(H, device="cuda")
+    want = ep.Buffer.add_rmsnorm_bwd(h, w, gy)
+    n = ep.ep_add_rmsnorm_bwd_workspace_bytes(T, H) // 4
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = ep.Buffer.add_rmsnorm_bwd(h, w, gy, stream=side.cuda_stream if raw else side)
+    mine = torch.full((n,), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(mine, torch.full_like(mine, 7.0))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
