@@ -11,6 +11,9 @@ entry points one to one.  ``Group`` / ``Handle`` / ``Buffer`` wrap them in
 the group -> handle -> dispatch -> expert -> combine flow of the NCCL EP
 paper (listing, Table II and Figure 2), and ``Buffer.dispatch`` returns
 ``recv_x, recv_i, recv_w, handle, event`` like that paper's Table V.
+``Buffer.add_rmsnorm``, ``Handle.route_scored``, ``Buffer.dispatch_quantized``,
+``Buffer.expert_gemm_int8`` and ``Buffer.quantize_int8`` are the layer's front
+and its INT8 path; their arguments are marshalled in C++ (``_marshal``).
 """
 
 from __future__ import annotations
