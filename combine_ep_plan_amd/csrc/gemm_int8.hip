@@ -21,6 +21,8 @@
 // k_grouped_gemm_i8: 128 x 128 tiles, 256 threads, two workgroups a CU; four
 // waves in 2 x 2, each 2 x 2 accumulators of 32 x 32; slabs of 128 bytes of
 // K, double-buffered in LDS with the chunk swizzle of gemm_common.h.
+#include <type_traits>
+
 #include "gemm_common.h"
 
 namespace epk {
@@ -504,6 +506,174 @@ __device__ __forceinline__ void mfma_i8_rows(i32x16 (&acc)[kFM2][kFN2], const Fr
   }
 }
 
+// The output tile of 128 WM rows by 256 columns (128 outputs for SwiGLU), a wave
+// with its FM x FN accumulators at (wm, wn): scaled and, through LDS as bf16 rows
+// (TN columns, the 16-byte chunk of column c of row r at (c / 8) ^ (((r / 4) % 4)
+// * 4), so the half-waves' rows r and r + 4 land on different banks), stored in
+// 16-byte row stores; 2-byte stores where a row of Y is no whole number of
+// vectors.  SX, SW, Y: of the tile's first row and column (Y: row).
+template <bool GLU, int FM, int FN, int WM>
+__device__ __forceinline__ void store_tile(const i32x16 (&acc)[FM][FN], u32x4 *lds,
+                                           const float *__restrict__ SX, const float *__restrict__ SW,
+                                           uint16_t *__restrict__ Y, int32_t rows, int32_t wrows,
+                                           int32_t n0, int32_t N, int wm, int wn) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  float sw[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int n = weight_row<GLU>(wn * FN * 32 + j * 32 + (lane & 31));
+    sw[j] = SW[n < wrows ? n : wrows - 1];
+  }
+  const int32_t NO = GLU ? N / 2 : N;
+  constexpr int TN = GLU ? kBN2 / 2 : kBN2;
+  const bool vec = (NO & 7) == 0;
+  const int32_t c0 = GLU ? n0 / 2 : n0;
+  uint16_t *so = reinterpret_cast<uint16_t *>(lds);
+  float *const ssx = reinterpret_cast<float *>(lds + kBM2 * kBN2 * 2 / 16);
+  __syncthreads();   // every wave is done with the slab buffers
+  ssx[tid] = SX[tid < rows ? tid : rows - 1];
+  __syncthreads();
+#define OSW(r_, cv_) ((r_) * TN + (((cv_) ^ ((((r_) >> 2) & 3) << 2)) << 3))
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int rr = wm * FM * 32 + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
+      const float sx = ssx[rr];
+      constexpr int kOut = GLU ? FN / 2 : FN;
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        float v;
+        if constexpr (GLU)
+          v = silu_mul((float)acc[i][2 * j][r] * (sx * sw[2 * j]),
+                       (float)acc[i][2 * j + 1][r] * (sx * sw[2 * j + 1]));
+        else
+          v = (float)acc[i][j][r] * (sx * sw[j]);
+        const int c = wn * (kOut * 32) + j * 32 + (lane & 31);
+        if (vec) so[OSW(rr, c >> 3) + (c & 7)] = bf16_bits(v);
+        else if (rr < rows && c0 + c < NO) Y[(int64_t)rr * NO + c0 + c] = bf16_bits(v);
+      }
+    }
+  if (!vec) return;
+  __syncthreads();
+  constexpr int kVecs = WM * FM * 32 * TN / 8;
+#pragma unroll 4
+  for (int q = 0; q < kVecs / kGemmThreads; ++q) {
+    const int idx = tid + q * kGemmThreads;
+    const int rr = idx / (TN / 8), cv = idx % (TN / 8), col = c0 + cv * 8;
+    if (rr < rows && col < NO)
+      *reinterpret_cast<u32x4 *>(Y + (int64_t)rr * NO + col) =
+          *reinterpret_cast<const u32x4 *>(so + OSW(rr, cv));
+  }
+#undef OSW
+}
+
+// A tile of at most 128 rows: four waves side by side, each all rows by 64
+// columns (4 x 2 accumulators), slabs of X and W straight into a ring of three in
+// LDS, two in flight, fragments read a quarter of a slab ahead and the loads
+// spread between the MFMAs.  256 experts, K = 7168, N = 4096, SwiGLU: 1280 us with
+// 34 rows an expert (1630 with 128 x 128 tiles), 1490 with 64 (1660), 1530 with 94
+// (1710), 1780 with 125 (2160); skewed with 64 on average 1045 (1395).
+constexpr int kHalfRows = 128, kSlabA1 = kHalfRows * kChunks;
+template <bool GLU>
+__device__ __forceinline__ void half_tile(__amdgpu_buffer_rsrc_t rX, __amdgpu_buffer_rsrc_t rW,
+                                          const float *SX, const float *SW, uint16_t *Y, int32_t rows,
+                                          int32_t wrows, int32_t n0, int32_t N, int32_t K, int wv,
+                                          u32x4 *lds) {
+  constexpr int RING = kSlabA1 + kSlabB2, NA = kSlabA1 / kGemmThreads, NB = kSlabB2 / kGemmThreads;
+  static_assert(NA == 4 && NB == 8, "the waits below count 12 loads a slab, three a quarter");
+  const int tid = threadIdx.x, lane = tid & 63;
+  uint32_t oa[NA], ob[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int q = i * kGemmThreads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    oa[i] = (uint32_t)((r < rows ? r : rows - 1) * K + (K == 64 ? c & 3 : c) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int q = i * kGemmThreads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    const int n = weight_row<GLU>(r);
+    ob[i] = (uint32_t)((n < wrows ? n : wrows - 1) * K + (K == 64 ? c & 3 : c) * 16);
+  }
+  const int KT = (K + kI8Slab - 1) / kI8Slab;
+  const bool half = K % kI8Slab != 0;
+  const int last = K > kI8Slab ? K - kI8Slab : 0;
+#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
+  // a quarter of a slab's loads: two of W, one of X
+  const auto issue = [&](int kt, int buf, int c) {
+    const int so = kt + 1 < KT ? kt * kI8Slab : last;
+    u32x4 *const a = lds + buf * RING + wv * 64, *const b = a + kSlabA1;
+    lds_load16_stream(rW, LDS_ADDR(b + 2 * c * kGemmThreads), ob[2 * c], so);
+    lds_load16_stream(rW, LDS_ADDR(b + (2 * c + 1) * kGemmThreads), ob[2 * c + 1], so);
+    lds_load16(rX, LDS_ADDR(a + c * kGemmThreads), oa[c], so);
+  };
+#undef LDS_ADDR
+  i32x16 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) issue(0, 0, c);
+  if (KT > 1) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) issue(1, 1, c);
+  }
+  int buf = 0, next = 2;
+  // a slab: its fragments a quarter ahead, slab kt + 2's loads between the MFMAs
+  const auto slab = [&](int kt, auto more, auto first) {
+    const u32x4 *sa = lds + buf * RING, *sb = sa + kSlabA1;
+    i32x4 fa[2][4], fb[2][2];
+    const auto read = [&](int c) {
+      const int cc = 2 * c + (lane >> 5);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        fb[c & 1][j] = __builtin_bit_cast(i32x4, sb[swz(wv * 64 + j * 32 + (lane & 31), cc)]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        fa[c & 1][i] = __builtin_bit_cast(i32x4, sa[swz(i * 32 + (lane & 31), cc)]);
+    };
+    constexpr int F = decltype(first)::value;
+    read(F);
+#pragma unroll
+    for (int c = F; c < 4; ++c) {
+      if (c + 1 < 4) read(c + 1);
+      if constexpr (decltype(more)::value) issue(kt + 2, next, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[c & 1][i], fb[c & 1][j], acc[i][j], 0, 0, 0);
+    }
+    buf = buf == 2 ? 0 : buf + 1;
+    next = next == 2 ? 0 : next + 1;
+  };
+  // slab kt landed for every wave, and every wave has read slab kt - 1
+#define I8H_SYNC(VM) asm volatile("s_waitcnt vmcnt(" #VM ") lgkmcnt(0)\n\ts_barrier" ::: "memory")
+  using std::integral_constant;
+  constexpr integral_constant<bool, true> kMore{};
+  constexpr integral_constant<bool, false> kNoMore{};
+  constexpr integral_constant<int, 0> kWhole{};
+  constexpr integral_constant<int, 2> kUpper{};
+  int kt = 0;
+  for (; kt + 2 < KT; ++kt) {
+    I8H_SYNC(12);
+    slab(kt, kMore, kWhole);
+  }
+  if (kt + 1 < KT) {
+    I8H_SYNC(12);
+    slab(kt, kNoMore, kWhole);
+    ++kt;
+  }
+  I8H_SYNC(0);
+  if (half) slab(kt, kNoMore, kUpper);
+  else slab(kt, kNoMore, kWhole);
+#undef I8H_SYNC
+  store_tile<GLU, 4, 2, 1>(acc, lds, SX, SW, Y, rows, wrows, n0, N, 0, wv);
+}
+
 template <bool GLU>
 __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
     const u32x4 *__restrict__ X, const float *__restrict__ SX, const u32x4 *__restrict__ W,
@@ -540,6 +710,12 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
     constexpr int kRing = (2 * kSlabA2 + 3 * kSlabB2) / 4;   // a wave's quarter of LDS
     static_assert(ring_slots(kRingWide) <= kRing, "one wave's ring");
     stream_all<GLU, false, true, false>(t, wv, lane, lds + wv * kRing, nullptr);
+    return;
+  }
+  if (rows <= kHalfRows) {
+    static_assert(3 * (kSlabA1 + kSlabB2) <= 2 * kSlabA2 + 3 * kSlabB2, "the ring fits");
+    half_tile<GLU>(rX, rW, SX + row0, SWt, Y + (int64_t)row0 * (GLU ? N / 2 : N), rows, wrows, n0, N, K,
+                   wv, lds);
     return;
   }
   const int wm = wv >> 1, wn = wv & 1;
@@ -714,67 +890,23 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
 #undef I8W_OFF
 #undef LDS_ADDR
 
-  float sw[kFN2];
-#pragma unroll
-  for (int j = 0; j < kFN2; ++j) {
-    const int n = weight_row<GLU>(wn * kWTN2 + j * 32 + (lane & 31));
-    sw[j] = SWt[n < wrows ? n : wrows - 1];
-  }
-  const int32_t NO = GLU ? N / 2 : N;
-  // Through LDS as bf16 rows (TN columns, the 16-byte chunk of column c of row
-  // r at (c / 8) ^ (((r / 4) % 4) * 4), so the half-waves' rows r and r + 4
-  // land on different banks), then 16-byte row stores; 2-byte stores where a
-  // row of Y is no whole number of vectors.
-  constexpr int TN = GLU ? kBN2 / 2 : kBN2;
-  const bool vec = (NO & 7) == 0;
-  const int32_t c0 = GLU ? n0 / 2 : n0;
-  uint16_t *so = reinterpret_cast<uint16_t *>(lds);
-  float *const ssx = reinterpret_cast<float *>(lds + kBM2 * kBN2 * 2 / 16);
-  __syncthreads();   // every wave is done with the slab buffers
-  ssx[tid] = SX[row0 + (tid < rows ? tid : rows - 1)];
-  __syncthreads();
-#define OSW(r_, cv_) ((r_) * TN + (((cv_) ^ ((((r_) >> 2) & 3) << 2)) << 3))
-#pragma unroll
-  for (int i = 0; i < kFM2; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int rr = wm * kWTM2 + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
-      const float sx = ssx[rr];
-      constexpr int kOut = GLU ? kFN2 / 2 : kFN2;
-#pragma unroll
-      for (int j = 0; j < kOut; ++j) {
-        float v;
-        if constexpr (GLU)
-          v = silu_mul((float)acc[i][2 * j][r] * (sx * sw[2 * j]),
-                       (float)acc[i][2 * j + 1][r] * (sx * sw[2 * j + 1]));
-        else
-          v = (float)acc[i][j][r] * (sx * sw[j]);
-        const int c = wn * (kOut * 32) + j * 32 + (lane & 31);
-        if (vec) so[OSW(rr, c >> 3) + (c & 7)] = bf16_bits(v);
-        else if (rr < rows && c0 + c < NO) Y[(int64_t)(row0 + rr) * NO + c0 + c] = bf16_bits(v);
-      }
-    }
-  if (!vec) return;
-  __syncthreads();
-  constexpr int kVecs = kBM2 * TN / 8;
-#pragma unroll 4
-  for (int q = 0; q < kVecs / kGemmThreads; ++q) {
-    const int idx = tid + q * kGemmThreads;
-    const int rr = idx / (TN / 8), cv = idx % (TN / 8), col = c0 + cv * 8;
-    if (rr < rows && col < NO)
-      *reinterpret_cast<u32x4 *>(Y + (int64_t)(row0 + rr) * NO + col) =
-          *reinterpret_cast<const u32x4 *>(so + OSW(rr, cv));
-  }
-#undef OSW
+  store_tile<GLU, kFM2, kFN2, 2>(acc, lds, SX + row0, SWt, Y + (int64_t)row0 * (GLU ? N / 2 : N), rows,
+                                 wrows, n0, N, wm, wn);
 }
 
-// Which kernel: 256 x 256 tiles with at least 128 rows an expert on average
-// (and N of a column tile); the streaming kernel with at most 32; 128 x 128
-// tiles between.
+// Which kernel, by the rows an expert has on average: the streaming kernel while
+// groups stay within its one pass of 64 rows over the weights, 256 x 256 tiles
+// (whose short tiles stream and whose half tiles take 128 rows) above; 128 x 128
+// tiles where N has no 256 columns.  Up to 56 rows where the large tiles are too
+// few units for 256 compute units (16 experts, K = 2048, N = 1024, 50 rows: 13.6
+// us streaming, 28.8 in large tiles; 64 rows, K = 4096, N = 2048: 77 and 54), up
+// to 16 elsewhere: 256 experts, K = 7168, N = 4096, even groups of 19 rows 1167 us
+// and 1196, of 32 rows 1256 and 1258, skewed ones of 32 on average 1196 and 749.
 enum class I8Kernel { kStream, kTiles, kWide };
 static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
-  if (g.n >= (int64_t)(kBM2 / 2) * g.E && N >= kBN2) return I8Kernel::kWide;
-  return g.n <= (int64_t)32 * g.E ? I8Kernel::kStream : I8Kernel::kTiles;
+  const bool fills = N >= kBN2 && (int64_t)g.E * ((N + kBN2 - 1) / kBN2) >= 256;
+  if (g.n <= (int64_t)(fills ? 16 : 56) * g.E) return I8Kernel::kStream;
+  return N >= kBN2 ? I8Kernel::kWide : I8Kernel::kTiles;
 }
 // The streaming kernel splits K while the groups that can have rows, times
 // their column tiles, are few units for the 1024 waves the GPU holds of it.

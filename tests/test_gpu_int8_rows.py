@@ -171,7 +171,7 @@ def test_gemm_int8(layout, R, cap, S, T, E, k, K, N, glu):
     _check_gemm(layout, R, cap, S, T, E, k, K, N, glu, hot=2 if T == 300 else None)
 
 
-# at least 128 rows an expert and N >= 256: the large tiles; full, short and single-row tails
+# many rows an expert and N >= 256: the large tiles; full, short and single-row tails
 @pytest.mark.parametrize("glu", [False, True])
 @pytest.mark.parametrize("T,E,k,K,N,hot", [(1030, 4, 2, 64, 256, None), (1500, 4, 2, 128, 272, 1),
                                            (700, 4, 4, 192, 512, 3), (520, 2, 2, 1088, 336, None),
@@ -179,6 +179,17 @@ def test_gemm_int8(layout, R, cap, S, T, E, k, K, N, glu):
 def test_gemm_int8_large_groups(T, E, k, K, N, hot, glu):
     print(f"[gemm int8] T={T} E={E} k={k} K={K} N={N} glu={glu}", flush=True)
     _check_gemm("ht", 1, 0, 0, T, E, k, K, N, glu, hot=hot)
+
+
+# tiles of 65 to 128 rows, and shorter ones beside them; one to nine slabs of K
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("layout,cap,T,E,k,K,N,hot", [
+    ("ht", 0, 190, 4, 2, 64, 256, None), ("ht", 0, 190, 4, 2, 128, 272, 1), ("ht", 0, 220, 4, 2, 192, 512, None),
+    ("ll", 128, 200, 4, 2, 256, 288, None), ("ht", 0, 230, 4, 2, 1088, 336, 3), ("ht", 0, 70, 1, 1, 384, 256, None),
+    ("ll", 66, 400, 2, 1, 448, 256, None), ("ht", 0, 160, 64, 8, 256, 1024, 5)])
+def test_gemm_int8_half_tiles(layout, cap, T, E, k, K, N, hot, glu):
+    print(f"[gemm int8] {layout} T={T} E={E} k={k} K={K} N={N} glu={glu}", flush=True)
+    _check_gemm(layout, 1, cap, 0, T, E, k, K, N, glu, hot=hot)
 
 
 @pytest.mark.parametrize("N", [1, 7, 20, 100, 257, 300])
