@@ -544,11 +544,12 @@ _NORM_RULES: dict = {}
 
 
 def _norm_rule(eps: float, quant: str | int) -> int:
-    """Address of the ep_norm_rule_t of these values (kept for the process's life)."""
+    """Address of the ep_norm_rule_t of these values (kept for the process's
+    life; threads that meet the values together get the same one)."""
     r = _NORM_RULES.get((eps, quant))
     if r is None:
         q = _QUANTS[quant] if isinstance(quant, str) else int(quant)
-        r = _NORM_RULES[(eps, quant)] = ep_norm_rule_t(eps, q, 0)
+        r = _NORM_RULES.setdefault((eps, quant), ep_norm_rule_t(eps, q, 0))
     return ctypes.addressof(r)
 
 
