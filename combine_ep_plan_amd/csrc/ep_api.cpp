@@ -884,8 +884,8 @@ ep_status_t ep_route_scored_bwd(ep_handle_t h, const ep_route_rule_t *rule,
       as_stream(stream)));
 }
 
-// Rows of a [.., H] tensor the row kernels take (H a multiple of 8, at most
-// kRowMaxChannels; rows an int32); false if it is no such tensor.
+// Rows of a [.., H] tensor that passed check_tensor, if the row kernels take
+// it (H a multiple of 8, rows an int32); false if they do not.
 static bool row_tensor(const ep_tensor_t *t, int64_t *rows, int64_t *H) {
   if (t->ndim < 2) return false;
   *H = t->sizes[t->ndim - 1];
@@ -984,10 +984,11 @@ ep_status_t ep_add_rmsnorm_bwd(const ep_norm_rule_t *rule, const ep_tensor_t *hi
                                ep_tensor_t *grad_weight, ep_tensor_t *workspace, void *stream) {
   if (!norm_rule_ok(rule) || rule->quant != EP_QUANT_NONE || !hidden) return EP_ERR_INVALID_ARG;
   epk::RmsNormBwd n{};
+  n.h_fp32 = hidden->dtype == EP_DTYPE_FP32;
+  ep_status_t st = check_tensor(hidden, EP_TAG_TOKENS, n.h_fp32 ? EP_DTYPE_FP32 : EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
   int64_t T, H;
   if (!row_tensor(hidden, &T, &H)) return EP_ERR_BAD_SHAPE;
-  ep_status_t st = check_stream_rows(hidden, T, H, &n.h_fp32);
-  if (st != EP_OK) return st;
   if (H > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
   st = check_norm_weight(weight, H, &n.w_fp32);
   if (st != EP_OK) return st;
