@@ -848,7 +848,7 @@ ep_status_t ep_route_scored(ep_handle_t h, const ep_route_rule_t *rule, const ep
     st = check_2d(scores, EP_TAG_ROUTER_LOGITS, EP_DTYPE_FP32, g.T, g.E);
     if (st != EP_OK) return st;
   }
-  if (g.T >= 1 << 26) return EP_ERR_UNSUPPORTED;   // a launch counts its threads in 32 bits
+  if (!epk::route_scored_fits(g)) return EP_ERR_UNSUPPORTED;
   return hip_status(epk::launch_route_scored(
       g, *rule, logits->data, bf16, bias ? static_cast<const float *>(bias->data) : nullptr,
       static_cast<int32_t *>(topk_idx->data), static_cast<float *>(topk_weights->data),
@@ -876,7 +876,7 @@ ep_status_t ep_route_scored_bwd(ep_handle_t h, const ep_route_rule_t *rule,
   }
   st = check_2d(grad_logits, EP_TAG_ROUTER_LOGITS, logits->dtype, g.T, g.E);
   if (st != EP_OK) return st;
-  if (g.T >= 1 << 26) return EP_ERR_UNSUPPORTED;
+  if (!epk::route_scored_fits(g)) return EP_ERR_UNSUPPORTED;
   return hip_status(epk::launch_route_scored_bwd(
       g, h->ws, *rule, logits->data, bf16, static_cast<const int32_t *>(topk_idx->data),
       static_cast<const float *>(grad_topk_weights->data),

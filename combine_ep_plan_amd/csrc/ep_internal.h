@@ -131,6 +131,7 @@ hipError_t launch_grouped_gemm_int8(const Geometry &g, const Workspace &ws, cons
 hipError_t launch_dispatch_rows8(const Geometry &g, const Workspace &ws, const uint8_t *x,
                                  const float *xs, int32_t H, int32_t S, uint8_t *recv,
                                  float *recv_s, hipStream_t s);
+bool route_scored_fits(const Geometry &g);
 hipError_t launch_route_scored(const Geometry &g, const ep_route_rule_t &r, const void *logits,
                                bool bf16, const float *bias, int32_t *idx, float *w, float *scores,
                                hipStream_t s);

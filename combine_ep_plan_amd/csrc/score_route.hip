@@ -568,6 +568,13 @@ static unsigned score_blocks(int32_t T, int G) {
   return (unsigned)((T + per - 1) / per);
 }
 
+// T < 2^26, and a launch counts its threads in 32 bits: with a wave a token
+// (E > 256) workgroups of 256 threads for four tokens, up to 2^26 - 4 of them.
+bool route_scored_fits(const Geometry &g) {
+  const int G = wave_per_token(g.T, g.E, kManyForward) ? 64 : 16;
+  return g.T < 1 << 26 && (int64_t)score_blocks(g.T, G) * (64 * kScoreWaves) <= (int64_t)UINT32_MAX;
+}
+
 hipError_t launch_route_scored(const Geometry &g, const ep_route_rule_t &r, const void *logits,
                                bool bf16, const float *bias, int32_t *idx, float *w, float *scores,
                                hipStream_t s) {

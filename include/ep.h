@@ -621,7 +621,7 @@ typedef struct ep_route_rule {
  *               balance loss.
  * T, E and k are the handle's; needs no ep_plan.  Errors:
  * EP_ERR_INVALID_ARG for a rule outside the ranges above, EP_ERR_UNSUPPORTED
- * for T >= 2^26. */
+ * for T >= 2^26, and for T > 2^26 - 4 with E > 256. */
 ep_status_t ep_route_scored(ep_handle_t h, const ep_route_rule_t *rule, const ep_tensor_t *logits,
                             const ep_tensor_t *bias, ep_tensor_t *topk_idx,
                             ep_tensor_t *topk_weights, ep_tensor_t *scores, void *stream);

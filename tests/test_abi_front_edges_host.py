@@ -54,3 +54,25 @@ def test_norm_bwd_checks_hidden_like_the_other_tensors(lib):  # noqa: F811
     assert f(norm_rule(), view(BF16, T_, 256), w, h, None, h, None, None, None) == SHAPE
     assert f(norm_rule(), view(BF16, T_, 4, 252), w, h, None, h, None, None, None) == SHAPE
     assert f(norm_rule(), view(BF16, T_, -4, 256), w, h, None, h, None, None, None) == SHAPE
+
+
+def _route_handle(lib, T, E):  # noqa: F811
+    """A handle of T tokens on memory that is never touched."""
+    from tests.test_abi_host import FAKE, create
+    rc, g = create(lib, num_experts=E, num_ranks=1, hidden=64, max_tokens=T)
+    assert rc == OK
+    h = ctypes.c_void_p()
+    assert lib.ep_handle_create(g, T, FAKE, 1 << 40, ctypes.byref(h)) == OK
+    return h
+
+
+@pytest.mark.parametrize("T", [(1 << 26) - 3, (1 << 26) - 1])
+def test_route_counts_the_threads_it_launches(lib, T):  # noqa: F811
+    """More than 256 experts: a wave a token, four to a workgroup; 2^24
+    workgroups of 256 threads are past 32 bits."""
+    E = 257
+    h = _route_handle(lib, T, E)
+    rule = ep.RouteRule().ptr
+    lg, i, w = view(FP32, ep.TAG_ROUTER_LOGITS, T, E), view(3, ep.TAG_TOPK_IDX, T, 2), view(FP32, ep.TAG_TOPK_WEIGHTS, T, 2)
+    assert lib.ep_route_scored(h, rule, lg, None, i, w, None, None) == UNSUPPORTED
+    assert lib.ep_route_scored_bwd(h, rule, lg, i, w, None, lg, None) == UNSUPPORTED
