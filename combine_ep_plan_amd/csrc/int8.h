@@ -35,13 +35,12 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
 // ties to even; inv = 1 / s.  Adding 1.5 * 2^23 to y * inv in one fma leaves the
 // rounded quotient in the low mantissa bits (its low byte is the code); it is
 // off by one at most, and only next to a tie, since y * inv is within 2^-16 of
-// the quotient.  r = y - q*s is exact (q has 7 bits and |r| stays near s/2), so
-// one comparison of the largest |r| of the eight with s / 2 tells whether any
-// needs the settling below: a few in ten thousand do.  |y| <= amax keeps q
-// within 127.
+// the quotient.  r = y - q*s is exact (q has 7 bits and |r| stays near s/2), and
+// so is 2r (s/2 is not, below 2^-125), so one comparison of twice the largest
+// |r| of the eight with s tells whether any needs the settling below: a few in
+// ten thousand do.  |y| <= amax keeps q within 127.
 __device__ __forceinline__ u32x2 int8_codes(const float y[8], float s, float inv) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  const float half = 0.5f * s;
   float t[8], worst = 0.0f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -49,12 +48,12 @@ __device__ __forceinline__ u32x2 int8_codes(const float y[8], float s, float inv
     const float q = t[c] - kMagic;
     worst = fmaxf(worst, fabsf(__builtin_fmaf(-q, s, y[c])));
   }
-  if (worst >= half) {
+  if (worst + worst >= s) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float q = t[c] - kMagic, r = __builtin_fmaf(-q, s, y[c]), a = fabsf(r);
+      const float q = t[c] - kMagic, r = __builtin_fmaf(-q, s, y[c]), a2 = fabsf(r + r);
       const bool odd = (__float_as_uint(t[c]) & 1u) != 0u;
-      if (a > half || (a == half && odd)) t[c] += r > 0.0f ? 1.0f : -1.0f;
+      if (a2 > s || (a2 == s && odd)) t[c] += r > 0.0f ? 1.0f : -1.0f;
     }
   }
   uint32_t w[2];
