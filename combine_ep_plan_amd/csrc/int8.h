@@ -15,20 +15,21 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // Scale of a row (or of an FP8 block) whose largest magnitude is amax, from
 // the quotient of amax and the format's largest code: 1 for a row of zeros,
 // NaN for one that holds a value that is not finite (its codes are then 0, so
-// what it stands for is NaN, not a plausible number).  The scale stays at
-// 2^-126 or above, so that its reciprocal is finite.
-__device__ __forceinline__ float scale_of(uint32_t amax_bits, float quotient) {
+// what it stands for is NaN, not a plausible number), and never below `least`.
+__device__ __forceinline__ float scale_of(uint32_t amax_bits, float quotient, float least) {
   if (amax_bits >= kInfBits) return __uint_as_float(0x7FC00000u);
   if (amax_bits == 0u) return 1.0f;
-  return fmaxf(quotient, 1.17549435e-38f);
+  return fmaxf(quotient, least);
 }
 // INT8: times the rounded 1/127 -- a scale is free to be a last bit off, the
-// codes are decided against it -- FP8: the division its format is defined by.
+// codes are decided against it -- and at least 2^-126, so that its reciprocal is
+// finite.  FP8: the division its format is defined by, subnormal ones too (the
+// codes divide); at least the smallest float, where the quotient rounds to 0.
 __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
-  return scale_of(amax_bits, __uint_as_float(amax_bits) * (1.0f / 127.0f));
+  return scale_of(amax_bits, __uint_as_float(amax_bits) * (1.0f / 127.0f), 1.17549435e-38f);
 }
 __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
-  return scale_of(amax_bits, __uint_as_float(amax_bits) / 448.0f);
+  return scale_of(amax_bits, __uint_as_float(amax_bits) / 448.0f, __uint_as_float(1u));
 }
 
 // Eight codes in memory order: the integer nearest to the exact quotient y / s,

@@ -145,7 +145,7 @@ __device__ __forceinline__ u32x2 fp8_codes(const float y[8], float *scale, bool 
   a = row_max(a);
   float s = fp8_scale(a);
   if (pow2 && a != 0u && a < kInfBits) {
-    const uint32_t b = __float_as_uint(s);
+    const uint32_t b = __float_as_uint(s);   // subnormal ones end at 2^-126
     if (b & 0x007FFFFFu) s = __uint_as_float((b & 0x7F800000u) + 0x00800000u);
   }
   *scale = s;

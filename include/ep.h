@@ -677,11 +677,11 @@ typedef struct ep_norm_rule {
  * codes, scales: given if and only if rule.quant is not NONE: the rows in 8
  *               bits, quantised from the fp32 y.  FP8: e4m3 [T, H] and fp32
  *               [T, H/128] (tag FP8_SCALES), H % 128 == 0, the FP8 dispatch's
- *               recipe.  INT8: int8 [T, H] and fp32 [T] (tag ROW_SCALES):
- *               scale = amax * fp32(1/127) (1 for a row of zeros, at least
- *               2^-126), code = the integer nearest to y / scale, ties to even.  A row
- *               (FP8: a block) with a value that is not finite gets codes 0
- *               and a NaN scale.
+ *               recipe (the scale at least 2^-149).  INT8: int8 [T, H] and
+ *               fp32 [T] (tag ROW_SCALES): scale = amax * fp32(1/127) (1 for a
+ *               row of zeros, at least 2^-126), code = the integer nearest to
+ *               y / scale, ties to even.  A row (FP8: a block) with a value
+ *               that is not finite gets codes 0 and a NaN scale.
  * At least one of y and codes is given.  Enqueues one kernel. */
 ep_status_t ep_add_rmsnorm(const ep_norm_rule_t *rule, const ep_tensor_t *x,
                            const ep_tensor_t *residual, const ep_tensor_t *weight,
