@@ -135,17 +135,27 @@ def library_path() -> str:
     return os.environ.get("EP_MI355X_LIB") or os.path.join(_HERE, _LIB_NAME)
 
 
+def _without_marshal(why: ImportError):
+    """What stands for the marshalling module where it cannot be loaded (it is
+    bound to the torch it was built with): the calls that need it say so."""
+    reason = str(why)   # the exception itself would keep its frames
+
+    def call(*_):
+        raise RuntimeError(f"combine_ep_plan_amd._marshal cannot be loaded ({reason}): build it with"
+                           " `python -m combine_ep_plan_amd.build` (there is no fallback path)")
+    return call
+
+
 def load_library():
-    """Load libep_mi355x.so and the marshalling module (raises if they have
-    not been built)."""
+    """Load libep_mi355x.so (raises if it has not been built) and the
+    marshalling module (without it the entry points it marshals raise)."""
     global _lib, _marshal_call
     if _lib is not None:
         return _lib
     path = library_path()
-    for f in (path, os.path.join(_HERE, "_marshal.so")):
-        if not os.path.exists(f):
-            raise RuntimeError(f"{f} is missing: build it with `python -m combine_ep_plan_amd.build`"
-                               " (there is no fallback path)")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m combine_ep_plan_amd.build`"
+                           " (there is no fallback path)")
     lib = ctypes.CDLL(path)
     S = c_int32
     sig = {
@@ -189,8 +199,11 @@ def load_library():
         fn.restype = res
         fn.argtypes = args
         _entry[name] = ctypes.cast(fn, c_void_p).value
-    from . import _marshal
-    _marshal_call = _marshal.call
+    try:
+        from . import _marshal
+        _marshal_call = _marshal.call
+    except ImportError as e:
+        _marshal_call = _without_marshal(e)
     _lib = lib
     return lib
 

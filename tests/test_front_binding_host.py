@@ -4,10 +4,12 @@ hands to the library and what it needs to load.  No GPU."""
 from __future__ import annotations
 
 import ctypes
+import subprocess
 import sys
 import threading
 
 import combine_ep_plan_amd as ep
+from tests.test_abi_host import ROOT
 
 
 def test_norm_rules_are_one_object_whatever_thread_asks_first():
@@ -37,3 +39,27 @@ def test_norm_rules_are_one_object_whatever_thread_asks_first():
     for g in got:
         assert g == kept
     assert all(ep.ep_norm_rule_t.from_address(a).eps == e for a, e in zip(kept, eps))
+
+
+NO_MARSHAL = """
+import sys
+import torch
+sys.modules["combine_ep_plan_amd._marshal"] = None   # as where it is not built, or for another torch
+import combine_ep_plan_amd as ep
+ep.load_library()
+assert ep.ep_status_string(0) == "EP_OK"
+g = ep.Group(8, 1, 256, 2, 16, "ht")
+assert g.recv_shape(16)[-1] == 256
+x = torch.zeros(4, 64, dtype=torch.bfloat16)
+try:
+    ep.Buffer.quantize_int8(x)
+except RuntimeError as e:
+    print(e)
+"""
+
+
+def test_the_library_loads_without_the_marshalling_module():
+    """Only the entry points that are marshalled in C++ need it, and they say so."""
+    out = subprocess.run([sys.executable, "-c", NO_MARSHAL], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert "_marshal" in out.stdout and "python -m combine_ep_plan_amd.build" in out.stdout
