@@ -888,12 +888,14 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
     if (!half) mfma_i8_rows<0, NBK>(acc, fa0, fb0);                                            \
     mfma_i8_rows<0, NBK>(acc, fa1, fb1);                                                       \
   }
+  // a wave's 32-row blocks that hold rows: one at least, the tile has more than
+  // kHalfRows
+  static_assert(kHalfRows >= kWTM2, "both wave rows hold rows of the tile");
   const int live = (rows - wm * kWTM2 + 31) / 32;  // wave-uniform
   if (live >= kFM2) I8W_LOOP(kFM2)
   else if (live == 3) I8W_LOOP(3)
   else if (live == 2) I8W_LOOP(2)
-  else if (live == 1) I8W_LOOP(1)
-  else I8W_LOOP(0)
+  else I8W_LOOP(1)
 #undef I8W_LOOP
 #undef I8W_SLAB
 #undef I8W_STEP
