@@ -270,6 +270,20 @@ def _stream(stream):
     return c_void_p(int(stream))
 
 
+def _stream_object(stream) -> torch.cuda.Stream | None:
+    """The Stream of a call's stream argument: None, a Stream or an address."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream))
+
+
+def _event_on(stream) -> torch.cuda.Event:
+    """An event behind what a call has enqueued."""
+    ev = torch.cuda.Event()
+    ev.record(_stream_object(stream) or torch.cuda.current_stream())
+    return ev
+
+
 def _hold(obj) -> None:
     """A prepared call holds on to what it points to."""
     keep = getattr(_RECORDING, "keep", None)
@@ -864,8 +878,7 @@ class Buffer:
             ep_plan_dispatch(handle.ptr, topk_idx, x, topk_weights, recv, scales, ri, rw, stream)
         else:
             ep_dispatch(handle.ptr, x, topk_weights, recv, scales, ri, rw, stream)
-        ev = torch.cuda.Event()
-        ev.record(torch.cuda.current_stream() if stream is None else stream)
+        ev = _event_on(stream)
         recv_x = (recv, scales) if fp8 else recv
         return recv_x, ri, rw, handle, ev
 
@@ -978,8 +991,7 @@ class Buffer:
         gw = torch.empty(H, dtype=torch.float32, device=hidden.device)
         if workspace is None:
             n = ep_add_rmsnorm_bwd_workspace_bytes(hidden.numel() // H, H) // 4
-            on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-            with torch.cuda.stream(on):   # let go of on return: the memory is the call's stream's
+            with torch.cuda.stream(_stream_object(stream)):   # let go of on return: the memory is the call's stream's
                 workspace = torch.empty(n, dtype=torch.float32, device=hidden.device)
         ep_add_rmsnorm_bwd(hidden, weight, grad_y, grad_residual_out, grad, gw, workspace, eps, stream)
         return grad, gw
@@ -1010,8 +1022,7 @@ class Buffer:
         ri = torch.empty(rows, dtype=torch.int32, device=dev) if recv_meta else None
         rw = torch.empty(rows, dtype=torch.float32, device=dev) if recv_meta and topk_weights is not None else None
         ep_dispatch_quantized(handle.ptr, codes, scales, topk_weights, recv, rs, ri, rw, stream)
-        ev = torch.cuda.Event()
-        ev.record(torch.cuda.current_stream() if stream is None else stream)
+        ev = _event_on(stream)
         return (recv, rs), ri, rw, handle, ev
 
     def expert_gemm_int8(self, recv: torch.Tensor, recv_scales: torch.Tensor,
