@@ -8,9 +8,10 @@
 // by its writes.  One workgroup per token (per piece of a row for small
 // batches), 16-byte loads and stores; the stores cached or non-temporal by the
 // group's dispatch_stores, as in dispatch.hip.  Prefill (4096 x 7168, top-8):
-// 41-51 us cached (the rows in the Infinity Cache for the next kernel or
-// not), 47 streaming; with the INT8 GEMM behind it the pair is 0-2% faster
-// cached.
+// INT8 rows 52 us with cached stores where successive calls write other buffers,
+// 40 where they write the same one (its lines are still in the Infinity Cache),
+// 46 streaming; FP8 rows 59, 42 and 46.  With the INT8 GEMM behind it the pair is
+// 0-2% faster cached, so that is the default at this size.
 #include "device.h"
 #include "ep_internal.h"
 

@@ -929,7 +929,12 @@ static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
   return N >= kBN2 ? I8Kernel::kWide : I8Kernel::kTiles;
 }
 // The streaming kernel splits K while the groups that can have rows, times
-// their column tiles, are few units for the 1024 waves the GPU holds of it.
+// their column tiles, are few units: the GPU holds 2048 of its waves (1536 with
+// the larger ring), and a wave by itself takes 48 us for K = 7168 however few
+// there are.  K = 7168, two rows an expert, split and not: 20.9 and 48.9 us with
+// 256 units, 31.8 and 49.9 with 384, 34.8 and 50.5 with 512, 56.9 and 52.4 with
+// 768, 67.8 and 66.2 with 1024.  (K = 2048: 12.3 and 17.4 with 384, 20.2 and 18.2
+// with 768; eight rows an expert on 512 units: 19.4 and 19.6.)
 constexpr int64_t kStreamWaves = 512;
 static bool stream_split(const Geometry &g, int64_t ncol) {
   return (g.n < g.E ? g.n : g.E) * ncol < kStreamWaves;

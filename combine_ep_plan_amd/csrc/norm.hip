@@ -321,7 +321,10 @@ hipError_t launch_add_rmsnorm(const RmsNorm &n, hipStream_t s) {
 // result does not depend on scheduling.  16384 x 4096: 90 + 5 us, 5.9 TB/s.
 
 // Threads of a backward row, vectors a thread, rows a workgroup takes at a time
-// (narrow rows share one, so that there are few partial rows of grad_w).
+// (narrow rows share one, so that there are few partial rows of grad_w).  Rows
+// longer than 8192 channels have two or four vectors a thread and 1024 threads,
+// whose 128 registers do not hold them: 22 and 183 are spilled in bf16, 38 and 318
+// in fp32 (4096 x 12288: 132 and 243 us, 3.0 TB/s; 4096 x 20480: 610 and 811).
 struct BwdShape {
   int threads, vpt, rows;
 };

@@ -762,7 +762,9 @@ ep_status_t ep_dispatch_quantized(ep_handle_t h, const ep_tensor_t *tokens,
  * out:            bf16 [recv_rows, N], tag TOKENS; rows no group covers are
  *                 not written.
  * Errors: as for ep_expert_gemm_fp8; EP_ERR_UNSUPPORTED for K > 131071 or a
- * launch too large for one grid.  Enqueues two kernels (tile table, GEMM). */
+ * launch too large for one grid.  Enqueues two kernels (tile table, GEMM), or
+ * the GEMM alone for few rows an expert where T, or LL's capacity, is at most
+ * 128. */
 ep_status_t ep_expert_gemm_int8(ep_handle_t h, const ep_tensor_t *recv_tokens,
                                 const ep_tensor_t *recv_scales, const ep_tensor_t *expert_weights,
                                 const ep_tensor_t *expert_scales, const ep_tensor_t *slot_weights,
