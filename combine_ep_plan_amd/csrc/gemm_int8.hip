@@ -922,6 +922,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_grouped_gemm_i8_256(
 // us streaming, 28.8 in large tiles; 64 rows, K = 4096, N = 2048: 77 and 54), up
 // to 16 elsewhere: 256 experts, K = 7168, N = 4096, even groups of 19 rows 1167 us
 // and 1196, of 32 rows 1256 and 1258, skewed ones of 32 on average 1196 and 749.
+// Below: even groups of 4, 8 and 16 rows 1125, 1151, 1174 streaming and 1127, 1145,
+// 1155 in large tiles (K = 2048, N = 7168, of 4 and 16: 585, 700 and 612, 638),
+// skewed batches of 4, 8 and 16 on average 316, 490, 739 and 323, 421, 530: the
+// streaming kernel reads a hot expert's weights once for every 64 of its rows.
 enum class I8Kernel { kStream, kTiles, kWide };
 static I8Kernel i8_kernel(const Geometry &g, int32_t N) {
   const bool fills = N >= kBN2 && (int64_t)g.E * ((N + kBN2 - 1) / kBN2) >= 256;
