@@ -13,7 +13,9 @@ paper (listing, Table II and Figure 2), and ``Buffer.dispatch`` returns
 ``recv_x, recv_i, recv_w, handle, event`` like that paper's Table V.
 ``Buffer.add_rmsnorm``, ``Handle.route_scored``, ``Buffer.dispatch_quantized``,
 ``Buffer.expert_gemm_int8`` and ``Buffer.quantize_int8`` are the layer's front
-and its INT8 path; their arguments are marshalled in C++ (``_marshal``).
+and its INT8 path; ``Buffer.dropout``, ``Buffer.add_layernorm``,
+``Buffer.quantize_fp8_2d`` and ``Buffer.linear_fp8`` its dense half.  Their
+arguments are marshalled in C++ (``_marshal``).
 """
 
 from __future__ import annotations
@@ -41,6 +43,8 @@ __all__ = [
     "RouteRule", "ep_route_scored", "ep_route_scored_bwd", "ep_add_rmsnorm", "ep_add_rmsnorm_bwd",
     "ep_add_rmsnorm_bwd_workspace_bytes", "ep_quantize_int8", "ep_dispatch_quantized",
     "ep_expert_gemm_int8", "ep_expert_gemm_int8_swiglu",
+    "rng_state", "ep_dropout", "ep_add_layernorm", "ep_add_layernorm_bwd",
+    "ep_add_layernorm_bwd_workspace_bytes", "ep_quantize_fp8_2d", "ep_linear_fp8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,7 +55,7 @@ _LAYOUTS = {"ll": LAYOUT_LL, "ht": LAYOUT_HT, "static": LAYOUT_STATIC}
 FLAG_INDEX_RANGE, FLAG_CAPACITY, FLAG_SLOT_BUDGET, FLAG_PLAN_STALL, FLAG_SCALE_FORMAT = 1, 2, 4, 8, 16
 TAG_TOKENS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS, TAG_FP8_SCALES, TAG_EXPERT_GRADS = 0, 1, 2, 3, 4
 TAG_ROUTER_LOGITS, TAG_EXPERT_WEIGHTS, TAG_ROW_SCALES, TAG_ROUTER_BIAS = 5, 6, 7, 8
-TAG_NORM_WEIGHT, TAG_WORKSPACE = 9, 10
+TAG_NORM_WEIGHT, TAG_WORKSPACE, TAG_RNG_STATE, TAG_STATUS = 9, 10, 11, 12
 SLOTS_TRAINING, SLOTS_INFERENCE = 0, 1
 _SLOT_MODES = {"training": SLOTS_TRAINING, "inference": SLOTS_INFERENCE}
 STORES_AUTO, STORES_CACHED, STORES_STREAMING = 0, 1, 2
@@ -65,6 +69,8 @@ GROUP_MAX, GROUP_TOP2 = 0, 1
 _GROUP_SCORES = {"max": GROUP_MAX, "top2": GROUP_TOP2}
 QUANT_NONE, QUANT_FP8, QUANT_FP8_POW2, QUANT_INT8 = 0, 1, 2, 3
 _QUANTS = {"none": QUANT_NONE, "fp8": QUANT_FP8, "fp8_pow2": QUANT_FP8_POW2, "int8": QUANT_INT8}
+BLOCK_ROWS, BLOCK_SQUARE = 0, 1
+_BLOCKS = {"rows": BLOCK_ROWS, "square": BLOCK_SQUARE}
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float8_e4m3fn: 2, torch.int32: 3, torch.int8: 4}
 _STATUS = ["EP_OK", "EP_ERR_INVALID_ARG", "EP_ERR_BAD_TAG", "EP_ERR_BAD_DTYPE",
            "EP_ERR_BAD_SHAPE", "EP_ERR_NOT_PLANNED", "EP_ERR_WORKSPACE_TOO_SMALL",
@@ -102,7 +108,8 @@ _OPS = {"ep_route": 1, "ep_route_plan": 2, "ep_plan": 3, "ep_dispatch": 4, "ep_p
         "ep_expert_gemm_fp8": 13, "ep_expert_gemm_fp8_swiglu": 14, "ep_route_scored": 15,
         "ep_route_scored_bwd": 16, "ep_add_rmsnorm": 17, "ep_add_rmsnorm_bwd": 18,
         "ep_quantize_int8": 19, "ep_dispatch_quantized": 20, "ep_expert_gemm_int8": 21,
-        "ep_expert_gemm_int8_swiglu": 22}
+        "ep_expert_gemm_int8_swiglu": 22, "ep_dropout": 23, "ep_add_layernorm": 24,
+        "ep_add_layernorm_bwd": 25, "ep_quantize_fp8_2d": 26, "ep_linear_fp8": 27}
 
 
 class ep_route_rule_t(ctypes.Structure):
@@ -112,6 +119,23 @@ class ep_route_rule_t(ctypes.Structure):
 
 class ep_norm_rule_t(ctypes.Structure):
     _fields_ = [("eps", ctypes.c_double), ("quant", c_int32), ("reserved", c_int32)]
+
+
+class ep_dropout_rule_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double)]
+
+
+class ep_layernorm_rule_t(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("dropout", ctypes.c_double), ("quant", c_int32),
+                ("reserved", c_int32)]
+
+
+class ep_fp8_2d_rule_t(ctypes.Structure):
+    _fields_ = [("fp8_scales", c_int32), ("block", c_int32)]
+
+
+class ep_linear_rule_t(ctypes.Structure):
+    _fields_ = [("fp8_scales", c_int32), ("swiglu", c_int32)]
 
 
 class ep_handle_view_t(ctypes.Structure):
@@ -124,7 +148,7 @@ class ep_handle_view_t(ctypes.Structure):
 
 
 _lib = None
-_marshal_call = None             # the C++ marshalling (csrc/marshal.cpp) and the addresses it calls
+_marshal_call = _marshal_views = None   # the C++ marshalling (csrc/marshal.cpp) and the addresses it calls
 _entry: dict[str, int] = {}
 _T = POINTER(ep_tensor_t)
 
@@ -149,7 +173,7 @@ def _without_marshal(why: ImportError):
 def load_library():
     """Load libep_mi355x.so (raises if it has not been built) and the
     marshalling module (without it the entry points it marshals raise)."""
-    global _lib, _marshal_call
+    global _lib, _marshal_call, _marshal_views
     if _lib is not None:
         return _lib
     path = library_path()
@@ -192,6 +216,12 @@ def load_library():
         "ep_dispatch_quantized": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
         "ep_expert_gemm_int8": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
         "ep_expert_gemm_int8_swiglu": (S, [c_void_p, _T, _T, _T, _T, _T, _T, _T, c_void_p]),
+        "ep_dropout": (S, [POINTER(ep_dropout_rule_t), _T, _T, _T, _T, c_void_p]),
+        "ep_add_layernorm": (S, [POINTER(ep_layernorm_rule_t), c_void_p, c_void_p]),
+        "ep_add_layernorm_bwd_workspace_bytes": (S, [c_int64, c_int32, POINTER(c_size_t)]),
+        "ep_add_layernorm_bwd": (S, [POINTER(ep_layernorm_rule_t), c_void_p, c_void_p]),
+        "ep_quantize_fp8_2d": (S, [POINTER(ep_fp8_2d_rule_t), _T, _T, _T, _T, _T, c_void_p]),
+        "ep_linear_fp8": (S, [POINTER(ep_linear_rule_t), _T, _T, _T, _T, _T, _T, _T, c_void_p]),
         "ep_run_calls": (S, [POINTER(ep_call_t), c_int32, POINTER(c_int32)]),
     }
     for name, (res, args) in sig.items():
@@ -201,9 +231,9 @@ def load_library():
         _entry[name] = ctypes.cast(fn, c_void_p).value
     try:
         from . import _marshal
-        _marshal_call = _marshal.call
+        _marshal_call, _marshal_views = _marshal.call, _marshal.call_views
     except ImportError as e:
-        _marshal_call = _without_marshal(e)
+        _marshal_call = _marshal_views = _without_marshal(e)
     _lib = lib
     return lib
 
@@ -602,6 +632,36 @@ def _call(name: str, tags: bytes, stream, *args) -> None:
         raise EpError(code, name)
 
 
+def _call_views(name: str, tags: bytes, stream, rule: int, *tensors) -> None:
+    """The same for entry points (rule, struct of views, stream): the struct's
+    members are the tensors' views in order."""
+    if _marshal_views is None:
+        load_library()
+    if _recorders and getattr(_RECORDING, "calls", None) is not None:
+        dev = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
+        members = (c_void_p * len(tags))(*(ctypes.cast(_tensor(t, tag, dev), c_void_p) for t, tag in zip(tensors, tags)))
+        _hold(members)
+        _enqueue(name, rule, ctypes.addressof(members), _stream(stream))
+        return
+    if stream is not None:
+        stream = ((stream.device_index, stream.cuda_stream) if isinstance(stream, torch.cuda.Stream)
+                  else (torch.cuda.current_device(), int(stream)))
+    code = _marshal_views(_entry[name], tags, stream, rule, *tensors)
+    if code:
+        raise EpError(code, name)
+
+
+_RULES: dict = {}
+
+
+def _rule(kind, *values) -> int:
+    """Address of the rule of these values (kept like the norm's)."""
+    r = _RULES.get((kind, values))
+    if r is None:
+        r = _RULES.setdefault((kind, values), kind(*values))
+    return ctypes.addressof(r)
+
+
 _TAGS_ROUTE = bytes((_ADDR, _ADDR, TAG_ROUTER_LOGITS, TAG_ROUTER_BIAS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS,
                      TAG_ROUTER_LOGITS))
 _TAGS_ROUTE_BWD = bytes((_ADDR, _ADDR, TAG_ROUTER_LOGITS, TAG_TOPK_IDX, TAG_TOPK_WEIGHTS,
@@ -688,6 +748,75 @@ def ep_expert_gemm_int8_swiglu(h: int, recv_tokens: torch.Tensor, recv_scales: t
                                out: torch.Tensor, stream=None) -> None:
     ep_expert_gemm_int8(h, recv_tokens, recv_scales, expert_weights, expert_scales, slot_weights,
                         slot_scales, out, stream, swiglu=True)
+
+
+_TAGS_DROPOUT = bytes((_ADDR, TAG_RNG_STATE, TAG_TOKENS, TAG_TOKENS, TAG_TOKENS))
+_TAGS_LAYERNORM = {i8: bytes((TAG_TOKENS, TAG_TOKENS, TAG_NORM_WEIGHT, TAG_NORM_WEIGHT, TAG_RNG_STATE,
+                              TAG_TOKENS, TAG_TOKENS, TAG_TOKENS, TAG_ROW_SCALES if i8 else TAG_FP8_SCALES))
+                   for i8 in (True, False)}
+_TAGS_LAYERNORM_BWD = bytes((TAG_TOKENS, TAG_NORM_WEIGHT, TAG_TOKENS, TAG_TOKENS, TAG_RNG_STATE, TAG_TOKENS,
+                             TAG_TOKENS, TAG_NORM_WEIGHT, TAG_NORM_WEIGHT, TAG_WORKSPACE))
+_TAGS_QUANTIZE_2D = bytes((_ADDR, TAG_TOKENS, TAG_TOKENS, TAG_FP8_SCALES, TAG_TOKENS, TAG_FP8_SCALES))
+_TAGS_LINEAR = bytes((_ADDR, TAG_TOKENS, TAG_FP8_SCALES, TAG_EXPERT_WEIGHTS, TAG_FP8_SCALES, TAG_TOKENS,
+                      TAG_TOKENS, TAG_STATUS))
+
+
+def rng_state(seed: int, offset: int = 0, device: torch.device | str | None = None) -> torch.Tensor:
+    """Dropout's generator state on the device: int32 [4], the words of two
+    64-bit numbers, low word first.  A program gives each use of a seed its own
+    offset; a captured graph reads the state anew at every replay."""
+    words = [(v >> s) & 0xFFFFFFFF for v in (int(seed), int(offset)) for s in (0, 32)]
+    return torch.tensor([w - (w >> 31 << 32) for w in words], dtype=torch.int32,
+                        device=device if device is not None else "cuda")
+
+
+def ep_dropout(x: torch.Tensor, residual: torch.Tensor | None, out: torch.Tensor, p: float,
+               rng: torch.Tensor, stream=None) -> None:
+    _call("ep_dropout", _TAGS_DROPOUT, stream, _rule(ep_dropout_rule_t, p), rng, x, residual, out)
+
+
+def ep_add_layernorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
+                     bias: torch.Tensor | None, residual_out: torch.Tensor | None,
+                     y: torch.Tensor | None, codes: torch.Tensor | None = None,
+                     scales: torch.Tensor | None = None, eps: float = 1e-5, quant: str | int = "none",
+                     dropout: float = 0.0, rng: torch.Tensor | None = None, stream=None) -> None:
+    q = _QUANTS[quant] if isinstance(quant, str) else int(quant)
+    i8 = codes is not None and codes.dtype == torch.int8
+    _call_views("ep_add_layernorm", _TAGS_LAYERNORM[i8], stream, _rule(ep_layernorm_rule_t, eps, dropout, q, 0),
+                x, residual, weight, bias, rng, residual_out, y, codes, scales)
+
+
+def ep_add_layernorm_bwd_workspace_bytes(rows: int, hidden: int) -> int:
+    out = c_size_t()
+    _check(load_library().ep_add_layernorm_bwd_workspace_bytes(rows, hidden, ctypes.byref(out)),
+           "ep_add_layernorm_bwd_workspace_bytes")
+    return out.value
+
+
+def ep_add_layernorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor,
+                         grad_residual_out: torch.Tensor | None, grad: torch.Tensor | None,
+                         grad_x: torch.Tensor | None, grad_weight: torch.Tensor | None,
+                         grad_bias: torch.Tensor | None, workspace: torch.Tensor | None,
+                         eps: float = 1e-5, dropout: float = 0.0, rng: torch.Tensor | None = None,
+                         stream=None) -> None:
+    _call_views("ep_add_layernorm_bwd", _TAGS_LAYERNORM_BWD, stream,
+                _rule(ep_layernorm_rule_t, eps, dropout, QUANT_NONE, 0), hidden, weight, grad_y,
+                grad_residual_out, rng, grad, grad_x, grad_weight, grad_bias, workspace)
+
+
+def ep_quantize_fp8_2d(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor | None,
+                       codes_t: torch.Tensor | None, scales_t: torch.Tensor | None,
+                       block: str | int = "rows", pow2: bool = False, stream=None) -> None:
+    b = _BLOCKS[block] if isinstance(block, str) else int(block)
+    _call("ep_quantize_fp8_2d", _TAGS_QUANTIZE_2D, stream, _rule(ep_fp8_2d_rule_t, int(pow2), b), x, codes,
+          scales, codes_t, scales_t)
+
+
+def ep_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                  addend: torch.Tensor | None, out: torch.Tensor, swiglu: bool = False,
+                  pow2: bool = False, status: torch.Tensor | None = None, stream=None) -> None:
+    _call("ep_linear_fp8", _TAGS_LINEAR, stream, _rule(ep_linear_rule_t, int(pow2), int(swiglu)), x, x_scales,
+          w, w_scales, addend, out, status)
 
 
 # ---------------------------------------------------------------------------
@@ -1039,6 +1168,92 @@ class Buffer:
             out = torch.empty((rows, N // 2 if swiglu else N), dtype=torch.bfloat16, device=recv.device)
         ep_expert_gemm_int8(handle.ptr, recv.view(rows, K), recv_scales.view(rows), expert_weights,
                             expert_scales, slots, slot_scales, out, stream, swiglu=swiglu)
+        return out
+
+    @staticmethod
+    def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, residual: torch.Tensor | None = None,
+                out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+        """Dropout of rows [..., H] from the generator state ``rng``
+        (``rng_state``), added to ``residual`` where there is one; of the
+        gradient with the same state: its backward.  The result has the
+        residual's type, or ``out_dtype`` (default: x's)."""
+        out = torch.empty_like(x, dtype=out_dtype or x.dtype) if residual is None else torch.empty_like(residual)
+        ep_dropout(x, residual, out, p, rng, stream)
+        return out
+
+    @staticmethod
+    def add_layernorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
+                      bias: torch.Tensor | None = None, eps: float = 1e-5, quant: str = "none",
+                      y: bool = True, dropout: float = 0.0, rng: torch.Tensor | None = None, stream=None):
+        """Dropout of x, residual addition and layer norm of bf16 rows [..., H]:
+        returns (hidden, y, codes, scales), None for what was not asked for
+        (hidden is x itself without residual and dropout).  ``quant``: "int8",
+        "fp8", "fp8_pow2"."""
+        hidden = torch.empty_like(residual) if residual is not None else torch.empty_like(x) if dropout else None
+        out = torch.empty_like(x) if y else None
+        codes = scales = None
+        if quant != "none":
+            i8 = quant == "int8"
+            codes = torch.empty(x.shape, dtype=torch.int8 if i8 else torch.float8_e4m3fn, device=x.device)
+            scales = torch.empty(tuple(x.shape[:-1]) + (() if i8 else (x.shape[-1] // 128,)),
+                                 dtype=torch.float32, device=x.device)
+        ep_add_layernorm(x, residual, weight, bias, hidden, out, codes, scales, eps, quant, dropout,
+                         rng if dropout else None, stream)
+        return x if hidden is None else hidden, out, codes, scales
+
+    @staticmethod
+    def add_layernorm_bwd(hidden: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor,
+                          grad_residual_out: torch.Tensor | None = None, eps: float = 1e-5,
+                          dropout: float = 0.0, rng: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+        """Gradients (of the residual, of x, of weight and bias in fp32); without
+        dropout the first two are one tensor."""
+        H = hidden.shape[-1]
+        grad = torch.empty_like(hidden)
+        grad_x = torch.empty(hidden.shape, dtype=torch.bfloat16, device=hidden.device) if dropout else None
+        gw = torch.empty(H, dtype=torch.float32, device=hidden.device)
+        gb = torch.empty(H, dtype=torch.float32, device=hidden.device)
+        if workspace is None:
+            n = ep_add_layernorm_bwd_workspace_bytes(hidden.numel() // H, H) // 4
+            with torch.cuda.stream(_stream_object(stream)):   # let go of on return: the memory is the call's stream's
+                workspace = torch.empty(n, dtype=torch.float32, device=hidden.device)
+        ep_add_layernorm_bwd(hidden, weight, grad_y, grad_residual_out, grad, grad_x, gw, gb, workspace, eps,
+                             dropout, rng if dropout else None, stream)
+        return grad, grad if grad_x is None else grad_x, gw, gb
+
+    @staticmethod
+    def quantize_fp8_2d(x: torch.Tensor, block: str = "rows", rows: bool = True, transposed: bool = True,
+                        pow2: bool = False, stream=None):
+        """A bf16 matrix [R, C] to e4m3 by blocks, and its transpose: returns
+        (codes, scales, codes_t, scales_t), None for what was not asked for.
+        ``block`` "rows": a scale per row and 128 channels (transposed: per
+        channel and 128 rows, the rows padded to 128 with zeros); "square": a
+        scale per 128 x 128 (weights)."""
+        R, C = x.shape
+        rb, sq, dev = (R + 127) // 128, block == "square", x.device
+        codes = scales = codes_t = scales_t = None
+        if rows:
+            codes = torch.empty((R, C), dtype=torch.float8_e4m3fn, device=dev)
+            scales = torch.empty((rb if sq else R, C // 128), dtype=torch.float32, device=dev)
+        if transposed:
+            codes_t = torch.empty((C, rb * 128), dtype=torch.float8_e4m3fn, device=dev)
+            scales_t = torch.empty((C // 128 if sq else C, rb), dtype=torch.float32, device=dev)
+        ep_quantize_fp8_2d(x, codes, scales, codes_t, scales_t, block, pow2, stream)
+        return codes, scales, codes_t, scales_t
+
+    @staticmethod
+    def linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                   addend: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   out_dtype: torch.dtype = torch.bfloat16, swiglu: bool = False, pow2: bool = False,
+                   status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """FP8 rows [..., K] (a scale per 128) times FP8 weights [N, K] (a scale
+        per 128 x 128 square, or per row and 128), plus ``addend``; ``swiglu`` as
+        in ``expert_gemm``.  ``pow2``: every scale is a power of two."""
+        N = w.shape[0]
+        if out is None:
+            dt = addend.dtype if addend is not None else out_dtype
+            out = torch.empty(tuple(x.shape[:-1]) + (N // 2 if swiglu else N,), dtype=dt, device=x.device)
+        ep_linear_fp8(x, x_scales, w, w_scales, addend, out, swiglu, pow2, status, stream)
         return out
 
     def dup_grad_reduce(self, replica_grads: torch.Tensor, owner_grads: torch.Tensor,

@@ -1166,6 +1166,295 @@ ep_status_t ep_expert_gemm_int8_swiglu(ep_handle_t h, const ep_tensor_t *recv_to
                           slot_scales, out, stream, true);
 }
 
+// ---------------------------------------------------------------------------
+// the dense half of a layer
+
+// The generator's view and probability of a call; p 0 with no state is no dropout.
+static ep_status_t check_dropout(double p, const ep_tensor_t *rng, epk::Dropout *d) {
+  if (!(p >= 0.0 && p <= 1.0)) return EP_ERR_INVALID_ARG;
+  const ep_status_t st = check_tensor(rng, EP_TAG_RNG_STATE, EP_DTYPE_INT32);
+  if (st != EP_OK) return st;
+  if (rng->ndim != 1 || rng->sizes[0] != 4) return EP_ERR_BAD_SHAPE;
+  d->rng = static_cast<const int32_t *>(rng->data);
+  d->threshold = (uint32_t)std::floor((1.0 - p) * 65536.0 + 0.5);
+  d->scale = d->threshold ? (float)(65536.0 / d->threshold) : 0.0f;
+  return EP_OK;
+}
+
+ep_status_t ep_dropout(const ep_dropout_rule_t *rule, const ep_tensor_t *rng, const ep_tensor_t *x,
+                       const ep_tensor_t *residual, ep_tensor_t *out, void *stream) {
+  if (!rule || !x || !out) return EP_ERR_INVALID_ARG;
+  epk::DropoutAdd n{};
+  ep_status_t st = check_dropout(rule->p, rng, &n.drop);
+  if (st != EP_OK) return st;
+  n.x_fp32 = x->dtype == EP_DTYPE_FP32;
+  st = check_tensor(x, EP_TAG_TOKENS, n.x_fp32 ? EP_DTYPE_FP32 : EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  int64_t T, H;
+  if (!row_tensor(x, &T, &H)) return EP_ERR_BAD_SHAPE;
+  st = check_stream_rows(out, T, H, &n.out_fp32);
+  if (st != EP_OK) return st;
+  if (residual) {
+    bool fp32;
+    st = check_stream_rows(residual, T, H, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.out_fp32) return EP_ERR_BAD_DTYPE;
+    n.residual = residual->data;
+  }
+  n.x = x->data;
+  n.out = out->data;
+  n.count = T * H;
+  return hip_status(epk::launch_dropout(n, as_stream(stream)));
+}
+
+static bool layernorm_rule_ok(const ep_layernorm_rule_t *r) {
+  return r && std::isfinite(r->eps) && r->eps >= (double)FLT_MIN && r->reserved == 0 &&
+         r->dropout >= 0.0 && r->dropout <= 1.0 && r->quant >= EP_QUANT_NONE &&
+         r->quant <= EP_QUANT_INT8;
+}
+
+ep_status_t ep_add_layernorm(const ep_layernorm_rule_t *rule, const ep_layernorm_t *t, void *stream) {
+  if (!layernorm_rule_ok(rule) || !t) return EP_ERR_INVALID_ARG;
+  const int32_t q = rule->quant;
+  const bool drop = rule->dropout != 0.0;
+  if (drop != (t->rng != nullptr) || (t->residual || drop) != (t->residual_out != nullptr))
+    return EP_ERR_INVALID_ARG;
+  if ((q != EP_QUANT_NONE) != (t->codes != nullptr) || (t->codes == nullptr) != (t->scales == nullptr))
+    return EP_ERR_INVALID_ARG;
+  if (!t->y && !t->codes) return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_tensor(t->x, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  epk::LayerNorm n{};
+  int64_t T, H;
+  if (!row_tensor(t->x, &T, &H)) return EP_ERR_BAD_SHAPE;
+  if (H > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
+  if (drop) {
+    st = check_dropout(rule->dropout, t->rng, &n.drop);
+    if (st != EP_OK) return st;
+  }
+  if (t->residual) {
+    st = check_stream_rows(t->residual, T, H, &n.res_fp32);
+    if (st != EP_OK) return st;
+  }
+  if (t->residual_out) {
+    bool out_fp32;
+    st = check_stream_rows(t->residual_out, T, H, &out_fp32);
+    if (st != EP_OK) return st;
+    if (out_fp32 != n.res_fp32) return EP_ERR_BAD_DTYPE;
+  }
+  st = check_norm_weight(t->weight, H, &n.w_fp32);
+  if (st != EP_OK) return st;
+  if (t->bias) {
+    bool fp32;
+    st = check_norm_weight(t->bias, H, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.w_fp32) return EP_ERR_BAD_DTYPE;
+  }
+  if (t->y) {
+    st = check_tensor(t->y, EP_TAG_TOKENS, EP_DTYPE_BF16);
+    if (st != EP_OK) return st;
+    if (!is_rows(t->y, T, H)) return EP_ERR_BAD_SHAPE;
+  }
+  if (t->codes) {
+    const bool i8 = q == EP_QUANT_INT8;
+    if (!i8 && H % 128 != 0) return EP_ERR_UNSUPPORTED;
+    st = check_tensor(t->codes, EP_TAG_TOKENS, i8 ? EP_DTYPE_INT8 : EP_DTYPE_FP8_E4M3);
+    if (st != EP_OK) return st;
+    if (!is_rows(t->codes, T, H)) return EP_ERR_BAD_SHAPE;
+    st = check_tensor(t->scales, i8 ? EP_TAG_ROW_SCALES : EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (i8 ? numel(t->scales) != T : !is_rows(t->scales, T, H / 128)) return EP_ERR_BAD_SHAPE;
+  }
+  n.x = t->x->data;
+  n.residual = t->residual ? t->residual->data : nullptr;
+  n.w = t->weight->data;
+  n.b = t->bias ? t->bias->data : nullptr;
+  n.hidden = t->residual_out ? t->residual_out->data : nullptr;
+  n.y = t->y ? t->y->data : nullptr;
+  n.codes = t->codes ? static_cast<uint8_t *>(t->codes->data) : nullptr;
+  n.scales = t->scales ? static_cast<float *>(t->scales->data) : nullptr;
+  n.T = (int32_t)T;
+  n.H = (int32_t)H;
+  n.quant = q;
+  n.eps = rule->eps;
+  return hip_status(epk::launch_add_layernorm(n, as_stream(stream)));
+}
+
+ep_status_t ep_add_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes) {
+  const ep_status_t st = ep_add_rmsnorm_bwd_workspace_bytes(rows, H, bytes);
+  if (st == EP_OK) *bytes *= 2;   // a partial row of grad_weight and one of grad_bias
+  return st;
+}
+
+ep_status_t ep_add_layernorm_bwd(const ep_layernorm_rule_t *rule, const ep_layernorm_bwd_t *t,
+                                 void *stream) {
+  if (!layernorm_rule_ok(rule) || rule->quant != EP_QUANT_NONE || !t || !t->hidden)
+    return EP_ERR_INVALID_ARG;
+  const bool drop = rule->dropout != 0.0;
+  if (drop != (t->rng != nullptr) || drop != (t->grad_x != nullptr) || (!drop && !t->grad))
+    return EP_ERR_INVALID_ARG;
+  epk::LayerNormBwd n{};
+  n.h_fp32 = t->hidden->dtype == EP_DTYPE_FP32;
+  ep_status_t st = check_tensor(t->hidden, EP_TAG_TOKENS, n.h_fp32 ? EP_DTYPE_FP32 : EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  int64_t T, H;
+  if (!row_tensor(t->hidden, &T, &H)) return EP_ERR_BAD_SHAPE;
+  if (H > epk::kRowMaxChannels) return EP_ERR_UNSUPPORTED;
+  if (drop) {
+    st = check_dropout(rule->dropout, t->rng, &n.drop);
+    if (st != EP_OK) return st;
+    st = check_tensor(t->grad_x, EP_TAG_TOKENS, EP_DTYPE_BF16);
+    if (st != EP_OK) return st;
+    if (!is_rows(t->grad_x, T, H)) return EP_ERR_BAD_SHAPE;
+    n.gx = t->grad_x->data;
+  }
+  st = check_norm_weight(t->weight, H, &n.w_fp32);
+  if (st != EP_OK) return st;
+  st = check_tensor(t->grad_y, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  if (!is_rows(t->grad_y, T, H)) return EP_ERR_BAD_SHAPE;
+  bool fp32;
+  if (t->grad_residual_out) {
+    st = check_stream_rows(t->grad_residual_out, T, H, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.h_fp32) return EP_ERR_BAD_DTYPE;
+    n.ghidden = t->grad_residual_out->data;
+  }
+  if (t->grad) {
+    st = check_stream_rows(t->grad, T, H, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.h_fp32) return EP_ERR_BAD_DTYPE;
+    n.gh = t->grad->data;
+  }
+  for (ep_tensor_t *g : {t->grad_weight, t->grad_bias}) {
+    if (!g) continue;
+    st = check_tensor(g, EP_TAG_NORM_WEIGHT, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (g->ndim != 1 || g->sizes[0] != H) return EP_ERR_BAD_SHAPE;
+  }
+  if (t->grad_weight || t->grad_bias) {
+    const int64_t need = (int64_t)epk::norm_bwd_groups((int32_t)T, (int32_t)H) * 2 * H;
+    if (need > 0) {
+      st = check_tensor(t->workspace, EP_TAG_WORKSPACE, EP_DTYPE_FP32);
+      if (st != EP_OK) return st;
+      if (t->workspace->ndim != 1) return EP_ERR_BAD_SHAPE;
+      if (t->workspace->sizes[0] < need) return EP_ERR_WORKSPACE_TOO_SMALL;
+      n.part = static_cast<float *>(t->workspace->data);
+    }
+    n.gw = t->grad_weight ? static_cast<float *>(t->grad_weight->data) : nullptr;
+    n.gb = t->grad_bias ? static_cast<float *>(t->grad_bias->data) : nullptr;
+  }
+  n.hidden = t->hidden->data;
+  n.w = t->weight->data;
+  n.gy = t->grad_y->data;
+  n.T = (int32_t)T;
+  n.H = (int32_t)H;
+  n.eps = rule->eps;
+  return hip_status(epk::launch_layernorm_bwd(n, as_stream(stream)));
+}
+
+ep_status_t ep_quantize_fp8_2d(const ep_fp8_2d_rule_t *rule, const ep_tensor_t *x, ep_tensor_t *codes,
+                               ep_tensor_t *scales, ep_tensor_t *codes_t, ep_tensor_t *scales_t,
+                               void *stream) {
+  if (!rule || (rule->fp8_scales != EP_FP8_SCALES_AMAX && rule->fp8_scales != EP_FP8_SCALES_POW2) ||
+      (rule->block != EP_FP8_BLOCK_ROWS && rule->block != EP_FP8_BLOCK_SQUARE))
+    return EP_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr) ||
+      (!codes && !codes_t))
+    return EP_ERR_INVALID_ARG;
+  ep_status_t st = check_tensor(x, EP_TAG_TOKENS, EP_DTYPE_BF16);
+  if (st != EP_OK) return st;
+  if (x->ndim != 2) return EP_ERR_BAD_SHAPE;
+  const int64_t R = x->sizes[0], C = x->sizes[1];
+  if (C <= 0 || C % 128 != 0) return EP_ERR_BAD_SHAPE;
+  const int64_t rb = (R + 127) / 128, cb = C / 128;
+  if (R > INT32_MAX - 127 || C > INT32_MAX - 127 || rb * cb >= (int64_t)1 << 24) return EP_ERR_UNSUPPORTED;
+  const bool sq = rule->block == EP_FP8_BLOCK_SQUARE;
+  if (codes) {
+    st = check_tensor(codes, EP_TAG_TOKENS, EP_DTYPE_FP8_E4M3);
+    if (st != EP_OK) return st;
+    st = check_tensor(scales, EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (!is_2d(codes, R, C) || !is_2d(scales, sq ? rb : R, cb)) return EP_ERR_BAD_SHAPE;
+  }
+  if (codes_t) {
+    st = check_tensor(codes_t, EP_TAG_TOKENS, EP_DTYPE_FP8_E4M3);
+    if (st != EP_OK) return st;
+    st = check_tensor(scales_t, EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+    if (st != EP_OK) return st;
+    if (!is_2d(codes_t, C, rb * 128) || !is_2d(scales_t, sq ? cb : C, rb)) return EP_ERR_BAD_SHAPE;
+  }
+  epk::Quantize2d n{};
+  n.x = static_cast<const uint16_t *>(x->data);
+  n.R = (int32_t)R;
+  n.C = (int32_t)C;
+  n.codes = codes ? static_cast<uint8_t *>(codes->data) : nullptr;
+  n.scales = scales ? static_cast<float *>(scales->data) : nullptr;
+  n.codes_t = codes_t ? static_cast<uint8_t *>(codes_t->data) : nullptr;
+  n.scales_t = scales_t ? static_cast<float *>(scales_t->data) : nullptr;
+  n.square = sq;
+  n.pow2 = rule->fp8_scales == EP_FP8_SCALES_POW2;
+  return hip_status(epk::launch_quantize_2d(n, as_stream(stream)));
+}
+
+ep_status_t ep_linear_fp8(const ep_linear_rule_t *rule, const ep_tensor_t *x,
+                          const ep_tensor_t *x_scales, const ep_tensor_t *w,
+                          const ep_tensor_t *w_scales, const ep_tensor_t *addend, ep_tensor_t *out,
+                          ep_tensor_t *status, void *stream) {
+  if (!rule || (rule->fp8_scales != EP_FP8_SCALES_AMAX && rule->fp8_scales != EP_FP8_SCALES_POW2) ||
+      (rule->swiglu != 0 && rule->swiglu != 1) || !out)
+    return EP_ERR_INVALID_ARG;
+  const bool glu = rule->swiglu == 1;
+  if (glu && addend) return EP_ERR_INVALID_ARG;
+  epk::Linear n{};
+  ep_status_t st = check_tensor(x, EP_TAG_TOKENS, EP_DTYPE_FP8_E4M3);
+  if (st != EP_OK) return st;
+  st = check_tensor(x_scales, EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  st = check_tensor(w, EP_TAG_EXPERT_WEIGHTS, EP_DTYPE_FP8_E4M3);
+  if (st != EP_OK) return st;
+  st = check_tensor(w_scales, EP_TAG_FP8_SCALES, EP_DTYPE_FP32);
+  if (st != EP_OK) return st;
+  if (x->ndim < 2 || w->ndim != 2) return EP_ERR_BAD_SHAPE;
+  const int64_t K = x->sizes[x->ndim - 1], N = w->sizes[0];
+  if (K <= 0 || K % 128 != 0 || w->sizes[1] != K) return EP_ERR_BAD_SHAPE;
+  const int64_t M = numel(x) / K;
+  if (K > epk::kLinearMaxK || M > INT32_MAX - 255 || N > INT32_MAX - 255) return EP_ERR_UNSUPPORTED;
+  if (glu && N % 16 != 0) return EP_ERR_BAD_SHAPE;
+  if (!is_rows(x_scales, M, K / 128)) return EP_ERR_BAD_SHAPE;
+  if (is_2d(w_scales, (N + 127) / 128, K / 128)) n.row_scales = false;   // (N = 1: the same)
+  else if (is_2d(w_scales, N, K / 128)) n.row_scales = true;
+  else return EP_ERR_BAD_SHAPE;
+  st = check_stream_rows(out, M, glu ? N / 2 : N, &n.out_fp32);
+  if (st != EP_OK) return st;
+  if (glu && n.out_fp32) return EP_ERR_BAD_DTYPE;
+  if (addend) {
+    bool fp32;
+    st = check_stream_rows(addend, M, N, &fp32);
+    if (st != EP_OK) return st;
+    if (fp32 != n.out_fp32) return EP_ERR_BAD_DTYPE;
+    n.addend = addend->data;
+  }
+  if (status) {
+    st = check_tensor(status, EP_TAG_STATUS, EP_DTYPE_INT32);
+    if (st != EP_OK) return st;
+    if (status->ndim != 1 || status->sizes[0] != 1) return EP_ERR_BAD_SHAPE;
+    n.status = static_cast<uint32_t *>(status->data);
+  }
+  n.x = static_cast<const uint8_t *>(x->data);
+  n.w = static_cast<const uint8_t *>(w->data);
+  n.xs = static_cast<const float *>(x_scales->data);
+  n.ws = static_cast<const float *>(w_scales->data);
+  n.out = out->data;
+  n.M = (int32_t)M;
+  n.N = (int32_t)N;
+  n.K = (int32_t)K;
+  n.glu = glu;
+  n.pow2 = rule->fp8_scales == EP_FP8_SCALES_POW2;
+  if (!epk::linear_fp8_fits(n)) return EP_ERR_UNSUPPORTED;
+  return hip_status(epk::launch_linear_fp8(n, as_stream(stream)));
+}
+
 ep_status_t ep_run_calls(const ep_call_t *calls, int32_t n, int32_t *failed) {
   if (failed != nullptr) *failed = 0;
   if (n < 0 || (n > 0 && calls == nullptr)) return EP_ERR_INVALID_ARG;
@@ -1222,6 +1511,25 @@ ep_status_t ep_run_calls(const ep_call_t *calls, int32_t n, int32_t *failed) {
         break;
       case EP_OP_EXPERT_GEMM_INT8_SWIGLU:
         st = ep_expert_gemm_int8_swiglu(h, t(1), t(2), t(3), t(4), t(5), t(6), t(7), c.p[8]);
+        break;
+      case EP_OP_DROPOUT:
+        st = ep_dropout(static_cast<const ep_dropout_rule_t *>(c.p[0]), t(1), t(2), t(3), t(4), c.p[5]);
+        break;
+      case EP_OP_ADD_LAYERNORM:
+        st = ep_add_layernorm(static_cast<const ep_layernorm_rule_t *>(c.p[0]),
+                              static_cast<const ep_layernorm_t *>(c.p[1]), c.p[2]);
+        break;
+      case EP_OP_ADD_LAYERNORM_BWD:
+        st = ep_add_layernorm_bwd(static_cast<const ep_layernorm_rule_t *>(c.p[0]),
+                                  static_cast<const ep_layernorm_bwd_t *>(c.p[1]), c.p[2]);
+        break;
+      case EP_OP_QUANTIZE_FP8_2D:
+        st = ep_quantize_fp8_2d(static_cast<const ep_fp8_2d_rule_t *>(c.p[0]), t(1), t(2), t(3), t(4),
+                                t(5), c.p[6]);
+        break;
+      case EP_OP_LINEAR_FP8:
+        st = ep_linear_fp8(static_cast<const ep_linear_rule_t *>(c.p[0]), t(1), t(2), t(3), t(4), t(5),
+                           t(6), t(7), c.p[8]);
         break;
       default: st = EP_ERR_INVALID_ARG; break;
     }

@@ -28,6 +28,12 @@ constexpr uint32_t kFlagScaleFormat = 16u;
 
 enum Layout : int32_t { kLL = 0, kHT = 1, kStatic = 2 };
 
+struct Dropout {
+  const int32_t *rng;  // seed (low, high word) and offset (low, high), or null: nothing is dropped
+  uint32_t threshold;  // a value stays if its 16 bits are below it (65536: all do)
+  float scale;         // factor of the kept values, 65536 / threshold (0 if none is kept)
+};
+
 // Device tables carved out of the caller's workspace (each 256-byte aligned).
 struct Workspace {
   uint32_t *status;      // [1]  EP_FLAG_* bits
@@ -160,6 +166,58 @@ struct RmsNormBwd {
 };
 int32_t norm_bwd_groups(int32_t T, int32_t H);  // partial rows of grad_weight in the workspace
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &n, hipStream_t s);
+// sums of G partial rows of C columns: the first `split` into dw, the others into db (null: dropped)
+hipError_t launch_norm_dw(const float *part, int32_t G, int32_t C, int32_t split, float *dw, float *db,
+                          hipStream_t s);
+struct LayerNorm {
+  const void *x, *residual, *w, *b;
+  void *hidden, *y;
+  uint8_t *codes;
+  float *scales;
+  int32_t T, H, quant;
+  bool res_fp32, w_fp32;
+  double eps;
+  Dropout drop;   // rng null: none
+};
+hipError_t launch_add_layernorm(const LayerNorm &n, hipStream_t s);
+struct LayerNormBwd {
+  const void *hidden, *w, *gy, *ghidden;
+  void *gh, *gx;  // gradients of the stream and, with dropout, of the branch
+  float *gw, *gb, *part;
+  int32_t T, H;
+  bool h_fp32, w_fp32;
+  double eps;
+  Dropout drop;
+};
+hipError_t launch_layernorm_bwd(const LayerNormBwd &n, hipStream_t s);
+struct DropoutAdd {
+  const void *x, *residual;
+  void *out;
+  int64_t count;  // a multiple of 8
+  bool x_fp32, out_fp32;
+  Dropout drop;
+};
+hipError_t launch_dropout(const DropoutAdd &n, hipStream_t s);
+struct Quantize2d {
+  const uint16_t *x;
+  int32_t R, C;
+  uint8_t *codes, *codes_t;   // either may be null, with its scales
+  float *scales, *scales_t;
+  bool square, pow2;
+};
+hipError_t launch_quantize_2d(const Quantize2d &n, hipStream_t s);
+struct Linear {
+  const uint8_t *x, *w;
+  const float *xs, *ws;
+  const void *addend;
+  void *out;
+  uint32_t *status;           // or null
+  int32_t M, N, K;
+  bool row_scales, out_fp32, glu, pow2;
+};
+constexpr int64_t kLinearMaxK = (int64_t)1 << 22;  // 32-bit offsets inside a tile of 256 rows
+bool linear_fp8_fits(const Linear &n);
+hipError_t launch_linear_fp8(const Linear &n, hipStream_t s);
 hipError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int32_t K, uint8_t *codes,
                                 float *scales, hipStream_t s);
 // static scratch (scratch.hip): device address on the current device, and a

@@ -1,0 +1,362 @@
+// linear_fp8.hip -- matrix product on FP8 operands with a scale per block of 128,
+// for the dense half of a layer (shared experts, projections, and their data and
+// weight gradients), on gfx950.
+//
+//   out[m, n] = addend[m, n] + sum_b SX[m, b] * SW[n or n / 128, b] *
+//                              sum_{c in block b} X[m, c] * W[n, c]
+//
+// X is [M, K] e4m3 codes with a scale per row and 128 of K; W is [N, K] with a
+// scale per 128 x 128 square (weights) or per row (a gradient's transposed
+// operand).  A slab is 128 of K: one scale block, 128 bytes a row.
+//
+// The weights are the matrix instruction's A operand and the tokens its B
+// operand, so a lane's accumulators belong to one token and four consecutive
+// channels: with a square's scale (uniform over the wave's channels) the fold of
+// a slab's partial sum into the running one is a single fma with a factor per
+// lane, and results leave as four channels at a time.
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes the whole slab of a 16 x 16 block at
+// once, so a partial sum is four registers and two sets of them are enough to
+// fold one block while the next is multiplied.
+#include "ep_internal.h"
+#include "gemm_common.h"
+
+namespace epk {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+enum LinearOut : int { kOutBf16 = 0, kOutFp32 = 1, kOutGlu = 2 };
+
+struct LinArgs {
+  const u32x4 *x, *w;       // codes, 16-byte vectors
+  const float *xs, *ws;
+  const void *addend;       // or null
+  void *out;
+  int32_t M, N, K;
+};
+
+// silu(g) * u in fp32: the hardware reciprocal and exponential (far below the
+// rounding that follows); below -64, where 1 + e^-g leaves the reciprocal's range,
+// g * u * e^g in fp64.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  if (g < -64.0f) return (float)((double)g * (double)u * exp((double)g));
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Channels n .. n + 3 of token m (m < M).
+template <int OUT>
+__device__ __forceinline__ void store4(const LinArgs &a, int32_t m, int32_t n, f32x4 v) {
+  if (n >= a.N) return;
+  if constexpr (OUT == kOutGlu) {   // N % 16 == 0: all four are there
+    const int64_t at = (int64_t)m * (a.N / 2) + n / 2;
+    static_cast<uint32_t *>(a.out)[at / 2] = pack_bf16x2(silu_times(v.x, v.y), silu_times(v.z, v.w));
+  } else {
+    const int64_t at = (int64_t)m * a.N + n;
+    if ((a.N & 3) == 0) {
+      if constexpr (OUT == kOutFp32) {
+        if (a.addend) v += static_cast<const f32x4 *>(a.addend)[at / 4];
+        static_cast<f32x4 *>(a.out)[at / 4] = v;
+      } else {
+        if (a.addend) {
+          const u32x2 r = static_cast<const u32x2 *>(a.addend)[at / 4];
+          v += f32x4{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
+        }
+        static_cast<u32x2 *>(a.out)[at / 4] = u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+      }
+      return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (n + r >= a.N) break;
+      if constexpr (OUT == kOutFp32) {
+        static_cast<float *>(a.out)[at + r] = v[r] + (a.addend ? static_cast<const float *>(a.addend)[at + r] : 0.0f);
+      } else {
+        const float b = a.addend ? bf16_lo(static_cast<const uint16_t *>(a.addend)[at + r]) : 0.0f;
+        static_cast<uint16_t *>(a.out)[at + r] = (uint16_t)pack_bf16x2(v[r] + b, 0.0f);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ i32x8 join_codes(const u32x4 lo, const u32x4 hi) {
+  return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+__device__ __forceinline__ f32x4 mfma_slab(const i32x8 &a, const i32x8 &b, const f32x4 &c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);  // both e4m3, times 2^0
+}
+
+// ---------------------------------------------------------------------------
+// tiles
+//
+// WN x WM waves, each NA x MB blocks of 16 channels x 16 tokens.  Slabs go from
+// global memory straight into LDS, two buffers; the next slab's loads are issued
+// behind the barrier that publishes this one, so they have this slab's products
+// to land in.
+
+template <int WN_, int WM_, int NA_, int MB_>
+struct LinShape {
+  static constexpr int WN = WN_, WM = WM_, NA = NA_, MB = MB_;
+  static constexpr int BN = WN * NA * 16, BM = WM * MB * 16, threads = 64 * WN * WM;
+};
+
+// Tile of workgroup blockIdx.x: XCD x (b % 8) takes a contiguous eighth of the
+// tiles, in blocks of `span` token tiles by all channel tiles, tokens first, so
+// that the tiles an XCD runs at once share their rows and weights in its L2.
+__device__ __forceinline__ bool linear_tile(int32_t tm, int32_t tn, int32_t span, int32_t &mt, int32_t &nt) {
+  const int32_t total = tm * tn, per = (total + kXcds - 1) / kXcds;
+  const int32_t x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, i = x * per + slot;
+  if (slot >= per || i >= total) return false;
+  const int32_t g = i / (span * tn), rem = i - g * span * tn;
+  const int32_t h = tm - g * span < span ? tm - g * span : span;
+  mt = g * span + rem % h;
+  nt = rem / h;
+  return true;
+}
+
+template <class S, bool ROW, int OUT>
+__global__ __launch_bounds__(S::threads, S::threads >= 512 ? 2 : 2) void k_linear_fp8(LinArgs a, int32_t tm,
+                                                                                     int32_t tn, int32_t span) {
+  constexpr int NS = S::BM + (ROW ? S::BN : 0);   // scales a slab
+  __shared__ u32x4 sw[2][S::BN * kChunks], sx[2][S::BM * kChunks];
+  __shared__ __attribute__((aligned(16))) float ssc[2][NS];
+  int32_t mt, nt;
+  if (!linear_tile(tm, tn, span, mt, nt)) return;
+  const int32_t m0 = mt * S::BM, n0 = nt * S::BN;
+  const int32_t rows = a.M - m0 < S::BM ? a.M - m0 : S::BM, wrows = a.N - n0 < S::BN ? a.N - n0 : S::BN;
+  const int32_t KV = a.K / 16, NB = a.K / 128;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
+  const int wn = wv / S::WM, wm = wv % S::WM;
+
+  // resources over the tile's rows (32-bit offsets: K <= 2^22); rows past the end read the last
+  const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.w + (int64_t)n0 * KV), (short)0, wrows * a.K, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.x + (int64_t)m0 * KV), (short)0, rows * a.K, kBufDword3);
+  constexpr int LW = S::BN * kChunks / S::threads, LX = S::BM * kChunks / S::threads;
+  static_assert(LW * S::threads == S::BN * kChunks && LX * S::threads == S::BM * kChunks, "whole loads");
+  // slot q of a slab holds chunk (q % 8) ^ ((r / 2) % 8) of row r = q / 8
+  uint32_t ow[LW], ox[LX];
+#pragma unroll
+  for (int i = 0; i < LW; ++i) {
+    const int q = i * S::threads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    ow[i] = (uint32_t)(((r < wrows ? r : wrows - 1) * KV + c) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < LX; ++i) {
+    const int q = i * S::threads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+    ox[i] = (uint32_t)(((r < rows ? r : rows - 1) * KV + c) * 16);
+  }
+  // the slab's scales: each wave brings 64 (some the same ones as another)
+  static_assert(NS / 64 <= S::WN * S::WM, "a load of scales a wave");
+  const int part = wv % (NS / 64);
+  const bool of_x = part < S::BM / 64;   // wave-uniform
+  const int srow = (of_x ? part : part - S::BM / 64) * 64 + lane, slast = (of_x ? rows : wrows) - 1;
+  const uint32_t osc = (uint32_t)((srow < slast ? srow : slast) * NB * 4);
+  const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)n0 * NB), (short)0,
+      (of_x ? rows : wrows) * NB * 4, kBufDword3);
+#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
+#define LIN_ISSUE(kt, buf)                                                                            \
+  {                                                                                                   \
+    _Pragma("unroll") for (int i = 0; i < LW; ++i)                                                    \
+        lds_load16(rW, LDS_ADDR(&sw[buf][i * S::threads + wv * 64]), ow[i], (kt) * 128);              \
+    _Pragma("unroll") for (int i = 0; i < LX; ++i)                                                    \
+        lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), ox[i], (kt) * 128);              \
+    lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, (kt) * 4);                                     \
+  }
+  f32x4 acc[S::NA][S::MB];
+#pragma unroll
+  for (int i = 0; i < S::NA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // the square that holds the wave's channels (S::NA * 16 divides 128)
+  static_assert(128 % (S::NA * 16) == 0, "a wave's channels lie in one square");
+  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * S::NA * 16) / 128;
+  const float *const wsq = a.ws + (int64_t)(sq < nsq ? sq : nsq - 1) * NB;
+  const int rl = lane & 15, cl = 2 * (lane >> 4);
+  LIN_ISSUE(0, 0);
+  for (int32_t kt = 0; kt < NB; ++kt) {
+    const int buf = kt & 1;
+    // this wave's loads of slab kt landed, its reads of the one before done; then everyone's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + 1 < NB) LIN_ISSUE(kt + 1, buf ^ 1);
+    i32x8 fx[S::MB];
+    float s[S::MB];
+    const float sb = ROW ? 1.0f : wsq[kt];
+#pragma unroll
+    for (int j = 0; j < S::MB; ++j) {
+      const int r = (wm * S::MB + j) * 16 + rl;
+      fx[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 1)]);
+      s[j] = ssc[buf][r] * sb;
+    }
+#pragma unroll
+    for (int i = 0; i < S::NA; ++i) {
+      const int r = (wn * S::NA + i) * 16 + rl;
+      const i32x8 fw = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 1)]);
+      f32x4 sn;
+      if constexpr (ROW)
+        sn = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * S::NA + i) * 16 + (lane >> 4) * 4]);
+#pragma unroll
+      for (int j = 0; j < S::MB; ++j) {
+        const f32x4 p = mfma_slab(fw, fx[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[i][j][q] = __builtin_fmaf(p[q], ROW ? sn[q] * s[j] : s[j], acc[i][j][q]);
+      }
+    }
+  }
+#undef LIN_ISSUE
+#undef LDS_ADDR
+#pragma unroll
+  for (int j = 0; j < S::MB; ++j) {
+    const int32_t m = (wm * S::MB + j) * 16 + rl;
+    if (m >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < S::NA; ++i)
+      store4<OUT>(a, m0 + m, n0 + (wn * S::NA + i) * 16 + (lane >> 4) * 4, acc[i][j]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few tokens
+//
+// The weights are streamed once: a workgroup takes 16 channels, its eight waves
+// every eighth slab each, weights and tokens straight from memory into the
+// matrix instruction's registers, four slabs' loads in flight a wave.  The waves'
+// sums are joined through LDS in a fixed order.
+
+constexpr int kFewWaves = 8, kFewSlabs = 4;
+
+template <int MT, bool ROW, int OUT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
+  __shared__ f32x4 red[kFewWaves][MT * 64];
+  const int tid = threadIdx.x, lane = tid & 63, rl = lane & 15, q4 = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16, KV = a.K / 16, NB = a.K / 128;
+  const int32_t n = n0 + rl < a.N ? n0 + rl : a.N - 1;
+  const u32x4 *const pw = a.w + (int64_t)n * KV + 2 * q4;
+  const u32x4 *px[MT];
+  const float *ps[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int32_t m = m0 + j * 16 + rl < a.M ? m0 + j * 16 + rl : a.M - 1;
+    px[j] = a.x + (int64_t)m * KV + 2 * q4;
+    ps[j] = a.xs + (int64_t)m * NB;
+  }
+  const float *pn[4];   // ROW: the scales of this lane's four channels
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int32_t c = n0 + q4 * 4 + r < a.N ? n0 + q4 * 4 + r : a.N - 1;
+    pn[r] = a.ws + (int64_t)c * NB;
+  }
+  const float *const wsq = a.ws + (int64_t)(n0 / 128) * NB;
+  f32x4 acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int32_t k0 = wv; k0 < NB; k0 += kFewWaves * kFewSlabs) {
+    u32x4 w[kFewSlabs][2], x[kFewSlabs][MT][2];
+    float s[kFewSlabs][MT], sn[kFewSlabs][4];
+#pragma unroll
+    for (int u = 0; u < kFewSlabs; ++u) {
+      const int32_t k = k0 + u * kFewWaves;
+      if (k >= NB) break;
+      w[u][0] = load_stream(pw + k * 8);
+      w[u][1] = load_stream(pw + k * 8 + 1);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        x[u][j][0] = px[j][k * 8];
+        x[u][j][1] = px[j][k * 8 + 1];
+        s[u][j] = ps[j][k];
+      }
+      if constexpr (ROW) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sn[u][r] = pn[r][k];
+      } else {
+        sn[u][0] = wsq[k];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFewSlabs; ++u) {
+      if (k0 + u * kFewWaves >= NB) break;
+      const i32x8 fw = join_codes(w[u][0], w[u][1]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const f32x4 p = mfma_slab(fw, join_codes(x[u][j][0], x[u][j][1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[j][r] = __builtin_fmaf(p[r], (ROW ? sn[u][r] : sn[u][0]) * s[u][j], acc[j][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) red[wv][j * 64 + lane] = acc[j];
+  __syncthreads();
+  for (int e = tid; e < MT * 64; e += 64 * kFewWaves) {
+    f32x4 v = red[0][e];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) v += red[i][e];
+    const int32_t m = m0 + (e >> 6) * 16 + (e & 15);
+    if (m < a.M) store4<OUT>(a, m, n0 + ((e >> 4) & 3) * 4, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+typedef LinShape<2, 4, 8, 4> LinShape256;   // 256 x 256, 8 waves of 128 x 64
+typedef LinShape<2, 2, 4, 4> LinShape128;   // 128 x 128, 4 waves of 64 x 64
+typedef LinShape<2, 2, 2, 2> LinShape64;    // 64 x 64, 4 waves of 32 x 32
+
+static int64_t tiles_of(const Linear &n, int32_t b) {
+  return (int64_t)((n.M + b - 1) / b) * ((n.N + b - 1) / b);
+}
+
+template <class S, bool ROW, int OUT>
+static void launch_tiles(const LinArgs &a, int32_t span, hipStream_t s) {
+  const int32_t tm = (a.M + S::BM - 1) / S::BM, tn = (a.N + S::BN - 1) / S::BN;
+  const unsigned grid = (unsigned)((((int64_t)tm * tn + kXcds - 1) / kXcds) * kXcds);
+  hipLaunchKernelGGL((k_linear_fp8<S, ROW, OUT>), dim3(grid), dim3(S::threads), 0, s, a, tm, tn, span);
+}
+
+template <bool ROW, int OUT>
+static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
+  if (n.M <= 64) {
+    const int mt = n.M <= 16 ? 1 : n.M <= 32 ? 2 : 4;
+    const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
+    if (mt == 1) hipLaunchKernelGGL((k_linear_fp8_few<1, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
+    else if (mt == 2) hipLaunchKernelGGL((k_linear_fp8_few<2, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_fp8_few<4, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
+  } else if (tiles_of(n, 256) >= 192) {
+    launch_tiles<LinShape256, ROW, OUT>(a, 4, s);
+  } else if (tiles_of(n, 128) >= 256) {
+    launch_tiles<LinShape128, ROW, OUT>(a, 8, s);
+  } else {
+    launch_tiles<LinShape64, ROW, OUT>(a, 8, s);
+  }
+}
+
+// A launch counts its threads in 32 bits, and a tile index is an int32.
+bool linear_fp8_fits(const Linear &n) {
+  const int64_t few = ((int64_t)n.N + 15) / 16;
+  return n.M <= 64 ? few * 64 * kFewWaves < (int64_t)1 << 32
+                   : tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
+}
+
+hipError_t launch_linear_fp8(const Linear &n, hipStream_t s) {
+  if (n.M == 0 || n.N == 0) return hipSuccess;
+  const LinArgs a{reinterpret_cast<const u32x4 *>(n.x), reinterpret_cast<const u32x4 *>(n.w), n.xs, n.ws,
+                  n.addend, n.out, n.M, n.N, n.K};
+  const int out = n.glu ? kOutGlu : n.out_fp32 ? kOutFp32 : kOutBf16;
+#define L(ROW)                                                        \
+  do {                                                                \
+    if (out == kOutGlu) launch_linear_form<ROW, kOutGlu>(n, a, s);    \
+    else if (out == kOutFp32) launch_linear_form<ROW, kOutFp32>(n, a, s); \
+    else launch_linear_form<ROW, kOutBf16>(n, a, s);                  \
+  } while (0)
+  if (n.row_scales) L(true);
+  else L(false);
+#undef L
+  return hipGetLastError();
+}
+
+}  // namespace epk

@@ -18,7 +18,8 @@
 
 namespace {
 
-constexpr int kMaxArgs = 9;
+constexpr int kMaxArgs = 9;   // of an entry point, the stream among them
+constexpr int kMaxViews = 12;  // of a struct of views
 
 // ep_dtype_t of a tensor, -1 if the library has none.
 int32_t dtype_of(const at::Tensor &t) {
@@ -71,11 +72,27 @@ bool describe(PyObject *o, int32_t tag, int64_t dev, ep_tensor_t *v) {
   return true;
 }
 
+// The device and address of a call's stream argument: None for the current
+// stream, or a torch.cuda.Stream's (device, address) as two ints in a tuple.
+bool stream_of(PyObject *o, int64_t *dev, void **stream) {
+  if (o == Py_None) {
+    *dev = c10::hip::current_device();
+    *stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)*dev).stream();
+    return true;
+  }
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) {
+    PyErr_SetString(PyExc_TypeError, "stream: None or (device, address)");
+    return false;
+  }
+  *dev = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 0));
+  *stream = PyLong_AsVoidPtr(PyTuple_GET_ITEM(o, 1));
+  return !PyErr_Occurred();
+}
+
 // call(fn, tags, stream, args...) -> status.  fn: address of the entry point;
 // tags: one byte per argument, a tensor's ep_tensor_tag_t or 0xFF for an
-// address given as an int; None is NULL.  stream: None for the current stream,
-// or a torch.cuda.Stream's (device, address) as two ints in a tuple.  The
-// stream is passed last.
+// address given as an int; None is NULL.  stream: as stream_of takes it; it is
+// passed last.
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n < 3 || !PyBytes_Check(args[1])) {
     PyErr_SetString(PyExc_TypeError, "call(fn, tags, stream, args...)");
@@ -93,19 +110,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
   void *p[kMaxArgs] = {};
   ep_tensor_t views[kMaxArgs];
   try {
-    if (args[2] == Py_None) {
-      dev = c10::hip::current_device();
-      p[m] = c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
-    } else {
-      if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) != 2) {
-        PyErr_SetString(PyExc_TypeError, "stream: None or (device, address)");
-        return nullptr;
-      }
-      PyObject *d = PyTuple_GET_ITEM(args[2], 0), *s = PyTuple_GET_ITEM(args[2], 1);
-      dev = PyLong_AsLongLong(d);
-      p[m] = PyLong_AsVoidPtr(s);
-      if (PyErr_Occurred()) return nullptr;
-    }
+    if (!stream_of(args[2], &dev, &p[m])) return nullptr;
     for (Py_ssize_t i = 0; i < m; ++i) {
       PyObject *o = args[3 + i];
       if (o == Py_None) continue;
@@ -127,6 +132,13 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
   Py_BEGIN_ALLOW_THREADS
   switch (m + 1) {
     case 4: st = reinterpret_cast<ep_status_t (*)(P, P, P, P)>(fn)(p[0], p[1], p[2], p[3]); break;
+    case 6:
+      st = reinterpret_cast<ep_status_t (*)(P, P, P, P, P, P)>(fn)(p[0], p[1], p[2], p[3], p[4], p[5]);
+      break;
+    case 7:
+      st = reinterpret_cast<ep_status_t (*)(P, P, P, P, P, P, P)>(fn)(p[0], p[1], p[2], p[3], p[4],
+                                                                      p[5], p[6]);
+      break;
     case 8:
       st = reinterpret_cast<ep_status_t (*)(P, P, P, P, P, P, P, P)>(fn)(p[0], p[1], p[2], p[3],
                                                                          p[4], p[5], p[6], p[7]);
@@ -141,7 +153,41 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+// call_views(fn, tags, stream, rule, tensors...) -> status, for entry points
+// (rule, struct of views, stream): the tensors' views, or NULL for None, are the
+// struct's members in order.
+PyObject *call_views(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n < 4 || !PyBytes_Check(args[1]) || n - 4 != PyBytes_GET_SIZE(args[1]) || n - 4 > kMaxViews) {
+    PyErr_SetString(PyExc_TypeError, "call_views(fn, tags, stream, rule, tensors...), one tag per tensor");
+    return nullptr;
+  }
+  void *fn = PyLong_AsVoidPtr(args[0]), *rule = PyLong_AsVoidPtr(args[3]), *stream;
+  if (PyErr_Occurred()) return nullptr;
+  const auto *tags = reinterpret_cast<const unsigned char *>(PyBytes_AS_STRING(args[1]));
+  int64_t dev;
+  ep_tensor_t views[kMaxViews];
+  ep_tensor_t *p[kMaxViews] = {};
+  try {
+    if (!stream_of(args[2], &dev, &stream)) return nullptr;
+    for (Py_ssize_t i = 0; i < n - 4; ++i) {
+      if (args[4 + i] == Py_None) continue;
+      if (!describe(args[4 + i], tags[i], dev, &views[i])) return nullptr;
+      p[i] = &views[i];
+    }
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+  ep_status_t st;
+  Py_BEGIN_ALLOW_THREADS
+  st = reinterpret_cast<ep_status_t (*)(void *, void *, void *)>(fn)(rule, p, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 PyMethodDef methods[] = {
+    {"call_views", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_views)), METH_FASTCALL,
+     "call_views(fn, tags, stream, rule, tensors...) -> status"},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL,
      "call(fn, tags, stream, args...) -> status"},
     {nullptr, nullptr, 0, nullptr}};

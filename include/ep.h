@@ -87,7 +87,7 @@ typedef enum ep_status {
 /* Tensor roles (NCCL EP paper listing, Table IV).  EP_TAG_EXPERT_GRADS and the
  * roles after it are this library's additions: for the duplicated-expert
  * gradient reduce, the routing step, the replica-weight prefetch, INT8 rows and
- * weights, the router's balance bias, and the norm. */
+ * weights, the router's balance bias, the norm, dropout, and the dense products. */
 typedef enum ep_tensor_tag {
   EP_TAG_TOKENS = 0,        /* token rows: dispatch in/out, combine in/out, their grads */
   EP_TAG_TOPK_IDX = 1,      /* expert ids (int32); -1 = no expert */
@@ -95,11 +95,14 @@ typedef enum ep_tensor_tag {
   EP_TAG_FP8_SCALES = 3,    /* one fp32 scale per 128 channels of an FP8 row */
   EP_TAG_EXPERT_GRADS = 4,  /* expert parameter gradients */
   EP_TAG_ROUTER_LOGITS = 5,  /* router logits or scores per token and expert, and their gradients */
-  EP_TAG_EXPERT_WEIGHTS = 6, /* expert parameters: owners' weights and prefetch slots */
+  EP_TAG_EXPERT_WEIGHTS = 6, /* expert parameters: owners' weights and prefetch slots; the
+                                weights of a dense product */
   EP_TAG_ROW_SCALES = 7,     /* one fp32 scale per INT8 row (tokens), or per row of INT8 weights */
   EP_TAG_ROUTER_BIAS = 8,    /* balance bias of each expert (fp32) */
   EP_TAG_NORM_WEIGHT = 9,    /* the norm's weight per channel and its gradient */
-  EP_TAG_WORKSPACE = 10      /* scratch memory of one call (fp32, 1-D) */
+  EP_TAG_WORKSPACE = 10,     /* scratch memory of one call (fp32, 1-D) */
+  EP_TAG_RNG_STATE = 11,     /* dropout's generator: int32 [4], seed and offset (low word, high word) */
+  EP_TAG_STATUS = 12         /* int32 [1]: EP_FLAG_* bits OR-ed in by a call that has no handle */
 } ep_tensor_tag_t;
 
 typedef enum ep_dtype {
@@ -782,6 +785,172 @@ ep_status_t ep_expert_gemm_int8_swiglu(ep_handle_t h, const ep_tensor_t *recv_to
                                        void *stream);
 
 /* ------------------------------------------------------------------------
+ * The dense half of a layer: dropout of a branch, layer norm, and FP8 products
+ * with a scale per block of 128 (shared experts, projections), forward and
+ * backward.  None needs a handle.  A training step's chain:
+ *   ep_add_layernorm (dropout, residual, FP8 rows) -> ep_linear_fp8 -> ...
+ *   backward: ep_quantize_fp8_2d of the gradient -> ep_linear_fp8 against the
+ *   transposed weights' codes (data) and against the transposed rows' codes
+ *   (weights) -> ep_add_layernorm_bwd. */
+
+/* Dropout from a counter-based generator (Philox4x32-10, Salmon et al.,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011); the mask is never
+ * stored.  Value i of the tensor (row-major) has the 16 bits
+ *   half i % 8 (0 the low half of word 0, 1 its high half, ...) of the four
+ *   words of Philox(counter = (i / 8, offset), key = seed)
+ * -- 64-bit counter halves and key, low word first -- and stays if they are below
+ * round((1 - p) * 65536).  So for a kept value x, scale = fp32(65536 / that):
+ *   out = round(x * scale + residual)    (the fma in fp32, then out's type)
+ * and a dropped one gives the residual (0 without one), whatever x holds.  The
+ * same state and shape give the same mask in every call here that takes them,
+ * so the backward is ep_dropout of the gradient without a residual.  Give every
+ * use of a seed its own offset; the state is read on the device, so that a
+ * captured call drops other values when the state has been changed.
+ * rule.p:   0 <= p <= 1 (1 drops everything).
+ * rng:      int32 [4], tag RNG_STATE: seed low, high, offset low, high word.
+ * x:        bf16 or fp32 [T, H] (any leading shape), tag TOKENS; H % 8 == 0.
+ * residual: NULL or rows of out's dtype, tag TOKENS.
+ * out:      bf16 or fp32 [T, H], tag TOKENS; may be the residual's own buffer,
+ *           or x's of the same dtype.
+ * Enqueues one kernel. */
+typedef struct ep_dropout_rule {
+  double p;
+} ep_dropout_rule_t;
+ep_status_t ep_dropout(const ep_dropout_rule_t *rule, const ep_tensor_t *rng, const ep_tensor_t *x,
+                       const ep_tensor_t *residual, ep_tensor_t *out, void *stream);
+
+typedef struct ep_layernorm_rule {
+  double eps;       /* added to the variance; finite, at least 2^-126 */
+  double dropout;   /* probability of dropping a value of x, 0..1 (0: none) */
+  int32_t quant;    /* ep_quant_t (0 for the backward) */
+  int32_t reserved; /* must be 0 */
+} ep_layernorm_rule_t;
+
+/* Dropout, residual addition and layer norm of token rows.  For every row:
+ *   h = round(dropout(x) + residual) to the residual's dtype (bf16 without one;
+ *       h = x without residual and dropout)
+ *   y = n * w + b,  n = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps)
+ * The norm reads h as it is stored.  The sums run in double, about the row's
+ * first value; h - mean and 1/sqrt are rounded once to fp32, y = fma(n, w, b).
+ * x:            bf16 [T, H] (any leading shape), tag TOKENS; H % 8 == 0,
+ *               H <= 32768, T < 2^31.
+ * residual:     NULL, or bf16 or fp32 [T, H], tag TOKENS.
+ * weight:       bf16 or fp32 [H], tag NORM_WEIGHT.
+ * bias:         NULL or [H] of the weight's dtype, tag NORM_WEIGHT.
+ * rng:          the dropout's state (see ep_dropout): given if and only if
+ *               rule.dropout is not 0.
+ * residual_out: [T, H] of the residual's dtype (bf16 without one), tag TOKENS: h.
+ *               Given if and only if residual or dropout is; may be the
+ *               residual's own buffer.
+ * y, codes, scales: as for ep_add_rmsnorm (INT8 codes from the row's largest |y|).
+ * At least one of y and codes is given.  A row that holds a value that is not
+ * finite is NaN throughout.  Enqueues one kernel. */
+typedef struct ep_layernorm {
+  const ep_tensor_t *x, *residual, *weight, *bias, *rng;
+  ep_tensor_t *residual_out, *y, *codes, *scales;
+} ep_layernorm_t;
+ep_status_t ep_add_layernorm(const ep_layernorm_rule_t *rule, const ep_layernorm_t *t, void *stream);
+
+/* Bytes of the workspace ep_add_layernorm_bwd needs for grad_weight and
+ * grad_bias (partial sums; 0 for no rows).  Errors: EP_ERR_INVALID_ARG. */
+ep_status_t ep_add_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes);
+
+/* Backward of ep_add_layernorm.  With n as above, r = 1 / sqrt(variance + eps)
+ * and g = grad_y * w:
+ *   grad = r * (g - mean(g) - n * mean(g * n)) + grad_residual_out
+ *   grad_x = dropout(grad)   (from grad before it is rounded)
+ *   grad_weight = sum over rows of grad_y * n,  grad_bias = sum over rows of grad_y
+ * hidden:            bf16 or fp32 [T, H], tag TOKENS: h (residual_out, or x).
+ * weight:            as in the forward.
+ * grad_y:            bf16 [T, H], tag TOKENS.
+ * grad_residual_out: NULL or [T, H] of hidden's dtype, tag TOKENS: the
+ *                    gradient that reaches h by the residual stream.
+ * rng:               the forward's state, unchanged: given if and only if
+ *                    rule.dropout is not 0.
+ * grad:              [T, H] output of hidden's dtype, tag TOKENS: the gradient
+ *                    of the residual (without dropout: of x alike); may be the
+ *                    buffer of grad_residual_out.  May be NULL with dropout.
+ * grad_x:            bf16 [T, H] output, tag TOKENS: the gradient of x.  Given
+ *                    if and only if rule.dropout is not 0.
+ * grad_weight, grad_bias: NULL or fp32 [H] output, tag NORM_WEIGHT (0 for no rows).
+ * workspace:         fp32, 1-D, tag WORKSPACE, of at least
+ *                    ep_add_layernorm_bwd_workspace_bytes; may be NULL where
+ *                    neither is asked for.  One call in flight at a time may use it.
+ * The sums are added in a fixed order: results repeat bit for bit.
+ * Enqueues up to two kernels. */
+typedef struct ep_layernorm_bwd {
+  const ep_tensor_t *hidden, *weight, *grad_y, *grad_residual_out, *rng;
+  ep_tensor_t *grad, *grad_x, *grad_weight, *grad_bias, *workspace;
+} ep_layernorm_bwd_t;
+ep_status_t ep_add_layernorm_bwd(const ep_layernorm_rule_t *rule, const ep_layernorm_bwd_t *t,
+                                 void *stream);
+
+/* What shares a scale in ep_quantize_fp8_2d. */
+typedef enum ep_fp8_block {
+  EP_FP8_BLOCK_ROWS = 0,  /* 128 channels of one row (transposed: 128 rows of one channel) */
+  EP_FP8_BLOCK_SQUARE = 1 /* a 128 x 128 square */
+} ep_fp8_block_t;
+
+typedef struct ep_fp8_2d_rule {
+  int32_t fp8_scales; /* EP_FP8_SCALES_AMAX: amax / 448, or _POW2: the power of two at or above it */
+  int32_t block;      /* ep_fp8_block_t */
+} ep_fp8_2d_rule_t;
+
+/* Quantisation of a bf16 matrix [R, C] to e4m3 codes by blocks, and of its
+ * transpose, read once: a gradient's rows (for the data gradient) and columns
+ * (for the weights'), or a weight and its transpose.  With Rp = R rounded up to
+ * 128:
+ *   ROWS:   scales [R, C/128], codes as ep_quantize_fp8's; scales_t [C, Rp/128],
+ *           one per channel and 128 rows
+ *   SQUARE: scales [Rp/128, C/128], one per 128 x 128 square (the last rows' are
+ *           fewer); scales_t its transpose [C/128, Rp/128], and the transposed
+ *           codes are the same codes
+ * A block that holds a value that is not finite gets codes 0 and a NaN scale.
+ * x:                 bf16 [R, C], tag TOKENS; C % 128 == 0.
+ * codes, scales:     both NULL, or e4m3 [R, C], tag TOKENS, and fp32, tag FP8_SCALES.
+ * codes_t, scales_t: both NULL, or e4m3 [C, Rp], tag TOKENS (0 past R), and fp32.
+ * At least one pair is given.  EP_ERR_UNSUPPORTED for 2^24 squares or more.
+ * Enqueues one kernel. */
+ep_status_t ep_quantize_fp8_2d(const ep_fp8_2d_rule_t *rule, const ep_tensor_t *x, ep_tensor_t *codes,
+                               ep_tensor_t *scales, ep_tensor_t *codes_t, ep_tensor_t *scales_t,
+                               void *stream);
+
+typedef struct ep_linear_rule {
+  int32_t fp8_scales; /* EP_FP8_SCALES_AMAX, or _POW2: every scale is a power of two */
+  int32_t swiglu;     /* 1: the SwiGLU store */
+} ep_linear_rule_t;
+
+/* Product of FP8 rows and FP8 weights with a scale per block of 128:
+ *   out[m, n] = round( sum_b xs[m, b] * ws[., b] * sum_{c in block b} x[m, c] * w[n, c]
+ *                      + addend[m, n] )
+ * (exact e4m3 products, fp32 accumulation; the addend joins in fp32).  With
+ * swiglu the rows of w interleave gate (even) and up (odd) projections and out
+ * [M, N/2] is silu(gate) * up of the fp32 sums, rounded once.
+ * x:        e4m3 [M, K] (any leading shape), tag TOKENS; K % 128 == 0, K <= 2^22.
+ * x_scales: fp32 [M, K/128], tag FP8_SCALES.
+ * w:        e4m3 [N, K], tag EXPERT_WEIGHTS.
+ * w_scales: fp32, tag FP8_SCALES: [ceil(N/128), K/128], one per 128 x 128 square,
+ *           or [N, K/128], one per row and 128 of K.
+ * addend:   NULL or [M, N] of out's dtype, tag TOKENS; may be out's own buffer (a
+ *           main gradient that grows).  Not with swiglu.
+ * out:      bf16 or fp32 [M, N], tag TOKENS; with swiglu bf16 [M, N/2], N % 16 == 0.
+ * status:   NULL or int32 [1], tag STATUS.  With EP_FP8_SCALES_POW2, a scale that
+ *           is not a positive normal power of two makes the call OR
+ *           EP_FLAG_SCALE_FORMAT into it (the block is then taken at the
+ *           scale's exponent).
+ * The gradients are this product too.  With grad_out [M, N] quantised by
+ * ep_quantize_fp8_2d (ROWS): the data gradient is x = codes, w = the weight's
+ * transposed codes (SQUARE); the weight gradient [N, K] is x = codes_t of
+ * grad_out, w = codes_t of the rows (ROWS), out fp32 with the main gradient as
+ * the addend.  The sums have a fixed order: results repeat bit for bit.
+ * Errors: EP_ERR_UNSUPPORTED for K > 2^22 or a launch too large for one grid.
+ * Enqueues one kernel. */
+ep_status_t ep_linear_fp8(const ep_linear_rule_t *rule, const ep_tensor_t *x,
+                          const ep_tensor_t *x_scales, const ep_tensor_t *w,
+                          const ep_tensor_t *w_scales, const ep_tensor_t *addend, ep_tensor_t *out,
+                          ep_tensor_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
  * Recorded calls.  A launch-bound loop -- a low-latency decode step, a few
  * kernels of a few microseconds each (NCCL EP listing, Table III: the LL
  * mode for batches of 1 to 128 tokens) -- spends about as much host time
@@ -813,12 +982,17 @@ typedef enum ep_op {
   EP_OP_QUANTIZE_INT8 = 19,
   EP_OP_DISPATCH_QUANTIZED = 20,
   EP_OP_EXPERT_GEMM_INT8 = 21,
-  EP_OP_EXPERT_GEMM_INT8_SWIGLU = 22
+  EP_OP_EXPERT_GEMM_INT8_SWIGLU = 22,
+  EP_OP_DROPOUT = 23,
+  EP_OP_ADD_LAYERNORM = 24,
+  EP_OP_ADD_LAYERNORM_BWD = 25,
+  EP_OP_QUANTIZE_FP8_2D = 26,
+  EP_OP_LINEAR_FP8 = 27
 } ep_op_t;
 
 /* One recorded call.  p holds the entry point's pointer arguments in its
- * own order -- the handle first where it takes one, the tensor views and rules
- * (NULL where the entry point accepts NULL), the stream last; i0 holds its one
+ * own order -- the handle first where it takes one, the tensor views, rules and
+ * ep_layernorm(_bwd)_t (NULL where the entry point accepts NULL), the stream last; i0 holds its one
  * integer argument (ep_quantize_fp8's fp8_scales; p is then tokens, codes,
  * scales, stream).  Slots past the entry point's arguments are ignored. */
 typedef struct ep_call {
