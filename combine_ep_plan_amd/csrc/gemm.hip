@@ -617,15 +617,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kScaleBufs = 4;
 constexpr int kF8Block = 128;  // K per scale; also the slab depth in bytes
 
-// E8M0 exponent of a power-of-two fp32 scale; *bad is set if it is not one.
-__device__ __forceinline__ uint32_t scale_exponent(float s, uint32_t *bad) {
-  const uint32_t b = __float_as_uint(s);
-  const uint32_t e = b >> 23;  // a set sign bit makes it 256 or more
-  // no branch: a mantissa bit, a sign, a zero or an all-ones exponent
-  *bad |= (b & 0x007FFFFFu) | (uint32_t)(e - 1u > 0xFDu);
-  return e & 0xFFu;
-}
-
 // WP2 (a group with power-of-two weight scales and amax row scales): each
 // block's MFMAs take the weight columns' exponents as their B block scales,
 // so the fold multiplies by the row scale alone (one FMA per element); a

@@ -126,6 +126,15 @@ __device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t 
                :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base) : "memory");
 }
 
+// E8M0 exponent of a power-of-two fp32 scale; *bad is set if it is not one.
+__device__ __forceinline__ uint32_t scale_exponent(float s, uint32_t *bad) {
+  const uint32_t b = __float_as_uint(s);
+  const uint32_t e = b >> 23;  // a set sign bit makes it 256 or more
+  // no branch: a mantissa bit, a sign, a zero or an all-ones exponent
+  *bad |= (b & 0x007FFFFFu) | (uint32_t)(e - 1u > 0xFDu);
+  return e & 0xFFu;
+}
+
 // Workgroups of a GEMM launch: per XCD, room for an eighth of each kind of
 // row tile rounded up (at most max_tiles / 8 + 2 row tiles), times the
 // column tiles (balanced_tile).

@@ -31,6 +31,7 @@ struct LinArgs {
   const float *xs, *ws;
   const void *addend;       // or null
   void *out;
+  uint32_t *status;         // or null
   int32_t M, N, K;
 };
 
@@ -84,6 +85,22 @@ __device__ __forceinline__ f32x4 mfma_slab(const i32x8 &a, const i32x8 &b, const
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);  // both e4m3, times 2^0
 }
 
+// Thirty-two codes (a lane's of a slab) times 2^(exponent of s) as four bf16 operands: exact.
+__device__ __forceinline__ void widen(const i32x8 &c, float s, bf16x8 (&o)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t w = (uint32_t)c[2 * g + (h >> 1)];
+      const bf16x2 v = (h & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
+      o[g][2 * h] = v.x;
+      o[g][2 * h + 1] = v.y;
+    }
+  }
+}
+#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
+
 // ---------------------------------------------------------------------------
 // tiles
 //
@@ -112,9 +129,11 @@ __device__ __forceinline__ bool linear_tile(int32_t tm, int32_t tn, int32_t span
   return true;
 }
 
-template <class S, bool ROW, int OUT>
-__global__ __launch_bounds__(S::threads, S::threads >= 512 ? 2 : 2) void k_linear_fp8(LinArgs a, int32_t tm,
-                                                                                     int32_t tn, int32_t span) {
+template <class S, bool ROW, bool POW2, int OUT>
+__global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t tm, int32_t tn,
+                                                              int32_t span) {
+  constexpr bool EXACT = OUT == kOutFp32;
+  constexpr int NA = S::NA, MB = S::MB;
   constexpr int NS = S::BM + (ROW ? S::BN : 0);   // scales a slab
   __shared__ u32x4 sw[2][S::BN * kChunks], sx[2][S::BM * kChunks];
   __shared__ __attribute__((aligned(16))) float ssc[2][NS];
@@ -155,66 +174,144 @@ __global__ __launch_bounds__(S::threads, S::threads >= 512 ? 2 : 2) void k_linea
   const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)n0 * NB), (short)0,
       (of_x ? rows : wrows) * NB * 4, kBufDword3);
-#define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
-#define LIN_ISSUE(kt, buf)                                                                            \
-  {                                                                                                   \
-    _Pragma("unroll") for (int i = 0; i < LW; ++i)                                                    \
-        lds_load16(rW, LDS_ADDR(&sw[buf][i * S::threads + wv * 64]), ow[i], (kt) * 128);              \
-    _Pragma("unroll") for (int i = 0; i < LX; ++i)                                                    \
-        lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), ox[i], (kt) * 128);              \
-    lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, (kt) * 4);                                     \
-  }
-  f32x4 acc[S::NA][S::MB];
+  const auto issue = [&](int32_t k, int buf) {
+    const int32_t kt = k < NB ? k : NB - 1;   // past the end: the last slab again, which nobody reads
 #pragma unroll
-  for (int i = 0; i < S::NA; ++i)
+    for (int i = 0; i < LW; ++i)
+      lds_load16(rW, LDS_ADDR(&sw[buf][i * S::threads + wv * 64]), ow[i], kt * 128);
 #pragma unroll
-    for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  // the square that holds the wave's channels (S::NA * 16 divides 128)
-  static_assert(128 % (S::NA * 16) == 0, "a wave's channels lie in one square");
-  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * S::NA * 16) / 128;
+    for (int i = 0; i < LX; ++i)
+      lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), ox[i], kt * 128);
+    lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, kt * 4);
+  };
+  // the square that holds the wave's channels
+  static_assert(128 % (NA * 16) == 0 && NA % 2 == 0, "a wave's channels lie in one square");
+  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * NA * 16) / 128;
   const float *const wsq = a.ws + (int64_t)(sq < nsq ? sq : nsq - 1) * NB;
   const int rl = lane & 15, cl = 2 * (lane >> 4);
-  LIN_ISSUE(0, 0);
-  for (int32_t kt = 0; kt < NB; ++kt) {
+
+  f32x4 acc[NA][MB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t bad = 0u;
+  i32x8 wf[2];
+  float wsc[2];      // row scales with POW2: those of the two fragments' rows
+  f32x4 sn[4];       // ... without: of the lane's four channels in the fragments (three in use: one folds late)
+  struct Rows {
+    i32x8 f[MB];     // the wave's token fragments
+    float s[MB];     // and scales, times the square's (POW2: alone)
+    float sq;        // the square's
+  } ra, rb;
+  const auto read_w = [&](int buf, int i) {
+    const int r = (wn * NA + i) * 16 + rl;
+    wf[i & 1] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 1)]);
+    if constexpr (POW2 && ROW) wsc[i & 1] = ssc[buf][S::BM + r];
+    if constexpr (!POW2 && ROW)
+      sn[i & 3] = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4]);
+  };
+  const auto read_x = [&](int buf, int32_t k, Rows &o) {
+    o.sq = ROW ? 1.0f : wsq[k < NB ? k : NB - 1];
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int r = (wm * MB + j) * 16 + rl;
+      o.f[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 1)]);
+      o.s[j] = POW2 ? ssc[buf][r] : ssc[buf][r] * o.sq;
+    }
+  };
+  // Slab kt, whose token fragments and first weight fragment are in registers.
+  // Before its last step everyone's reads of it are done and slab kt + 1 has
+  // landed: slab kt + 2 is sent for, into its place, and the next slab's first
+  // fragments are read under the last step's products.
+  const auto slab = [&](int32_t kt, Rows &x, Rows &next) {
     const int buf = kt & 1;
-    // this wave's loads of slab kt landed, its reads of the one before done; then everyone's
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + 1 < NB) LIN_ISSUE(kt + 1, buf ^ 1);
-    i32x8 fx[S::MB];
-    float s[S::MB];
-    const float sb = ROW ? 1.0f : wsq[kt];
+    f32x4 p[MB];
+    bf16x8 xb[EXACT ? MB : 1][4];
+    if constexpr (EXACT) {
 #pragma unroll
-    for (int j = 0; j < S::MB; ++j) {
-      const int r = (wm * S::MB + j) * 16 + rl;
-      fx[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 1)]);
-      s[j] = ssc[buf][r] * sb;
+      for (int j = 0; j < MB; ++j) widen(x.f[j], POW2 ? x.s[j] : 1.0f, xb[j]);
     }
+    int ex[MB], eq = 127;
+    if constexpr (POW2) {
 #pragma unroll
-    for (int i = 0; i < S::NA; ++i) {
-      const int r = (wn * S::NA + i) * 16 + rl;
-      const i32x8 fw = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 1)]);
-      f32x4 sn;
-      if constexpr (ROW)
-        sn = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * S::NA + i) * 16 + (lane >> 4) * 4]);
+      for (int j = 0; j < MB; ++j) ex[j] = (int)scale_exponent(x.s[j], &bad);
+      if constexpr (!ROW) eq = (int)scale_exponent(x.sq, &bad);
+    }
+    const auto fold = [&](int i, int j) {
 #pragma unroll
-      for (int j = 0; j < S::MB; ++j) {
-        const f32x4 p = mfma_slab(fw, fx[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      for (int q = 0; q < 4; ++q)
+        acc[i][j][q] = __builtin_fmaf(p[j][q], ROW ? sn[i & 3][q] * x.s[j] : x.s[j], acc[i][j][q]);
+    };
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[i][j][q] = __builtin_fmaf(p[q], ROW ? sn[q] * s[j] : s[j], acc[i][j][q]);
+    for (int i = 0; i < NA; ++i) {
+      if (i + 1 < NA) {
+        read_w(buf, i + 1);
+      } else {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        issue(kt + 2, buf);
+        read_x(buf ^ 1, kt + 1, next);
       }
-    }
-  }
-#undef LIN_ISSUE
-#undef LDS_ADDR
+      const i32x8 w = wf[i & 1];
+      if constexpr (EXACT) {
+        bf16x8 wb[4];
+        float f = 1.0f;
+        if constexpr (POW2) {
+          f = ROW ? wsc[i & 1] : x.sq;
+          if constexpr (ROW) (void)scale_exponent(f, &bad);
+        }
+        widen(w, f, wb);
 #pragma unroll
-  for (int j = 0; j < S::MB; ++j) {
-    const int32_t m = (wm * S::MB + j) * 16 + rl;
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < MB; ++j) {
+            f32x4 &t = POW2 ? acc[i][j] : p[j];
+            if (!POW2 && c == 0 && i > 0) fold(i - 1, j);
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[j][c],
+                                                        !POW2 && c == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : t, 0, 0, 0);
+          }
+      } else if constexpr (POW2) {
+        const int ew = ROW ? (int)scale_exponent(wsc[i & 1], &bad) : eq;
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x.f[j], acc[i][j], 0, 0, 0, ew, 0, ex[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          if (i > 0) fold(i - 1, j);
+          p[j] = mfma_slab(w, x.f[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        }
+      }
+      if (i + 1 == NA) read_w(buf ^ 1, 0);
+    }
+    if constexpr (!POW2) {
+#pragma unroll
+      for (int j = 0; j < MB; ++j) fold(NA - 1, j);
+    }
+  };
+  issue(0, 0);
+  issue(1, 1);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LW + LX + 1) : "memory");   // slab 0 landed
+  read_x(0, 0, ra);
+  read_w(0, 0);
+  int32_t kt = 0;
+  for (; kt + 1 < NB; kt += 2) {
+    slab(kt, ra, rb);
+    slab(kt + 1, rb, ra);
+  }
+  if (kt < NB) slab(kt, ra, rb);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands after the workgroup has ended
+  if constexpr (POW2) {
+    if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
+  }
+#pragma unroll
+  for (int j = 0; j < MB; ++j) {
+    const int32_t m = (wm * MB + j) * 16 + rl;
     if (m >= rows) continue;
 #pragma unroll
-    for (int i = 0; i < S::NA; ++i)
-      store4<OUT>(a, m0 + m, n0 + (wn * S::NA + i) * 16 + (lane >> 4) * 4, acc[i][j]);
+    for (int i = 0; i < NA; ++i)
+      store4<OUT>(a, m0 + m, n0 + (wn * NA + i) * 16 + (lane >> 4) * 4, acc[i][j]);
   }
 }
 
@@ -228,7 +325,7 @@ __global__ __launch_bounds__(S::threads, S::threads >= 512 ? 2 : 2) void k_linea
 
 constexpr int kFewWaves = 8, kFewSlabs = 4;
 
-template <int MT, bool ROW, int OUT>
+template <int MT, bool ROW, bool POW2, int OUT>
 __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
   __shared__ f32x4 red[kFewWaves][MT * 64];
   const int tid = threadIdx.x, lane = tid & 63, rl = lane & 15, q4 = lane >> 4;
@@ -251,6 +348,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
     pn[r] = a.ws + (int64_t)c * NB;
   }
   const float *const wsq = a.ws + (int64_t)(n0 / 128) * NB;
+  uint32_t bad = 0u;
   f32x4 acc[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -280,9 +378,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
     for (int u = 0; u < kFewSlabs; ++u) {
       if (k0 + u * kFewWaves >= NB) break;
       const i32x8 fw = join_codes(w[u][0], w[u][1]);
+      bf16x8 wb[4];
+      if constexpr (OUT == kOutFp32) widen(fw, 1.0f, wb);
+      if constexpr (POW2) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) (void)scale_exponent(s[u][j], &bad);
+#pragma unroll
+        for (int r = 0; r < (ROW ? 4 : 1); ++r) (void)scale_exponent(sn[u][r], &bad);
+      }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const f32x4 p = mfma_slab(fw, join_codes(x[u][j][0], x[u][j][1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        const i32x8 fx = join_codes(x[u][j][0], x[u][j][1]);
+        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (OUT == kOutFp32) {
+          bf16x8 xb[4];
+          widen(fx, 1.0f, xb);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[c], p, 0, 0, 0);
+        } else {
+          p = mfma_slab(fw, fx, p);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           acc[j][r] = __builtin_fmaf(p[r], (ROW ? sn[u][r] : sn[u][0]) * s[u][j], acc[j][r]);
@@ -291,6 +406,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < MT; ++j) red[wv][j * 64 + lane] = acc[j];
+  if constexpr (POW2) {
+    if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
+  }
   __syncthreads();
   for (int e = tid; e < MT * 64; e += 64 * kFewWaves) {
     f32x4 v = red[0][e];
@@ -311,28 +429,30 @@ static int64_t tiles_of(const Linear &n, int32_t b) {
   return (int64_t)((n.M + b - 1) / b) * ((n.N + b - 1) / b);
 }
 
-template <class S, bool ROW, int OUT>
+template <class S, bool ROW, bool POW2, int OUT>
 static void launch_tiles(const LinArgs &a, int32_t span, hipStream_t s) {
   const int32_t tm = (a.M + S::BM - 1) / S::BM, tn = (a.N + S::BN - 1) / S::BN;
   const unsigned grid = (unsigned)((((int64_t)tm * tn + kXcds - 1) / kXcds) * kXcds);
-  hipLaunchKernelGGL((k_linear_fp8<S, ROW, OUT>), dim3(grid), dim3(S::threads), 0, s, a, tm, tn, span);
+  hipLaunchKernelGGL((k_linear_fp8<S, ROW, POW2, OUT>), dim3(grid), dim3(S::threads), 0, s, a, tm, tn, span);
 }
 
-template <bool ROW, int OUT>
+template <bool ROW, bool POW2, int OUT>
 static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
   if (n.M <= 64) {
     const int mt = n.M <= 16 ? 1 : n.M <= 32 ? 2 : 4;
     const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
-    if (mt == 1) hipLaunchKernelGGL((k_linear_fp8_few<1, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
-    else if (mt == 2) hipLaunchKernelGGL((k_linear_fp8_few<2, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_fp8_few<4, ROW, OUT>), grid, dim3(64 * kFewWaves), 0, s, a);
-  } else if (tiles_of(n, 256) >= 192) {
-    launch_tiles<LinShape256, ROW, OUT>(a, 4, s);
-  } else if (tiles_of(n, 128) >= 256) {
-    launch_tiles<LinShape128, ROW, OUT>(a, 8, s);
-  } else {
-    launch_tiles<LinShape64, ROW, OUT>(a, 8, s);
+#define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * kFewWaves), 0, s, a)
+    if (mt == 1) L(1);
+    else if (mt == 2) L(2);
+    else L(4);
+#undef L
+    return;
   }
+  if constexpr (OUT != kOutFp32) {
+    if (tiles_of(n, 256) >= 192) return launch_tiles<LinShape256, ROW, POW2, OUT>(a, 4, s);
+  }
+  if (tiles_of(n, 128) >= 256) launch_tiles<LinShape128, ROW, POW2, OUT>(a, 8, s);
+  else launch_tiles<LinShape64, ROW, POW2, OUT>(a, 8, s);
 }
 
 // A launch counts its threads in 32 bits, and a tile index is an int32.
@@ -345,17 +465,18 @@ bool linear_fp8_fits(const Linear &n) {
 hipError_t launch_linear_fp8(const Linear &n, hipStream_t s) {
   if (n.M == 0 || n.N == 0) return hipSuccess;
   const LinArgs a{reinterpret_cast<const u32x4 *>(n.x), reinterpret_cast<const u32x4 *>(n.w), n.xs, n.ws,
-                  n.addend, n.out, n.M, n.N, n.K};
-  const int out = n.glu ? kOutGlu : n.out_fp32 ? kOutFp32 : kOutBf16;
-#define L(ROW)                                                        \
-  do {                                                                \
-    if (out == kOutGlu) launch_linear_form<ROW, kOutGlu>(n, a, s);    \
-    else if (out == kOutFp32) launch_linear_form<ROW, kOutFp32>(n, a, s); \
-    else launch_linear_form<ROW, kOutBf16>(n, a, s);                  \
+                  n.addend, n.out, n.status, n.M, n.N, n.K};
+#define L2(ROW, POW2)                                                   \
+  do {                                                                  \
+    if (n.glu) launch_linear_form<ROW, POW2, kOutGlu>(n, a, s);         \
+    else if (n.out_fp32) launch_linear_form<ROW, POW2, kOutFp32>(n, a, s); \
+    else launch_linear_form<ROW, POW2, kOutBf16>(n, a, s);              \
   } while (0)
-  if (n.row_scales) L(true);
-  else L(false);
-#undef L
+  if (n.row_scales && n.pow2) L2(true, true);
+  else if (n.row_scales) L2(true, false);
+  else if (n.pow2) L2(false, true);
+  else L2(false, false);
+#undef L2
   return hipGetLastError();
 }
 
