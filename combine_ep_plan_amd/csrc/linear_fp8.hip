@@ -109,9 +109,9 @@ __device__ __forceinline__ void widen(const i32x8 &c, float s, bf16x8 (&o)[4]) {
 // behind the barrier that publishes this one, so they have this slab's products
 // to land in.
 
-template <int WN_, int WM_, int NA_, int MB_>
+template <int WN_, int WM_, int NA_, int MB_, int ST_>
 struct LinShape {
-  static constexpr int WN = WN_, WM = WM_, NA = NA_, MB = MB_;
+  static constexpr int WN = WN_, WM = WM_, NA = NA_, MB = MB_, ST = ST_;   // ST: slabs in LDS
   static constexpr int BN = WN * NA * 16, BM = WM * MB * 16, threads = 64 * WN * WM;
 };
 
@@ -135,8 +135,9 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   constexpr bool EXACT = OUT == kOutFp32;
   constexpr int NA = S::NA, MB = S::MB;
   constexpr int NS = S::BM + (ROW ? S::BN : 0);   // scales a slab
-  __shared__ u32x4 sw[2][S::BN * kChunks], sx[2][S::BM * kChunks];
-  __shared__ __attribute__((aligned(16))) float ssc[2][NS];
+  __shared__ u32x4 sw[S::ST][S::BN * kChunks], sx[S::ST][S::BM * kChunks];
+  __shared__ __attribute__((aligned(16))) float ssc[S::ST][NS];
+  __shared__ float ssq[S::ST][ROW ? 1 : S::threads];   // a square's scale, for every lane of the wave
   int32_t mt, nt;
   if (!linear_tile(tm, tn, span, mt, nt)) return;
   const int32_t m0 = mt * S::BM, n0 = nt * S::BN;
@@ -174,6 +175,12 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)n0 * NB), (short)0,
       (of_x ? rows : wrows) * NB * 4, kBufDword3);
+  // the square that holds the wave's channels
+  static_assert(128 % (NA * 16) == 0 && NA % 2 == 0, "a wave's channels lie in one square");
+  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * NA * 16) / 128;
+  const __amdgpu_buffer_rsrc_t rQ = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.ws + (ROW ? 0 : (int64_t)(sq < nsq ? sq : nsq - 1) * NB)), (short)0, NB * 4, kBufDword3);
+  constexpr int kLoads = LW + LX + (ROW ? 1 : 2);   // of a wave, a slab
   const auto issue = [&](int32_t k, int buf) {
     const int32_t kt = k < NB ? k : NB - 1;   // past the end: the last slab again, which nobody reads
 #pragma unroll
@@ -183,11 +190,8 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     for (int i = 0; i < LX; ++i)
       lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), ox[i], kt * 128);
     lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, kt * 4);
+    if constexpr (!ROW) lds_load4(rQ, LDS_ADDR(&ssq[buf][wv * 64]), 0u, kt * 4);
   };
-  // the square that holds the wave's channels
-  static_assert(128 % (NA * 16) == 0 && NA % 2 == 0, "a wave's channels lie in one square");
-  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * NA * 16) / 128;
-  const float *const wsq = a.ws + (int64_t)(sq < nsq ? sq : nsq - 1) * NB;
   const int rl = lane & 15, cl = 2 * (lane >> 4);
 
   f32x4 acc[NA][MB];
@@ -198,12 +202,19 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   uint32_t bad = 0u;
   i32x8 wf[2];
   float wsc[2];      // row scales with POW2: those of the two fragments' rows
-  f32x4 sn[4];       // ... without: of the lane's four channels in the fragments (three in use: one folds late)
+  f32x4 sn[4], sl;   // ... without: of the lane's four channels in the fragments; in the slab's last one
+  f32x4 p[MB];       // the last step's partial sums, folded under the next step's products
   struct Rows {
     i32x8 f[MB];     // the wave's token fragments
     float s[MB];     // and scales, times the square's (POW2: alone)
     float sq;        // the square's
   } ra, rb;
+#pragma unroll
+  for (int j = 0; j < MB; ++j) {
+    p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    rb.s[j] = 0.0f;
+  }
+  sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto read_w = [&](int buf, int i) {
     const int r = (wn * NA + i) * 16 + rl;
     wf[i & 1] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 1)]);
@@ -211,22 +222,31 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     if constexpr (!POW2 && ROW)
       sn[i & 3] = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4]);
   };
-  const auto read_x = [&](int buf, int32_t k, Rows &o) {
-    o.sq = ROW ? 1.0f : wsq[k < NB ? k : NB - 1];
+  const auto read_x = [&](int buf, Rows &o) {
+    o.sq = ROW ? 1.0f : ssq[buf][wv * 64 + lane];
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
       const int r = (wm * MB + j) * 16 + rl;
       o.f[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 1)]);
-      o.s[j] = POW2 ? ssc[buf][r] : ssc[buf][r] * o.sq;
+      o.s[j] = POW2 || ROW ? ssc[buf][r] : ssc[buf][r] * o.sq;
     }
   };
-  // Slab kt, whose token fragments and first weight fragment are in registers.
-  // Before its last step everyone's reads of it are done and slab kt + 1 has
-  // landed: slab kt + 2 is sent for, into its place, and the next slab's first
-  // fragments are read under the last step's products.
-  const auto slab = [&](int32_t kt, Rows &x, Rows &next) {
-    const int buf = kt & 1;
-    f32x4 p[MB];
+  const auto fold = [&](int i, int j, float f, const f32x4 &n) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[j][q], ROW ? n[q] * f : f, acc[i][j][q]);
+  };
+  const auto fold_before = [&](int i, int j, const Rows &x, const Rows &before) {
+    if (i > 0) fold(i - 1, j, x.s[j], sn[(i - 1) & 3]);
+    else fold(NA - 1, j, before.s[j], sl);
+  };
+  // A slab whose token fragments and first weight fragment are in registers.
+  // Before its last step everyone's reads of it are done and the next slab has
+  // landed: slab kt + ST is sent for, into its place, and the next slab's first
+  // fragments are read under the last step's products.  A step's sums are folded
+  // under the next step's products (the last one's under the next slab's first,
+  // with the scales of before, which `next` still holds); sched_barrier keeps the
+  // compiler from folding each sum at once, waiting for it.
+  const auto slab = [&](int32_t kt, int buf, int nbuf, Rows &x, Rows &next) {
     bf16x8 xb[EXACT ? MB : 1][4];
     if constexpr (EXACT) {
 #pragma unroll
@@ -238,20 +258,14 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
       for (int j = 0; j < MB; ++j) ex[j] = (int)scale_exponent(x.s[j], &bad);
       if constexpr (!ROW) eq = (int)scale_exponent(x.sq, &bad);
     }
-    const auto fold = [&](int i, int j) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[i][j][q] = __builtin_fmaf(p[j][q], ROW ? sn[i & 3][q] * x.s[j] : x.s[j], acc[i][j][q]);
-    };
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       if (i + 1 < NA) {
         read_w(buf, i + 1);
       } else {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads) : "memory");
         __builtin_amdgcn_sched_barrier(0);
-        issue(kt + 2, buf);
-        read_x(buf ^ 1, kt + 1, next);
+        issue(kt + S::ST, buf);
       }
       const i32x8 w = wf[i & 1];
       if constexpr (EXACT) {
@@ -267,7 +281,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
           for (int j = 0; j < MB; ++j) {
             f32x4 &t = POW2 ? acc[i][j] : p[j];
-            if (!POW2 && c == 0 && i > 0) fold(i - 1, j);
+            if (!POW2 && c == 0) fold_before(i, j, x, next);
             t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[j][c],
                                                         !POW2 && c == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : t, 0, 0, 0);
           }
@@ -279,28 +293,37 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
       } else {
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          if (i > 0) fold(i - 1, j);
+          fold_before(i, j, x, next);
           p[j] = mfma_slab(w, x.f[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (i + 1 == NA) read_w(buf ^ 1, 0);
     }
-    if constexpr (!POW2) {
-#pragma unroll
-      for (int j = 0; j < MB; ++j) fold(NA - 1, j);
-    }
+    if constexpr (ROW && !POW2) sl = sn[(NA - 1) & 3];
+    read_w(nbuf, 0);
+    read_x(nbuf, next);
   };
-  issue(0, 0);
-  issue(1, 1);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LW + LX + 1) : "memory");   // slab 0 landed
-  read_x(0, 0, ra);
+#pragma unroll
+  for (int i = 0; i < S::ST; ++i) issue(i, i);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 1) * kLoads) : "memory");   // slab 0 landed
+  read_x(0, ra);
   read_w(0, 0);
+  static_assert((S::ST & (S::ST - 1)) == 0, "slab kt is in buffer kt % ST");
+  constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
   for (; kt + 1 < NB; kt += 2) {
-    slab(kt, ra, rb);
-    slab(kt + 1, rb, ra);
+    slab(kt, kt & kMask, (kt + 1) & kMask, ra, rb);
+    slab(kt + 1, (kt + 1) & kMask, (kt + 2) & kMask, rb, ra);
   }
-  if (kt < NB) slab(kt, ra, rb);
+  if (kt < NB) {
+    slab(kt, kt & kMask, (kt + 1) & kMask, ra, rb);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) rb.s[j] = ra.s[j];
+  }
+  if constexpr (!POW2) {
+#pragma unroll
+    for (int j = 0; j < MB; ++j) fold(NA - 1, j, rb.s[j], sl);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands after the workgroup has ended
   if constexpr (POW2) {
     if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
@@ -421,9 +444,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
 
 // ---------------------------------------------------------------------------
 
-typedef LinShape<2, 4, 8, 4> LinShape256;   // 256 x 256, 8 waves of 128 x 64
-typedef LinShape<2, 2, 4, 4> LinShape128;   // 128 x 128, 4 waves of 64 x 64
-typedef LinShape<2, 2, 2, 2> LinShape64;    // 64 x 64, 4 waves of 32 x 32
+typedef LinShape<2, 4, 8, 4, 2> LinShape256;   // 256 x 256, 8 waves of 128 x 64
+typedef LinShape<2, 2, 4, 4, 2> LinShape128;   // 128 x 128, 4 waves of 64 x 64
+typedef LinShape<2, 2, 2, 2, 4> LinShape64;    // 64 x 64, 4 waves of 32 x 32
 
 static int64_t tiles_of(const Linear &n, int32_t b) {
   return (int64_t)((n.M + b - 1) / b) * ((n.N + b - 1) / b);
