@@ -147,25 +147,19 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
   const int wn = wv / S::WM, wm = wv % S::WM;
 
-  // resources over the tile's rows (32-bit offsets: K <= 2^22); rows past the end read the last
+  // resources over the tile's rows (32-bit offsets: K <= 2^22); rows past the end are out of their
+  // range, by the lane's offset alone, and read as zeros
   const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(a.w + (int64_t)n0 * KV), (short)0, wrows * a.K, kBufDword3);
   const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(a.x + (int64_t)m0 * KV), (short)0, rows * a.K, kBufDword3);
   constexpr int LW = S::BN * kChunks / S::threads, LX = S::BM * kChunks / S::threads;
   static_assert(LW * S::threads == S::BN * kChunks && LX * S::threads == S::BM * kChunks, "whole loads");
-  // slot q of a slab holds chunk (q % 8) ^ ((r / 2) % 8) of row r = q / 8
-  uint32_t ow[LW], ox[LX];
-#pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    const int q = i * S::threads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
-    ow[i] = (uint32_t)(((r < wrows ? r : wrows - 1) * KV + c) * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < LX; ++i) {
-    const int q = i * S::threads + tid, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
-    ox[i] = (uint32_t)(((r < rows ? r : rows - 1) * KV + c) * 16);
-  }
+  // Slot q of a slab holds chunk (q % 8) ^ ((r / 2) % 8) of row r = q / 8.  A load of
+  // the workgroup fills kStep rows (a multiple of 16: the same chunk in each).
+  constexpr int kStep = S::threads / 8;
+  static_assert(kStep % 16 == 0, "the swizzle repeats");
+  const uint32_t off = (uint32_t)(((tid >> 3) * KV + ((tid & 7) ^ ((tid >> 4) & 7))) * 16);
   // the slab's scales: each wave brings 64 (some the same ones as another)
   static_assert(NS / 64 <= S::WN * S::WM, "a load of scales a wave");
   const int part = wv % (NS / 64);
@@ -181,18 +175,23 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const __amdgpu_buffer_rsrc_t rQ = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(a.ws + (ROW ? 0 : (int64_t)(sq < nsq ? sq : nsq - 1) * NB)), (short)0, NB * 4, kBufDword3);
   constexpr int kLoads = LW + LX + (ROW ? 1 : 2);   // of a wave, a slab
-  const auto issue = [&](int32_t k, int buf) {
+  // loads lo .. hi - 1 of slab k's kLoads
+  const auto issue = [&](int32_t k, int buf, int lo, int hi) {
     const int32_t kt = k < NB ? k : NB - 1;   // past the end: the last slab again, which nobody reads
 #pragma unroll
-    for (int i = 0; i < LW; ++i)
-      lds_load16(rW, LDS_ADDR(&sw[buf][i * S::threads + wv * 64]), ow[i], kt * 128);
-#pragma unroll
-    for (int i = 0; i < LX; ++i)
-      lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), ox[i], kt * 128);
-    lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, kt * 4);
-    if constexpr (!ROW) lds_load4(rQ, LDS_ADDR(&ssq[buf][wv * 64]), 0u, kt * 4);
+    for (int i = lo; i < hi; ++i) {
+      if (i < LX) lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), off + (uint32_t)(i * kStep * a.K), kt * 128);
+      else if (i < LX + LW)
+        lds_load16(rW, LDS_ADDR(&sw[buf][(i - LX) * S::threads + wv * 64]), off + (uint32_t)((i - LX) * kStep * a.K), kt * 128);
+      else if (i == LX + LW) lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, kt * 4);
+      else lds_load4(rQ, LDS_ADDR(&ssq[buf][ROW ? 0 : wv * 64]), 0u, kt * 4);
+    }
   };
-  const int rl = lane & 15, cl = 2 * (lane >> 4);
+  // a lane's 32 codes of a slab are chunks q and q + 4 of its row, q = lane / 16 (the same for both
+  // operands, which is all the product needs): the 16 lanes that LDS serves at a time -- 0-3, 12-15,
+  // 20-27, then 4-11, 16-19, 28-31 -- then meet 16 different places of its 256-byte rows, where
+  // chunks 2 q and 2 q + 1 met every one twice
+  const int rl = lane & 15, cl = lane >> 4;
 
   f32x4 acc[NA][MB];
 #pragma unroll
@@ -204,125 +203,135 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   float wsc[2];      // row scales with POW2: those of the two fragments' rows
   f32x4 sn[4], sl;   // ... without: of the lane's four channels in the fragments; in the slab's last one
   f32x4 p[MB];       // the last step's partial sums, folded under the next step's products
-  struct Rows {
-    i32x8 f[MB];     // the wave's token fragments
-    float s[MB];     // and scales, times the square's (POW2: alone)
-    float sq;        // the square's
-  } ra, rb;
+  i32x8 xf[MB];      // the wave's token fragments
+  float sa[MB], sb[MB], qa = 1.0f, qb = 1.0f;   // their scales (times the square's, POW2: apart), two slabs in turn
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
     p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    rb.s[j] = 0.0f;
+    sb[j] = 0.0f;
   }
   sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto read_w = [&](int buf, int i) {
     const int r = (wn * NA + i) * 16 + rl;
-    wf[i & 1] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 1)]);
+    wf[i & 1] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
     if constexpr (POW2 && ROW) wsc[i & 1] = ssc[buf][S::BM + r];
     if constexpr (!POW2 && ROW)
       sn[i & 3] = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4]);
   };
-  const auto read_x = [&](int buf, Rows &o) {
-    o.sq = ROW ? 1.0f : ssq[buf][wv * 64 + lane];
+  const auto read_x = [&](int buf, int j) {
+    const int r = (wm * MB + j) * 16 + rl;
+    xf[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 4)]);
+  };
+  const auto read_s = [&](int buf, float (&f)[MB], float &q) {
+    q = ROW ? 1.0f : ssq[buf][ROW ? 0 : wv * 64 + lane];
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
-      const int r = (wm * MB + j) * 16 + rl;
-      o.f[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 1)]);
-      o.s[j] = POW2 || ROW ? ssc[buf][r] : ssc[buf][r] * o.sq;
+      const float v = ssc[buf][(wm * MB + j) * 16 + rl];
+      f[j] = POW2 || ROW ? v : v * q;
     }
   };
   const auto fold = [&](int i, int j, float f, const f32x4 &n) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[j][q], ROW ? n[q] * f : f, acc[i][j][q]);
   };
-  const auto fold_before = [&](int i, int j, const Rows &x, const Rows &before) {
-    if (i > 0) fold(i - 1, j, x.s[j], sn[(i - 1) & 3]);
-    else fold(NA - 1, j, before.s[j], sl);
-  };
-  // A slab whose token fragments and first weight fragment are in registers.
-  // Before its last step everyone's reads of it are done and the next slab has
-  // landed: slab kt + ST is sent for, into its place, and the next slab's first
-  // fragments are read under the last step's products.  A step's sums are folded
-  // under the next step's products (the last one's under the next slab's first,
-  // with the scales of before, which `next` still holds); sched_barrier keeps the
-  // compiler from folding each sum at once, waiting for it.
-  const auto slab = [&](int32_t kt, int buf, int nbuf, Rows &x, Rows &next) {
+  // A slab whose token fragments, first weight fragment and scales f, fq are in
+  // registers.  Before its last step everyone's reads of it are done and the next
+  // slab has landed: slab kt + ST is sent for, into its place, and the next slab's
+  // first fragments are read, a token fragment as soon as the last products that
+  // use its registers are under way.  A step's sums are folded under the next step's
+  // products (the last one's under the next slab's first, with that slab's scales
+  // g, which the next slab's replace only then).  sched_barrier holds that order:
+  // left alone, the compiler folds each sum at once and waits for it.
+  const auto slab = [&](int32_t kt, int buf, int nbuf, float (&f)[MB], float &fq, float (&g)[MB], float &gq) {
     bf16x8 xb[EXACT ? MB : 1][4];
     if constexpr (EXACT) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) widen(x.f[j], POW2 ? x.s[j] : 1.0f, xb[j]);
+      for (int j = 0; j < MB; ++j) widen(xf[j], POW2 ? f[j] : 1.0f, xb[j]);
     }
     int ex[MB], eq = 127;
     if constexpr (POW2) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) ex[j] = (int)scale_exponent(x.s[j], &bad);
-      if constexpr (!ROW) eq = (int)scale_exponent(x.sq, &bad);
+      for (int j = 0; j < MB; ++j) ex[j] = (int)scale_exponent(f[j], &bad);
+      if constexpr (!ROW) eq = (int)scale_exponent(fq, &bad);
     }
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      if (i + 1 < NA) {
+      const bool last = i + 1 == NA;
+      const i32x8 w = wf[i & 1];
+      const float ws = POW2 && ROW ? wsc[i & 1] : fq;
+      const f32x4 n = i > 0 ? sn[(i - 1) & 3] : sl;
+      if (!last) {
         read_w(buf, i + 1);
       } else {
+        if constexpr (ROW && !POW2) sl = sn[i & 3];
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads) : "memory");
         __builtin_amdgcn_sched_barrier(0);
-        issue(kt + S::ST, buf);
+        read_w(nbuf, 0);
+        read_s(nbuf, g, gq);
       }
-      const i32x8 w = wf[i & 1];
+      // what goes out under products j of the last step
+      const auto behind = [&](int j) {
+        if (last) {
+          read_x(nbuf, j);
+          issue(kt + S::ST, buf, j * kLoads / MB, (j + 1) * kLoads / MB);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
       if constexpr (EXACT) {
         bf16x8 wb[4];
-        float f = 1.0f;
-        if constexpr (POW2) {
-          f = ROW ? wsc[i & 1] : x.sq;
-          if constexpr (ROW) (void)scale_exponent(f, &bad);
-        }
-        widen(w, f, wb);
+        if constexpr (POW2 && ROW) (void)scale_exponent(ws, &bad);
+        widen(w, POW2 ? ws : 1.0f, wb);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int j = 0; j < MB; ++j) {
             f32x4 &t = POW2 ? acc[i][j] : p[j];
-            if (!POW2 && c == 0) fold_before(i, j, x, next);
+            if (!POW2 && c == 0) fold(i > 0 ? i - 1 : NA - 1, j, i > 0 ? f[j] : g[j], n);
             t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[j][c],
                                                         !POW2 && c == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : t, 0, 0, 0);
+            if (c == 1) behind(j);
           }
       } else if constexpr (POW2) {
-        const int ew = ROW ? (int)scale_exponent(wsc[i & 1], &bad) : eq;
+        const int ew = ROW ? (int)scale_exponent(ws, &bad) : eq;
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x.f[j], acc[i][j], 0, 0, 0, ew, 0, ex[j]);
+        for (int j = 0; j < MB; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xf[j], acc[i][j], 0, 0, 0, ew, 0, ex[j]);
+          behind(j);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          fold_before(i, j, x, next);
-          p[j] = mfma_slab(w, x.f[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-          __builtin_amdgcn_sched_barrier(0);
+          fold(i > 0 ? i - 1 : NA - 1, j, i > 0 ? f[j] : g[j], n);
+          p[j] = mfma_slab(w, xf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          behind(j);
         }
       }
     }
-    if constexpr (ROW && !POW2) sl = sn[(NA - 1) & 3];
-    read_w(nbuf, 0);
-    read_x(nbuf, next);
   };
 #pragma unroll
-  for (int i = 0; i < S::ST; ++i) issue(i, i);
+  for (int i = 0; i < S::ST; ++i) issue(i, i, 0, kLoads);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 1) * kLoads) : "memory");   // slab 0 landed
-  read_x(0, ra);
+#pragma unroll
+  for (int j = 0; j < MB; ++j) read_x(0, j);
+  read_s(0, sa, qa);
   read_w(0, 0);
-  static_assert((S::ST & (S::ST - 1)) == 0, "slab kt is in buffer kt % ST");
+  static_assert((S::ST & (S::ST - 1)) == 0 && S::ST >= 2, "slab kt is in buffer kt % ST");
   constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
   for (; kt + 1 < NB; kt += 2) {
-    slab(kt, kt & kMask, (kt + 1) & kMask, ra, rb);
-    slab(kt + 1, (kt + 1) & kMask, (kt + 2) & kMask, rb, ra);
+    const int b = S::ST == 2 ? 0 : kt & kMask;   // (kt is even)
+    slab(kt, b, b + 1, sa, qa, sb, qb);
+    slab(kt + 1, b + 1, S::ST == 2 ? 0 : (kt + 2) & kMask, sb, qb, sa, qa);
   }
   if (kt < NB) {
-    slab(kt, kt & kMask, (kt + 1) & kMask, ra, rb);
+    const int b = S::ST == 2 ? 0 : kt & kMask;
+    slab(kt, b, b + 1, sa, qa, sb, qb);
 #pragma unroll
-    for (int j = 0; j < MB; ++j) rb.s[j] = ra.s[j];
+    for (int j = 0; j < MB; ++j) sb[j] = sa[j];
   }
   if constexpr (!POW2) {
 #pragma unroll
-    for (int j = 0; j < MB; ++j) fold(NA - 1, j, rb.s[j], sl);
+    for (int j = 0; j < MB; ++j) fold(NA - 1, j, sb[j], sl);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands after the workgroup has ended
   if constexpr (POW2) {
@@ -355,13 +364,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16, KV = a.K / 16, NB = a.K / 128;
   const int32_t n = n0 + rl < a.N ? n0 + rl : a.N - 1;
-  const u32x4 *const pw = a.w + (int64_t)n * KV + 2 * q4;
+  const u32x4 *const pw = a.w + (int64_t)n * KV + q4;
   const u32x4 *px[MT];
   const float *ps[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int32_t m = m0 + j * 16 + rl < a.M ? m0 + j * 16 + rl : a.M - 1;
-    px[j] = a.x + (int64_t)m * KV + 2 * q4;
+    px[j] = a.x + (int64_t)m * KV + q4;
     ps[j] = a.xs + (int64_t)m * NB;
   }
   const float *pn[4];   // ROW: the scales of this lane's four channels
@@ -383,11 +392,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
       const int32_t k = k0 + u * kFewWaves;
       if (k >= NB) break;
       w[u][0] = load_stream(pw + k * 8);
-      w[u][1] = load_stream(pw + k * 8 + 1);
+      w[u][1] = load_stream(pw + k * 8 + 4);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         x[u][j][0] = px[j][k * 8];
-        x[u][j][1] = px[j][k * 8 + 1];
+        x[u][j][1] = px[j][k * 8 + 4];
         s[u][j] = ps[j][k];
       }
       if constexpr (ROW) {
