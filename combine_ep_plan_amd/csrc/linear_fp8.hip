@@ -199,12 +199,12 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   uint32_t bad = 0u;
-  i32x8 wf[2];
-  float wsc[2];      // row scales with POW2: those of the two fragments' rows
+  i32x8 wf[3];       // weight fragments: read two steps ahead
+  float wsc[3];      // row scales with POW2: those of the fragments' rows
   f32x4 sn[4], sl;   // ... without: of the lane's four channels in the fragments; in the slab's last one
   f32x4 p[MB];       // the last step's partial sums, folded under the next step's products
   i32x8 xf[MB];      // the wave's token fragments
-  float sa[MB], sb[MB], qa = 1.0f, qb = 1.0f;   // their scales (times the square's, POW2: apart), two slabs in turn
+  float sa[MB], sb[MB], qa = 1.0f, qb = 1.0f;   // their scales and the square's, two slabs in turn
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
     p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -213,8 +213,8 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto read_w = [&](int buf, int i) {
     const int r = (wn * NA + i) * 16 + rl;
-    wf[i & 1] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
-    if constexpr (POW2 && ROW) wsc[i & 1] = ssc[buf][S::BM + r];
+    wf[i % 3] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
+    if constexpr (POW2 && ROW) wsc[i % 3] = ssc[buf][S::BM + r];
     if constexpr (!POW2 && ROW)
       sn[i & 3] = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4]);
   };
@@ -225,24 +225,29 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const auto read_s = [&](int buf, float (&f)[MB], float &q) {
     q = ROW ? 1.0f : ssq[buf][ROW ? 0 : wv * 64 + lane];
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      const float v = ssc[buf][(wm * MB + j) * 16 + rl];
-      f[j] = POW2 || ROW ? v : v * q;
-    }
+    for (int j = 0; j < MB; ++j) f[j] = ssc[buf][(wm * MB + j) * 16 + rl];
   };
   const auto fold = [&](int i, int j, float f, const f32x4 &n) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[j][q], ROW ? n[q] * f : f, acc[i][j][q]);
   };
-  // A slab whose token fragments, first weight fragment and scales f, fq are in
-  // registers.  Before its last step everyone's reads of it are done and the next
-  // slab has landed: slab kt + ST is sent for, into its place, and the next slab's
-  // first fragments are read, a token fragment as soon as the last products that
-  // use its registers are under way.  A step's sums are folded under the next step's
-  // products (the last one's under the next slab's first, with that slab's scales
-  // g, which the next slab's replace only then).  sched_barrier holds that order:
-  // left alone, the compiler folds each sum at once and waits for it.
+  // A slab whose token fragments, first two weight fragments and scales f, fq are
+  // in registers.  Before its last step everyone's reads of it are done and the
+  // next slab has landed: the next slab's first fragments are read, a token fragment
+  // as soon as the last products that use its registers are under way, and slab
+  // kt + ST is sent for, into this one's place, LP loads behind each product from
+  // there on into the next slab (all at once they hold up the products behind
+  // them).  A step's sums are folded under the next step's products (the last one's
+  // under the next slab's first, with that slab's scales g, which the next slab's
+  // replace only then).  sched_barrier holds that order: left alone, the compiler
+  // folds each sum at once and waits for it.
+  constexpr int LP = (kLoads + NA * MB - 1) / (NA * MB);
+  constexpr int kFirst = MB * LP < kLoads ? MB * LP : kLoads;   // a slab's loads under the last step
   const auto slab = [&](int32_t kt, int buf, int nbuf, float (&f)[MB], float &fq, float (&g)[MB], float &gq) {
+    if constexpr (!ROW && !POW2) {
+#pragma unroll
+      for (int j = 0; j < MB; ++j) f[j] *= fq;
+    }
     bf16x8 xb[EXACT ? MB : 1][4];
     if constexpr (EXACT) {
 #pragma unroll
@@ -257,24 +262,25 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const bool last = i + 1 == NA;
-      const i32x8 w = wf[i & 1];
-      const float ws = POW2 && ROW ? wsc[i & 1] : fq;
+      const i32x8 w = wf[i % 3];
+      const float ws = POW2 && ROW ? wsc[i % 3] : fq;
       const f32x4 n = i > 0 ? sn[(i - 1) & 3] : sl;
-      if (!last) {
-        read_w(buf, i + 1);
-      } else {
+      if (i + 2 < NA) read_w(buf, i + 2);
+      if (last) {
         if constexpr (ROW && !POW2) sl = sn[i & 3];
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads) : "memory");
         __builtin_amdgcn_sched_barrier(0);
         read_w(nbuf, 0);
+        read_w(nbuf, 1);
         read_s(nbuf, g, gq);
       }
-      // what goes out under products j of the last step
+      // what goes out behind product j: loads at .. at + LP - 1 of slab kt + ST in the
+      // last step, of slab kt - 1 + ST before
       const auto behind = [&](int j) {
-        if (last) {
-          read_x(nbuf, j);
-          issue(kt + S::ST, buf, j * kLoads / MB, (j + 1) * kLoads / MB);
-        }
+        if (last) read_x(nbuf, j);
+        const int at = (last ? j : (i + 1) * MB + j) * LP;
+        issue(last ? kt + S::ST : kt - 1 + S::ST, last ? buf : (S::ST == 2 ? nbuf : (kt - 1) & (S::ST - 1)), at,
+              at + LP < kLoads ? at + LP : kLoads);
         __builtin_amdgcn_sched_barrier(0);
       };
       if constexpr (EXACT) {
@@ -309,12 +315,13 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     }
   };
 #pragma unroll
-  for (int i = 0; i < S::ST; ++i) issue(i, i, 0, kLoads);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 1) * kLoads) : "memory");   // slab 0 landed
+  for (int i = 0; i < S::ST; ++i) issue(i, i, 0, i + 1 < S::ST ? kLoads : kFirst);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads + kFirst) : "memory");   // slab 0 landed
 #pragma unroll
   for (int j = 0; j < MB; ++j) read_x(0, j);
   read_s(0, sa, qa);
   read_w(0, 0);
+  read_w(0, 1);
   static_assert((S::ST & (S::ST - 1)) == 0 && S::ST >= 2, "slab kt is in buffer kt % ST");
   constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
