@@ -134,10 +134,15 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
                                                               int32_t span) {
   constexpr bool EXACT = OUT == kOutFp32;
   constexpr int NA = S::NA, MB = S::MB;
-  constexpr int NS = S::BM + (ROW ? S::BN : 0);   // scales a slab
+  // rows whose scales a tile reads: its tokens', then its channels' or its squares'
+  constexpr int NS = S::BM + (ROW ? S::BN : 64);
   __shared__ u32x4 sw[S::ST][S::BN * kChunks], sx[S::ST][S::BM * kChunks];
-  __shared__ __attribute__((aligned(16))) float ssc[S::ST][NS];
-  __shared__ float ssq[S::ST][ROW ? 1 : S::threads];   // a square's scale, for every lane of the wave
+  // Four slabs' scales a buffer.  Those of the four after are under way beside them; slab
+  // kt + ST goes out when slab kt + 1 is next to be read, whose four lie one buffer back
+  // with ST 2, up to two with ST 4.
+  constexpr int SB = S::ST == 2 ? 2 : 4;
+  static_assert(S::ST == 2 || S::ST == 4, "slabs in LDS");
+  __shared__ __attribute__((aligned(16))) float ssc[SB][NS][4];
   int32_t mt, nt;
   if (!linear_tile(tm, tn, span, mt, nt)) return;
   const int32_t m0 = mt * S::BM, n0 = nt * S::BN;
@@ -160,21 +165,25 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   constexpr int kStep = S::threads / 8;
   static_assert(kStep % 16 == 0, "the swizzle repeats");
   const uint32_t off = (uint32_t)(((tid >> 3) * KV + ((tid & 7) ^ ((tid >> 4) & 7))) * 16);
-  // the slab's scales: each wave brings 64 (some the same ones as another)
+  // Scales travel four slabs at a time, since a row's lie next to each other (16
+  // lines a load, where one slab's scales of 64 rows are 64): with slab k go the
+  // scales of rows 16 ((k + 3) % 4) .. + 15 of each 64 for slabs 4 g .. 4 g + 3, g =
+  // (k + 3) / 4, so that they are whole with slab 4 g.  Each wave brings 64 rows'
+  // (some the same ones as another).
   static_assert(NS / 64 <= S::WN * S::WM, "a load of scales a wave");
+  const int32_t nsq = (a.N + 127) / 128;
   const int part = wv % (NS / 64);
   const bool of_x = part < S::BM / 64;   // wave-uniform
-  const int srow = (of_x ? part : part - S::BM / 64) * 64 + lane, slast = (of_x ? rows : wrows) - 1;
-  const uint32_t osc = (uint32_t)((srow < slast ? srow : slast) * NB * 4);
+  const int32_t first = of_x ? 0 : ROW ? n0 : n0 / 128, left = (of_x ? rows : ROW ? wrows : nsq - first);
+  const uint32_t osc = (uint32_t)((((of_x ? part : part - S::BM / 64) * 64 + (lane >> 2)) * NB + (lane & 3)) * 4);
   const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)n0 * NB), (short)0,
-      (of_x ? rows : wrows) * NB * 4, kBufDword3);
-  // the square that holds the wave's channels
+      (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)first * NB), (short)0,
+      (left < 512 ? left : 512) * NB * 4, kBufDword3);
+  const auto issue_scales = [&](int32_t four, int piece) {   // rows past the end, slabs past the last: unused
+    lds_load4(rS, LDS_ADDR(&ssc[four & (SB - 1)][part * 64 + piece * 16][0]), osc + (uint32_t)(piece * 16 * NB * 4), four * 16);
+  };
   static_assert(128 % (NA * 16) == 0 && NA % 2 == 0, "a wave's channels lie in one square");
-  const int32_t nsq = (a.N + 127) / 128, sq = (n0 + wn * NA * 16) / 128;
-  const __amdgpu_buffer_rsrc_t rQ = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(a.ws + (ROW ? 0 : (int64_t)(sq < nsq ? sq : nsq - 1) * NB)), (short)0, NB * 4, kBufDword3);
-  constexpr int kLoads = LW + LX + (ROW ? 1 : 2);   // of a wave, a slab
+  constexpr int kLoads = LW + LX + 1;   // of a wave, a slab
   // loads lo .. hi - 1 of slab k's kLoads
   const auto issue = [&](int32_t k, int buf, int lo, int hi) {
     const int32_t kt = k < NB ? k : NB - 1;   // past the end: the last slab again, which nobody reads
@@ -183,8 +192,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
       if (i < LX) lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), off + (uint32_t)(i * kStep * a.K), kt * 128);
       else if (i < LX + LW)
         lds_load16(rW, LDS_ADDR(&sw[buf][(i - LX) * S::threads + wv * 64]), off + (uint32_t)((i - LX) * kStep * a.K), kt * 128);
-      else if (i == LX + LW) lds_load4(rS, LDS_ADDR(&ssc[buf][part * 64]), osc, kt * 4);
-      else lds_load4(rQ, LDS_ADDR(&ssq[buf][ROW ? 0 : wv * 64]), 0u, kt * 4);
+      else issue_scales((k + 3) >> 2, (k + 3) & 3);
     }
   };
   // a lane's 32 codes of a slab are chunks q and q + 4 of its row, q = lane / 16 (the same for both
@@ -211,21 +219,33 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     sb[j] = 0.0f;
   }
   sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const auto read_w = [&](int buf, int i) {
+  // POW2: scales of rows past the end are none of the caller's
+  const int xlive = rows - wm * MB * 16 - rl, wlive = wrows - wn * NA * 16 - rl;
+  const auto read_w = [&](int buf, int32_t k, int i) {
     const int r = (wn * NA + i) * 16 + rl;
     wf[i % 3] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
-    if constexpr (POW2 && ROW) wsc[i % 3] = ssc[buf][S::BM + r];
-    if constexpr (!POW2 && ROW)
-      sn[i & 3] = *reinterpret_cast<const f32x4 *>(&ssc[buf][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4]);
+    if constexpr (POW2 && ROW) {
+      const float v = ssc[(k >> 2) & (SB - 1)][S::BM + r][k & 3];
+      wsc[i % 3] = i * 16 < wlive ? v : 1.0f;
+    }
+    if constexpr (!POW2 && ROW) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sn[i & 3][q] = ssc[(k >> 2) & (SB - 1)][S::BM + (wn * NA + i) * 16 + (lane >> 4) * 4 + q][k & 3];
+    }
   };
   const auto read_x = [&](int buf, int j) {
     const int r = (wm * MB + j) * 16 + rl;
     xf[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 4)]);
   };
-  const auto read_s = [&](int buf, float (&f)[MB], float &q) {
-    q = ROW ? 1.0f : ssq[buf][ROW ? 0 : wv * 64 + lane];
+  const auto read_s = [&](int32_t k, float (&f)[MB], float &q) {
+    q = ROW ? 1.0f : ssc[(k >> 2) & (SB - 1)][ROW ? 0 : S::BM + wn * NA * 16 / 128][k & 3];
 #pragma unroll
-    for (int j = 0; j < MB; ++j) f[j] = ssc[buf][(wm * MB + j) * 16 + rl];
+    for (int j = 0; j < MB; ++j) {
+      const float v = ssc[(k >> 2) & (SB - 1)][(wm * MB + j) * 16 + rl][k & 3];
+      f[j] = !POW2 || j * 16 < xlive ? v : 1.0f;
+    }
+    if (POW2 && wn * NA * 16 >= wrows) q = 1.0f;
   };
   const auto fold = [&](int i, int j, float f, const f32x4 &n) {
 #pragma unroll
@@ -265,14 +285,14 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
       const i32x8 w = wf[i % 3];
       const float ws = POW2 && ROW ? wsc[i % 3] : fq;
       const f32x4 n = i > 0 ? sn[(i - 1) & 3] : sl;
-      if (i + 2 < NA) read_w(buf, i + 2);
+      if (i + 2 < NA) read_w(buf, kt, i + 2);
       if (last) {
         if constexpr (ROW && !POW2) sl = sn[i & 3];
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads) : "memory");
         __builtin_amdgcn_sched_barrier(0);
-        read_w(nbuf, 0);
-        read_w(nbuf, 1);
-        read_s(nbuf, g, gq);
+        read_w(nbuf, kt + 1, 0);
+        read_w(nbuf, kt + 1, 1);
+        read_s(kt + 1, g, gq);
       }
       // what goes out behind product j: loads at .. at + LP - 1 of slab kt + ST in the
       // last step, of slab kt - 1 + ST before
@@ -315,13 +335,15 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     }
   };
 #pragma unroll
+  for (int i = 0; i < 4; ++i) issue_scales(0, i);
+#pragma unroll
   for (int i = 0; i < S::ST; ++i) issue(i, i, 0, i + 1 < S::ST ? kLoads : kFirst);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads + kFirst) : "memory");   // slab 0 landed
 #pragma unroll
   for (int j = 0; j < MB; ++j) read_x(0, j);
   read_s(0, sa, qa);
-  read_w(0, 0);
-  read_w(0, 1);
+  read_w(0, 0, 0);
+  read_w(0, 0, 1);
   static_assert((S::ST & (S::ST - 1)) == 0 && S::ST >= 2, "slab kt is in buffer kt % ST");
   constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
