@@ -207,8 +207,10 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   uint32_t bad = 0u;
-  i32x8 wf[3];       // weight fragments: read two steps ahead
-  float wsc[3];      // row scales with POW2: those of the fragments' rows
+  // weight fragments, read two steps ahead (one where registers run out)
+  constexpr int WD = POW2 && NA == 8 ? 2 : 3;
+  i32x8 wf[WD];
+  float wsc[WD];     // row scales with POW2: those of the fragments' rows
   f32x4 sn[4], sl;   // ... without: of the lane's four channels in the fragments; in the slab's last one
   f32x4 p[MB];       // the last step's partial sums, folded under the next step's products
   i32x8 xf[MB];      // the wave's token fragments
@@ -223,10 +225,10 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const int xlive = rows - wm * MB * 16 - rl, wlive = wrows - wn * NA * 16 - rl;
   const auto read_w = [&](int buf, int32_t k, int i) {
     const int r = (wn * NA + i) * 16 + rl;
-    wf[i % 3] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
+    wf[i % WD] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
     if constexpr (POW2 && ROW) {
       const float v = ssc[(k >> 2) & (SB - 1)][S::BM + r][k & 3];
-      wsc[i % 3] = i * 16 < wlive ? v : 1.0f;
+      wsc[i % WD] = i * 16 < wlive ? v : 1.0f;
     }
     if constexpr (!POW2 && ROW) {
 #pragma unroll
@@ -282,16 +284,16 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const bool last = i + 1 == NA;
-      const i32x8 w = wf[i % 3];
-      const float ws = POW2 && ROW ? wsc[i % 3] : fq;
+      const i32x8 w = wf[i % WD];
+      const float ws = POW2 && ROW ? wsc[i % WD] : fq;
       const f32x4 n = i > 0 ? sn[(i - 1) & 3] : sl;
-      if (i + 2 < NA) read_w(buf, kt, i + 2);
+      if (i + WD - 1 < NA) read_w(buf, kt, i + WD - 1);
       if (last) {
         if constexpr (ROW && !POW2) sl = sn[i & 3];
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * kLoads) : "memory");
         __builtin_amdgcn_sched_barrier(0);
         read_w(nbuf, kt + 1, 0);
-        read_w(nbuf, kt + 1, 1);
+        if constexpr (WD == 3) read_w(nbuf, kt + 1, 1);
         read_s(kt + 1, g, gq);
       }
       // what goes out behind product j: loads at .. at + LP - 1 of slab kt + ST in the
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   for (int j = 0; j < MB; ++j) read_x(0, j);
   read_s(0, sa, qa);
   read_w(0, 0, 0);
-  read_w(0, 0, 1);
+  if constexpr (WD == 3) read_w(0, 0, 1);
   static_assert((S::ST & (S::ST - 1)) == 0 && S::ST >= 2, "slab kt is in buffer kt % ST");
   constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
@@ -379,102 +381,124 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 // ---------------------------------------------------------------------------
 // few tokens
 //
-// The weights are streamed once: a workgroup takes 16 channels, its eight waves
-// every eighth slab each, weights and tokens straight from memory into the
-// matrix instruction's registers, four slabs' loads in flight a wave.  The waves'
-// sums are joined through LDS in a fixed order.
+// The weights are streamed once: a workgroup takes 16 channels and all the tokens
+// (16 MT of them), its waves every so many slabs each.  A wave keeps a ring of slabs
+// in LDS of its own -- no barrier until the end -- filled by loads whose lanes
+// follow the memory: in the matrix instruction's order consecutive lanes are rows
+// apart and a load of 1 KB holds the address unit 88 cycles where it takes 22 (16
+// tokens, N 4096, K 7168: 11.0 us, straight into registers).  The waves' sums are
+// joined through LDS in a fixed order.
 
-constexpr int kFewWaves = 8, kFewSlabs = 4;
+template <int MT>
+struct FewShape {
+  static constexpr int waves = MT == 4 ? 4 : 8, ring = MT == 1 ? 4 : 3;   // LDS: 147, 160, 129 KB
+};
 
 template <int MT, bool ROW, bool POW2, int OUT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
-  __shared__ f32x4 red[kFewWaves][MT * 64];
+__global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(LinArgs a) {
+  constexpr int W = FewShape<MT>::waves, R = FewShape<MT>::ring;
+  __shared__ u32x4 slabs[W][R][(1 + MT) * 16 * kChunks];   // 16 rows of weights, then the tokens
+  __shared__ float scales[W][R][128];                      // the tokens', then the channels' or the square's
   const int tid = threadIdx.x, lane = tid & 63, rl = lane & 15, q4 = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16, KV = a.K / 16, NB = a.K / 128;
-  const int32_t n = n0 + rl < a.N ? n0 + rl : a.N - 1;
-  const u32x4 *const pw = a.w + (int64_t)n * KV + q4;
-  const u32x4 *px[MT];
-  const float *ps[MT];
+  const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16, NB = a.K / 128;
+  const int32_t rows = a.M - m0 < MT * 16 ? a.M - m0 : MT * 16, wrows = a.N - n0 < 16 ? a.N - n0 : 16;
+  const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.w + (int64_t)n0 * (a.K / 16)), (short)0, wrows * a.K, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.x + (int64_t)m0 * (a.K / 16)), (short)0, rows * a.K, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rXS = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.xs + (int64_t)m0 * NB), (short)0, rows * NB * 4, kBufDword3);
+  const __amdgpu_buffer_rsrc_t rWS = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.ws + (int64_t)(ROW ? n0 : n0 / 128) * NB), (short)0, (ROW ? wrows : 1) * NB * 4, kBufDword3);
+  // eight rows a load, chunks in the order of swz; rows past the end are out of range
+  const uint32_t off = (uint32_t)((lane >> 3) * a.K + ((lane & 7) ^ ((lane >> 4) & 3)) * 16);
+  const uint32_t oxs = (uint32_t)((lane < rows ? lane : rows - 1) * NB * 4);
+  const uint32_t ows = ROW ? (uint32_t)((rl < wrows ? rl : wrows - 1) * NB * 4) : 0u;
+  constexpr int kLoads = 2 + 2 * MT + 2;
+  const auto issue = [&](int32_t k, int slot) {
+    u32x4 *const d = slabs[wv][slot];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int32_t m = m0 + j * 16 + rl < a.M ? m0 + j * 16 + rl : a.M - 1;
-    px[j] = a.x + (int64_t)m * KV + q4;
-    ps[j] = a.xs + (int64_t)m * NB;
-  }
-  const float *pn[4];   // ROW: the scales of this lane's four channels
+    for (int i = 0; i < 2; ++i)   // rows 8 i ..: their chunks are permuted by 4 i more
+      lds_load16_stream(rW, LDS_ADDR(d + i * 64), (off ^ (uint32_t)(i * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int32_t c = n0 + q4 * 4 + r < a.N ? n0 + q4 * 4 + r : a.N - 1;
-    pn[r] = a.ws + (int64_t)c * NB;
-  }
-  const float *const wsq = a.ws + (int64_t)(n0 / 128) * NB;
+    for (int i = 0; i < 2 * MT; ++i)
+      lds_load16(rX, LDS_ADDR(d + (2 + i) * 64), (off ^ (uint32_t)((i & 1) * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
+    lds_load4(rXS, LDS_ADDR(&scales[wv][slot][0]), oxs, k * 4);
+    lds_load4(rWS, LDS_ADDR(&scales[wv][slot][64]), ows, k * 4);
+  };
   uint32_t bad = 0u;
   f32x4 acc[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int32_t k0 = wv; k0 < NB; k0 += kFewWaves * kFewSlabs) {
-    u32x4 w[kFewSlabs][2], x[kFewSlabs][MT][2];
-    float s[kFewSlabs][MT], sn[kFewSlabs][4];
+  // slab in `slot`, landed; `next`, if it is one, is sent for into its place once it is read
+  const auto slab = [&](int slot, int32_t next) {
+    const u32x4 *const d = slabs[wv][slot];
+    const float *const sc = scales[wv][slot];
+    const i32x8 fw = join_codes(d[swz(rl, q4)], d[swz(rl, q4 + 4)]);
+    i32x8 fx[MT];
+    float s[MT];
+    f32x4 sn;
 #pragma unroll
-    for (int u = 0; u < kFewSlabs; ++u) {
-      const int32_t k = k0 + u * kFewWaves;
-      if (k >= NB) break;
-      w[u][0] = load_stream(pw + k * 8);
-      w[u][1] = load_stream(pw + k * 8 + 4);
+    for (int j = 0; j < MT; ++j) {
+      fx[j] = join_codes(d[swz((1 + j) * 16 + rl, q4)], d[swz((1 + j) * 16 + rl, q4 + 4)]);
+      s[j] = sc[j * 16 + rl];
+    }
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        x[u][j][0] = px[j][k * 8];
-        x[u][j][1] = px[j][k * 8 + 4];
-        s[u][j] = ps[j][k];
-      }
-      if constexpr (ROW) {
+    for (int r = 0; r < 4; ++r) sn[r] = sc[64 + (ROW ? q4 * 4 + r : 0)];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (next < NB) issue(next, slot);
+    bf16x8 wb[4];
+    if constexpr (OUT == kOutFp32) widen(fw, 1.0f, wb);
+    if constexpr (POW2) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sn[u][r] = pn[r][k];
+      for (int j = 0; j < MT; ++j) (void)scale_exponent(s[j], &bad);
+#pragma unroll
+      for (int r = 0; r < (ROW ? 4 : 1); ++r) (void)scale_exponent(sn[r], &bad);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (OUT == kOutFp32) {
+        bf16x8 xb[4];
+        widen(fx[j], 1.0f, xb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[c], p, 0, 0, 0);
       } else {
-        sn[u][0] = wsq[k];
+        p = mfma_slab(fw, fx[j], p);
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], sn[r] * s[j], acc[j][r]);
     }
+  };
+  int32_t k = wv;
 #pragma unroll
-    for (int u = 0; u < kFewSlabs; ++u) {
-      if (k0 + u * kFewWaves >= NB) break;
-      const i32x8 fw = join_codes(w[u][0], w[u][1]);
-      bf16x8 wb[4];
-      if constexpr (OUT == kOutFp32) widen(fw, 1.0f, wb);
-      if constexpr (POW2) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) (void)scale_exponent(s[u][j], &bad);
-#pragma unroll
-        for (int r = 0; r < (ROW ? 4 : 1); ++r) (void)scale_exponent(sn[u][r], &bad);
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const i32x8 fx = join_codes(x[u][j][0], x[u][j][1]);
-        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (OUT == kOutFp32) {
-          bf16x8 xb[4];
-          widen(fx, 1.0f, xb);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[c], p, 0, 0, 0);
-        } else {
-          p = mfma_slab(fw, fx, p);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[j][r] = __builtin_fmaf(p[r], (ROW ? sn[u][r] : sn[u][0]) * s[u][j], acc[j][r]);
-      }
-    }
+  for (int i = 0; i < R; ++i)
+    if (k + i * W < NB) issue(k + i * W, i);
+  int slot = 0;
+  for (; k + (R - 1) * W < NB; k += W) {   // R slabs under way: the first has landed
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 1) * kLoads) : "memory");
+    slab(slot, k + R * W);
+    slot = slot + 1 == R ? 0 : slot + 1;
   }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) red[wv][j * 64 + lane] = acc[j];
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  for (; k < NB; k += W) {
+    slab(slot, NB);
+    slot = slot + 1 == R ? 0 : slot + 1;
+  }
   if constexpr (POW2) {
     if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
   }
+  f32x4 *const red = reinterpret_cast<f32x4 *>(&slabs[0][0][0]);
+  static_assert(W * MT * 64 * 16 <= (int)sizeof(slabs), "the waves' sums fit");
   __syncthreads();
-  for (int e = tid; e < MT * 64; e += 64 * kFewWaves) {
-    f32x4 v = red[0][e];
 #pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) v += red[i][e];
+  for (int j = 0; j < MT; ++j) red[(wv * MT + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  for (int e = tid; e < MT * 64; e += 64 * W) {
+    f32x4 v = red[e];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v += red[i * MT * 64 + e];
     const int32_t m = m0 + (e >> 6) * 16 + (e & 15);
     if (m < a.M) store4<OUT>(a, m, n0 + ((e >> 4) & 3) * 4, v);
   }
@@ -482,10 +506,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_fp8_few(LinArgs a) {
 
 // ---------------------------------------------------------------------------
 
-typedef LinShape<2, 4, 8, 4, 2> LinShape256;   // 256 x 256, 8 waves of 128 x 64
-typedef LinShape<2, 2, 4, 4, 2> LinShape128;   // 128 x 128, 4 waves of 64 x 64
-typedef LinShape<2, 2, 2, 2, 4> LinShape64;    // 64 x 64, 4 waves of 32 x 32
+typedef LinShape<2, 4, 8, 4, 2> Shape256;      // 256 x 256, 8 waves of 128 x 64
+typedef LinShape<2, 4, 4, 3, 2> Shape128x192;  // 128 channels x 192 tokens, 8 waves of 64 x 48
+typedef LinShape<2, 2, 4, 4, 2> Shape128;      // 128 x 128, 4 waves of 64 x 64
+typedef LinShape<2, 2, 2, 2, 4> Shape64;       // 64 x 64, 4 waves of 32 x 32
 
+// What a slab costs a compute unit that has its share of the tiles: `one` us for a
+// tile alone, `two` for two side by side (0: they do not fit).
+template <class S>
+static double tiles_cost(const Linear &n, double one, double two) {
+  const int64_t tiles = (int64_t)((n.M + S::BM - 1) / S::BM) * ((n.N + S::BN - 1) / S::BN);
+  const int64_t each = (tiles + 255) / 256;
+  return two > 0.0 ? (double)(each / 2) * two + (double)(each % 2) * one : (double)each * one;
+}
 static int64_t tiles_of(const Linear &n, int32_t b) {
   return (int64_t)((n.M + b - 1) / b) * ((n.N + b - 1) / b);
 }
@@ -499,27 +532,37 @@ static void launch_tiles(const LinArgs &a, int32_t span, hipStream_t s) {
 
 template <bool ROW, bool POW2, int OUT>
 static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
-  if (n.M <= 64) {
+  // 33 to 64 tokens: while a compute unit has at most one workgroup of 16 channels (64 x 2048 x 7168
+  // 13.3 us against 16.6 with 64 x 64 tiles, 64 x 7168 x 2048 9.2 against 7.4)
+  if (n.M <= 32 || (n.M <= 64 && n.N <= 4096)) {
     const int mt = n.M <= 16 ? 1 : n.M <= 32 ? 2 : 4;
     const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
-#define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * kFewWaves), 0, s, a)
+#define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * FewShape<MT>::waves), 0, s, a)
     if (mt == 1) L(1);
     else if (mt == 2) L(2);
     else L(4);
 #undef L
     return;
   }
-  if constexpr (OUT != kOutFp32) {
-    if (tiles_of(n, 256) >= 192) return launch_tiles<LinShape256, ROW, POW2, OUT>(a, 4, s);
+  if constexpr (OUT == kOutFp32) {
+    const double c192 = tiles_cost<Shape128x192>(n, 1.3, 0.0), c128 = tiles_cost<Shape128>(n, 1.0, 1.7),
+                 c64 = tiles_cost<Shape64>(n, 0.36, 0.6);
+    if (c192 <= c128 && c192 <= c64) launch_tiles<Shape128x192, ROW, POW2, OUT>(a, 5, s);
+    else if (c128 <= c64) launch_tiles<Shape128, ROW, POW2, OUT>(a, 8, s);
+    else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
+  } else {
+    const double c256 = tiles_cost<Shape256>(n, 1.9, 0.0), c128 = tiles_cost<Shape128>(n, 0.77, 1.22),
+                 c64 = tiles_cost<Shape64>(n, 0.30, 0.54);
+    if (c256 <= c128 && c256 <= c64) launch_tiles<Shape256, ROW, POW2, OUT>(a, 4, s);
+    else if (c128 <= c64) launch_tiles<Shape128, ROW, POW2, OUT>(a, 8, s);
+    else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
   }
-  if (tiles_of(n, 128) >= 256) launch_tiles<LinShape128, ROW, POW2, OUT>(a, 8, s);
-  else launch_tiles<LinShape64, ROW, POW2, OUT>(a, 8, s);
 }
 
 // A launch counts its threads in 32 bits, and a tile index is an int32.
 bool linear_fp8_fits(const Linear &n) {
   const int64_t few = ((int64_t)n.N + 15) / 16;
-  return n.M <= 64 ? few * 64 * kFewWaves < (int64_t)1 << 32
+  return n.M <= 64 ? few * 512 < (int64_t)1 << 32
                    : tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
 }
 
