@@ -85,19 +85,28 @@ __device__ __forceinline__ f32x4 mfma_slab(const i32x8 &a, const i32x8 &b, const
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);  // both e4m3, times 2^0
 }
 
-// Thirty-two codes (a lane's of a slab) times 2^(exponent of s) as four bf16 operands: exact.
-__device__ __forceinline__ void widen(const i32x8 &c, float s, bf16x8 (&o)[4]) {
+// Codes 8 g .. 8 g + 7 of a lane's 32 of a slab, times 2^(exponent of s), as a bf16
+// operand: exact.
+__device__ __forceinline__ bf16x8 widen(const i32x8 &c, int g, float s) {
+  bf16x8 o;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const uint32_t w = (uint32_t)c[2 * g + (h >> 1)];
-      const bf16x2 v = (h & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true)
-                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
-      o[g][2 * h] = v.x;
-      o[g][2 * h + 1] = v.y;
-    }
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t w = (uint32_t)c[2 * g + (h >> 1)];
+    const bf16x2 v = (h & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true)
+                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
+    o[2 * h] = v.x;
+    o[2 * h + 1] = v.y;
   }
+  return o;
+}
+__device__ __forceinline__ int exponent_of(float s) { return (int)((__float_as_uint(s) >> 23) & 0xFFu); }
+
+// Scales a caller called powers of two: if one is not, the flag goes into *status.
+// The workgroup's threads share the n scales.
+__device__ __forceinline__ void check_scales(const float *s, int64_t n, uint32_t *status) {
+  uint32_t bad = 0u;
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) (void)scale_exponent(s[i], &bad);
+  if (__ballot(bad != 0u) != 0u && (threadIdx.x & 63) == 0) atomicOr(status, kFlagScaleFormat);
 }
 #define LDS_ADDR(p) ((uint32_t)(size_t)LDS_PTR(p))
 
@@ -206,14 +215,15 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   for (int i = 0; i < NA; ++i)
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  uint32_t bad = 0u;
   // weight fragments, read two steps ahead (one where registers run out)
   constexpr int WD = POW2 && NA == 8 ? 2 : 3;
+  static_assert(!EXACT || WD == 3, "the next step's fragment is widened under this step's products");
   i32x8 wf[WD];
   float wsc[WD];     // row scales with POW2: those of the fragments' rows
   f32x4 sn[4], sl;   // ... without: of the lane's four channels in the fragments; in the slab's last one
   f32x4 p[MB];       // the last step's partial sums, folded under the next step's products
   i32x8 xf[MB];      // the wave's token fragments
+  bf16x8 xb[EXACT ? MB : 1][4], wb[2];   // EXACT: the widened ones, and two chunks of a weight fragment
   float sa[MB], sb[MB], qa = 1.0f, qb = 1.0f;   // their scales and the square's, two slabs in turn
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
@@ -221,15 +231,10 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     sb[j] = 0.0f;
   }
   sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // POW2: scales of rows past the end are none of the caller's
-  const int xlive = rows - wm * MB * 16 - rl, wlive = wrows - wn * NA * 16 - rl;
   const auto read_w = [&](int buf, int32_t k, int i) {
     const int r = (wn * NA + i) * 16 + rl;
     wf[i % WD] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
-    if constexpr (POW2 && ROW) {
-      const float v = ssc[(k >> 2) & (SB - 1)][S::BM + r][k & 3];
-      wsc[i % WD] = i * 16 < wlive ? v : 1.0f;
-    }
+    if constexpr (POW2 && ROW) wsc[i % WD] = ssc[(k >> 2) & (SB - 1)][S::BM + r][k & 3];
     if constexpr (!POW2 && ROW) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -243,11 +248,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const auto read_s = [&](int32_t k, float (&f)[MB], float &q) {
     q = ROW ? 1.0f : ssc[(k >> 2) & (SB - 1)][ROW ? 0 : S::BM + wn * NA * 16 / 128][k & 3];
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      const float v = ssc[(k >> 2) & (SB - 1)][(wm * MB + j) * 16 + rl][k & 3];
-      f[j] = !POW2 || j * 16 < xlive ? v : 1.0f;
-    }
-    if (POW2 && wn * NA * 16 >= wrows) q = 1.0f;
+    for (int j = 0; j < MB; ++j) f[j] = ssc[(k >> 2) & (SB - 1)][(wm * MB + j) * 16 + rl][k & 3];
   };
   const auto fold = [&](int i, int j, float f, const f32x4 &n) {
 #pragma unroll
@@ -270,16 +271,11 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
       for (int j = 0; j < MB; ++j) f[j] *= fq;
     }
-    bf16x8 xb[EXACT ? MB : 1][4];
-    if constexpr (EXACT) {
-#pragma unroll
-      for (int j = 0; j < MB; ++j) widen(xf[j], POW2 ? f[j] : 1.0f, xb[j]);
-    }
     int ex[MB], eq = 127;
-    if constexpr (POW2) {
+    if constexpr (POW2 && !EXACT) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) ex[j] = (int)scale_exponent(f[j], &bad);
-      if constexpr (!ROW) eq = (int)scale_exponent(fq, &bad);
+      for (int j = 0; j < MB; ++j) ex[j] = exponent_of(f[j]);
+      if constexpr (!ROW) eq = exponent_of(fq);
     }
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
@@ -306,21 +302,27 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
         __builtin_amdgcn_sched_barrier(0);
       };
       if constexpr (EXACT) {
-        bf16x8 wb[4];
-        if constexpr (POW2 && ROW) (void)scale_exponent(ws, &bad);
-        widen(w, POW2 ? ws : 1.0f, wb);
+        // chunk c's products, and under them the next chunk's widening: of the weights, and
+        // in the first step of the tokens (the next slab's in the last)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int j = 0; j < MB; ++j) {
             f32x4 &t = POW2 ? acc[i][j] : p[j];
             if (!POW2 && c == 0) fold(i > 0 ? i - 1 : NA - 1, j, i > 0 ? f[j] : g[j], n);
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[j][c],
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c & 1], xb[j][c],
                                                         !POW2 && c == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : t, 0, 0, 0);
-            if (c == 1) behind(j);
+            if (c == 0) behind(j);
+            if (i == 0 && c < 3) xb[j][c + 1] = widen(xf[j], c + 1, POW2 ? f[j] : 1.0f);
+            if (last && c == 3) xb[j][0] = widen(xf[j], 0, POW2 ? g[j] : 1.0f);
+            if (j == 0) {
+              if (c < 3) wb[(c + 1) & 1] = widen(w, c + 1, POW2 ? ws : 1.0f);
+              else wb[0] = widen(wf[last ? 0 : (i + 1) % WD], 0, !POW2 ? 1.0f : ROW ? wsc[last ? 0 : (i + 1) % WD] : last ? gq : fq);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
       } else if constexpr (POW2) {
-        const int ew = ROW ? (int)scale_exponent(ws, &bad) : eq;
+        const int ew = ROW ? exponent_of(ws) : eq;
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xf[j], acc[i][j], 0, 0, 0, ew, 0, ex[j]);
@@ -346,6 +348,11 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   read_s(0, sa, qa);
   read_w(0, 0, 0);
   if constexpr (WD == 3) read_w(0, 0, 1);
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int j = 0; j < MB; ++j) xb[j][0] = widen(xf[j], 0, POW2 ? sa[j] : 1.0f);
+    wb[0] = widen(wf[0], 0, !POW2 ? 1.0f : ROW ? wsc[0] : qa);
+  }
   static_assert((S::ST & (S::ST - 1)) == 0 && S::ST >= 2, "slab kt is in buffer kt % ST");
   constexpr int kMask = S::ST - 1;
   int32_t kt = 0;
@@ -366,7 +373,12 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands after the workgroup has ended
   if constexpr (POW2) {
-    if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
+    if (a.status) {   // each scale by one workgroup
+      if (nt == 0) check_scales(a.xs + (int64_t)m0 * NB, (int64_t)rows * NB, a.status);
+      if (mt == 0 && ROW) check_scales(a.ws + (int64_t)n0 * NB, (int64_t)wrows * NB, a.status);
+      if (mt == 0 && !ROW && n0 % 128 == 0)
+        check_scales(a.ws + (int64_t)(n0 / 128) * NB, (int64_t)((wrows + 127) / 128) * NB, a.status);
+    }
   }
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
@@ -427,7 +439,6 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
     lds_load4(rXS, LDS_ADDR(&scales[wv][slot][0]), oxs, k * 4);
     lds_load4(rWS, LDS_ADDR(&scales[wv][slot][64]), ows, k * 4);
   };
-  uint32_t bad = 0u;
   f32x4 acc[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -448,22 +459,13 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
     for (int r = 0; r < 4; ++r) sn[r] = sc[64 + (ROW ? q4 * 4 + r : 0)];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (next < NB) issue(next, slot);
-    bf16x8 wb[4];
-    if constexpr (OUT == kOutFp32) widen(fw, 1.0f, wb);
-    if constexpr (POW2) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) (void)scale_exponent(s[j], &bad);
-#pragma unroll
-      for (int r = 0; r < (ROW ? 4 : 1); ++r) (void)scale_exponent(sn[r], &bad);
-    }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (OUT == kOutFp32) {
-        bf16x8 xb[4];
-        widen(fx[j], 1.0f, xb);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[c], xb[c], p, 0, 0, 0);
+        for (int c = 0; c < 4; ++c)
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw, c, 1.0f), widen(fx[j], c, 1.0f), p, 0, 0, 0);
       } else {
         p = mfma_slab(fw, fx[j], p);
       }
@@ -487,7 +489,11 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
     slot = slot + 1 == R ? 0 : slot + 1;
   }
   if constexpr (POW2) {
-    if (a.status && __ballot(bad != 0u) != 0u && lane == 0) atomicOr(a.status, kFlagScaleFormat);
+    if (a.status) {
+      if (blockIdx.x == 0) check_scales(a.xs + (int64_t)m0 * NB, (int64_t)rows * NB, a.status);
+      if (ROW || n0 % 128 == 0)
+        check_scales(a.ws + (int64_t)(ROW ? n0 : n0 / 128) * NB, (int64_t)(ROW ? wrows : 1) * NB, a.status);
+    }
   }
   f32x4 *const red = reinterpret_cast<f32x4 *>(&slabs[0][0][0]);
   static_assert(W * MT * 64 * 16 <= (int)sizeof(slabs), "the waves' sums fit");
