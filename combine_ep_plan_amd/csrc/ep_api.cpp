@@ -1281,9 +1281,11 @@ ep_status_t ep_add_layernorm(const ep_layernorm_rule_t *rule, const ep_layernorm
 }
 
 ep_status_t ep_add_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t *bytes) {
-  const ep_status_t st = ep_add_rmsnorm_bwd_workspace_bytes(rows, H, bytes);
-  if (st == EP_OK) *bytes *= 2;   // a partial row of grad_weight and one of grad_bias
-  return st;
+  if (!bytes || rows < 0 || rows > INT32_MAX || H < 8 || H % 8 != 0 || H > epk::kRowMaxChannels)
+    return EP_ERR_INVALID_ARG;
+  // partial rows of grad_weight and of grad_bias
+  *bytes = sizeof(float) * 2 * (size_t)epk::layernorm_bwd_groups((int32_t)rows, H) * (size_t)H;
+  return EP_OK;
 }
 
 ep_status_t ep_add_layernorm_bwd(const ep_layernorm_rule_t *rule, const ep_layernorm_bwd_t *t,
@@ -1333,7 +1335,7 @@ ep_status_t ep_add_layernorm_bwd(const ep_layernorm_rule_t *rule, const ep_layer
     if (g->ndim != 1 || g->sizes[0] != H) return EP_ERR_BAD_SHAPE;
   }
   if (t->grad_weight || t->grad_bias) {
-    const int64_t need = (int64_t)epk::norm_bwd_groups((int32_t)T, (int32_t)H) * 2 * H;
+    const int64_t need = (int64_t)epk::layernorm_bwd_groups((int32_t)T, (int32_t)H) * 2 * H;
     if (need > 0) {
       st = check_tensor(t->workspace, EP_TAG_WORKSPACE, EP_DTYPE_FP32);
       if (st != EP_OK) return st;

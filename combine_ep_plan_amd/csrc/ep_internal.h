@@ -189,6 +189,7 @@ struct LayerNormBwd {
   double eps;
   Dropout drop;
 };
+int32_t layernorm_bwd_groups(int32_t T, int32_t H);  // partial rows, of 2 H, in the workspace at most
 hipError_t launch_layernorm_bwd(const LayerNormBwd &n, hipStream_t s);
 struct DropoutAdd {
   const void *x, *residual;

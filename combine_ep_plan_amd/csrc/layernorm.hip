@@ -214,8 +214,34 @@ hipError_t launch_add_layernorm(const LayerNorm &n, hipStream_t s) {
 // One reduction over a row gives its four sums, d = h - c as in the forward:
 // sum d, sum d^2, sum g and sum g * d; sum g * n follows from the last two.  g is
 // exact in fp64: means of terms that cancel keep no rounding of theirs.
-// Workgroups, partial rows and their join are the RMS norm's (norm.hip), with
-// the partial rows of grad_w and grad_b side by side.
+// A workgroup takes every G-th row (or group of rows), the next row's loads in
+// flight while one is reduced, and keeps its share of grad_w and grad_b in
+// registers; the G partial rows, both side by side, go to the workspace and
+// norm.hip's second kernel adds them in order, in fp64.  They are twice as long as
+// the RMS norm's, so there are no more workgroups of over 512 threads than compute
+// units (one fits: 4096 x 7168 with dropout 74 us against 79 with up to 512), and
+// fp32 rows of 2049 to 4096 channels go two to a workgroup of up to 1024 threads
+// (16384 x 4096 200 us against 210; bf16 rows 152 against 147, one to a workgroup).
+
+static BwdShape ln_bwd_shape(int32_t V, bool fp32) {
+  BwdShape b = bwd_shape(V);
+  if (fp32 && b.threads > 256 && b.threads <= 512) b.rows = 2;
+  return b;
+}
+
+static int32_t ln_bwd_groups(int32_t T, int32_t V, bool fp32) {
+  if (T == 0) return 0;
+  const BwdShape b = ln_bwd_shape(V, fp32);
+  const int64_t units = ((int64_t)T + b.rows - 1) / b.rows, most = b.threads * b.rows > 512 ? 256 : 512;
+  int64_t passes = (units + most - 1) / most;
+  if (passes < 2 && units > 256) passes = 2;
+  return (int32_t)((units + passes - 1) / passes);
+}
+
+int32_t layernorm_bwd_groups(int32_t T, int32_t H) {
+  const int32_t a = ln_bwd_groups(T, H / 8, false), b = ln_bwd_groups(T, H / 8, true);
+  return a > b ? a : b;
+}
 
 struct LnBwdArgs {
   const void *hidden;
@@ -233,7 +259,7 @@ struct LnBwdArgs {
 template <typename RT, int VPT>
 __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
   __shared__ double s_sum[2][4][16];
-  extern __shared__ double s_dw[];  // [rows - 1][2 H]
+  extern __shared__ float s_dw[];  // [rows - 1][2 H]
   const int tpr = blockDim.x / a.rows, slot = threadIdx.x / tpr, sub = threadIdx.x - slot * tpr;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = tpr >> 6, w0 = slot * nw;
   const bool drop = a.gx != nullptr;
@@ -319,6 +345,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
     }
     const double m1 = s[0] * a.inv_h, mean = shift + m1;
     const float rstd = rstd_of(not_below_zero(__builtin_fma(-m1, s[0], s[1])), a.inv_h, a.eps);
+    // n = (h - mean) * rstd with the mean in two floats: no step of n is wider than fp32
+    const float mh = (float)mean, ml = (float)(mean - (double)mh) * rstd;
     const float mg = (float)(s[2] * a.inv_h);
     const float mn = (float)(__builtin_fma(-m1, s[2], s[3]) * (double)rstd * a.inv_h);  // mean of g * n
 #pragma unroll
@@ -328,7 +356,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
       float o[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float n = (float)((double)h[i][c] - mean) * rstd;
+        const float n = __builtin_fmaf(h[i][c] - mh, rstd, -ml);
         o[c] = rstd * ((g[i][c] * w[i][c] - mg) - n * mn) + r[i][c];
         dw[i][c] += g[i][c] * n;
         db[i][c] += g[i][c];
@@ -347,11 +375,11 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
     if (a.rows > 1) {
       const int32_t H = a.V * 8;
       if (slot > 0 && sub < a.V) {
-        double *o = s_dw + (slot - 1) * 2 * H;
+        float *o = s_dw + (slot - 1) * 2 * H;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          o[c * a.V + sub] = (double)dw[0][c];
-          o[H + c * a.V + sub] = (double)db[0][c];
+          o[c * a.V + sub] = dw[0][c];
+          o[H + c * a.V + sub] = db[0][c];
         }
       }
       __syncthreads();
@@ -361,8 +389,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
         for (int c = 0; c < 8; ++c) {
           double sw = (double)dw[0][c], sb = (double)db[0][c];
           for (int i = 0; i < a.rows - 1; ++i) {
-            sw += s_dw[i * 2 * H + c * a.V + sub];
-            sb += s_dw[i * 2 * H + H + c * a.V + sub];
+            sw += (double)s_dw[i * 2 * H + c * a.V + sub];
+            sb += (double)s_dw[i * 2 * H + H + c * a.V + sub];
           }
           dw[0][c] = (float)sw;
           db[0][c] = (float)sb;
@@ -380,14 +408,14 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
 }
 
 hipError_t launch_layernorm_bwd(const LayerNormBwd &n, hipStream_t s) {
-  const int32_t G = norm_bwd_groups(n.T, n.H);
+  const int32_t G = ln_bwd_groups(n.T, n.H / 8, n.h_fp32);
   if (n.T > 0) {
-    const BwdShape sh = bwd_shape(n.H / 8);
+    const BwdShape sh = ln_bwd_shape(n.H / 8, n.h_fp32);
     const bool sums = n.gw || n.gb;
     const LnBwdArgs a{n.hidden, n.w, reinterpret_cast<const u32x4 *>(n.gy), n.ghidden, n.gh,
                       reinterpret_cast<u32x4 *>(n.gx), sums ? n.part : nullptr, n.T, n.H / 8,
                       n.w_fp32 ? 1 : 0, sh.rows, n.eps, 1.0 / n.H, n.drop};
-    const size_t lds = sizeof(double) * 2 * (size_t)(sh.rows - 1) * n.H;   // 56 KB at most
+    const size_t lds = sizeof(float) * 2 * (size_t)(sh.rows - 1) * n.H;   // 32 KB at most
 #define L2(RT, P)                                                                               \
   hipLaunchKernelGGL((k_layernorm_bwd<RT, P>), dim3((unsigned)G), dim3(sh.threads * sh.rows), lds, \
                      s, a)
