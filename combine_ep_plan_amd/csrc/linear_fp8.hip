@@ -17,6 +17,8 @@
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes the whole slab of a 16 x 16 block at
 // once, so a partial sum is four registers and two sets of them are enough to
 // fold one block while the next is multiplied.
+#include <type_traits>
+
 #include "ep_internal.h"
 #include "gemm_common.h"
 
@@ -74,6 +76,61 @@ __device__ __forceinline__ void store4(const LinArgs &a, int32_t m, int32_t n, f
         const float b = a.addend ? bf16_lo(static_cast<const uint16_t *>(a.addend)[at + r]) : 0.0f;
         static_cast<uint16_t *>(a.out)[at + r] = (uint16_t)pack_bf16x2(v[r] + b, 0.0f);
       }
+    }
+  }
+}
+
+// Whether a result's rows are whole 16-byte vectors.
+template <int OUT>
+__device__ __forceinline__ bool vector_rows(int32_t N) {
+  return (N & (OUT == kOutGlu ? 15 : OUT == kOutFp32 ? 3 : 7)) == 0;
+}
+
+// Tokens m + (0 .. 15), `live` of them there, x a wave's NA * 16 channels from n, through
+// 16 rows of its own in LDS, so that they leave in rows of up to 256 bytes: straight
+// from the accumulators a store writes 32 bytes a row, and the tiles of a prefill
+// product all end at once.
+template <int OUT, int NA>
+struct OutBlock {
+  static constexpr int channels = NA * (OUT == kOutGlu ? 8 : 16);   // of the result
+  static constexpr int stride = channels + 4;                       // floats; rows start four banks apart
+  static constexpr int bytes = 16 * stride * 4;
+};
+template <int OUT, int NA, int MB>
+__device__ __forceinline__ void store_block(const LinArgs &a, float *buf, int lane, const f32x4 (&acc)[NA][MB], int j,
+                                            int32_t m, int32_t live, int32_t n) {
+  using B = OutBlock<OUT, NA>;
+  float *const row = buf + (lane & 15) * B::stride;
+  const int q = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const f32x4 v = acc[i][j];
+    if constexpr (OUT == kOutGlu)
+      *reinterpret_cast<f32x2 *>(row + i * 8 + q * 2) = f32x2{silu_times(v.x, v.y), silu_times(v.z, v.w)};
+    else
+      *reinterpret_cast<f32x4 *>(row + i * 16 + q * 4) = v;
+  }
+  constexpr int P = OUT == kOutFp32 ? 4 : 8, each = B::channels / P;   // values a piece, pieces a row
+  const int32_t N = OUT == kOutGlu ? a.N / 2 : a.N, n0 = OUT == kOutGlu ? n / 2 : n;
+#pragma unroll
+  for (int t = 0; t < (16 * each + 63) / 64; ++t) {
+    const int k = t * 64 + lane, r = k / each, c = (k % each) * P;
+    if (r >= 16 || r >= live || n0 + c >= N) continue;
+    const f32x4 *const f = reinterpret_cast<const f32x4 *>(buf + r * B::stride + c);
+    const int64_t at = ((int64_t)(m + r) * N + n0 + c) / P;
+    if constexpr (OUT == kOutFp32) {
+      f32x4 v = f[0];
+      if (a.addend) v += static_cast<const f32x4 *>(a.addend)[at];
+      static_cast<f32x4 *>(a.out)[at] = v;
+    } else {
+      float v[8] = {f[0].x, f[0].y, f[0].z, f[0].w, f[1].x, f[1].y, f[1].z, f[1].w};
+      if (OUT == kOutBf16 && a.addend) {
+        float r8[8];
+        unpack8(static_cast<const u32x4 *>(a.addend)[at], r8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += r8[e];
+      }
+      static_cast<u32x4 *>(a.out)[at] = pack8(v);
     }
   }
 }
@@ -145,7 +202,9 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   constexpr int NA = S::NA, MB = S::MB;
   // rows whose scales a tile reads: its tokens', then its channels' or its squares'
   constexpr int NS = S::BM + (ROW ? S::BN : 64);
-  __shared__ u32x4 sw[S::ST][S::BN * kChunks], sx[S::ST][S::BM * kChunks];
+  constexpr int kSlabW = S::BN * kChunks, kSlabX = S::BM * kChunks;
+  __shared__ u32x4 slabs[S::ST * (kSlabW + kSlabX)];   // of weights, then of tokens; in the end the results
+  u32x4 *const sw = slabs, *const sx = slabs + S::ST * kSlabW;
   // Four slabs' scales a buffer.  Those of the four after are under way beside them; slab
   // kt + ST goes out when slab kt + 1 is next to be read, whose four lie one buffer back
   // with ST 2, up to two with ST 4.
@@ -198,9 +257,9 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
     const int32_t kt = k < NB ? k : NB - 1;   // past the end: the last slab again, which nobody reads
 #pragma unroll
     for (int i = lo; i < hi; ++i) {
-      if (i < LX) lds_load16(rX, LDS_ADDR(&sx[buf][i * S::threads + wv * 64]), off + (uint32_t)(i * kStep * a.K), kt * 128);
+      if (i < LX) lds_load16(rX, LDS_ADDR(&sx[buf * kSlabX + i * S::threads + wv * 64]), off + (uint32_t)(i * kStep * a.K), kt * 128);
       else if (i < LX + LW)
-        lds_load16(rW, LDS_ADDR(&sw[buf][(i - LX) * S::threads + wv * 64]), off + (uint32_t)((i - LX) * kStep * a.K), kt * 128);
+        lds_load16(rW, LDS_ADDR(&sw[buf * kSlabW + (i - LX) * S::threads + wv * 64]), off + (uint32_t)((i - LX) * kStep * a.K), kt * 128);
       else issue_scales((k + 3) >> 2, (k + 3) & 3);
     }
   };
@@ -216,7 +275,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   // weight fragments, read two steps ahead (one where registers run out)
-  constexpr int WD = POW2 && NA == 8 ? 2 : 3;
+  constexpr int WD = NA == 8 && (POW2 || ROW) ? 2 : 3;
   static_assert(!EXACT || WD == 3, "the next step's fragment is widened under this step's products");
   i32x8 wf[WD];
   float wsc[WD];     // row scales with POW2: those of the fragments' rows
@@ -233,7 +292,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   sl = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto read_w = [&](int buf, int32_t k, int i) {
     const int r = (wn * NA + i) * 16 + rl;
-    wf[i % WD] = join_codes(sw[buf][swz(r, cl)], sw[buf][swz(r, cl + 4)]);
+    wf[i % WD] = join_codes(sw[buf * kSlabW + swz(r, cl)], sw[buf * kSlabW + swz(r, cl + 4)]);
     if constexpr (POW2 && ROW) wsc[i % WD] = ssc[(k >> 2) & (SB - 1)][S::BM + r][k & 3];
     if constexpr (!POW2 && ROW) {
 #pragma unroll
@@ -243,7 +302,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   };
   const auto read_x = [&](int buf, int j) {
     const int r = (wm * MB + j) * 16 + rl;
-    xf[j] = join_codes(sx[buf][swz(r, cl)], sx[buf][swz(r, cl + 4)]);
+    xf[j] = join_codes(sx[buf * kSlabX + swz(r, cl)], sx[buf * kSlabX + swz(r, cl + 4)]);
   };
   const auto read_s = [&](int32_t k, float (&f)[MB], float &q) {
     q = ROW ? 1.0f : ssc[(k >> 2) & (SB - 1)][ROW ? 0 : S::BM + wn * NA * 16 / 128][k & 3];
@@ -379,6 +438,17 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
       if (mt == 0 && !ROW && n0 % 128 == 0)
         check_scales(a.ws + (int64_t)(n0 / 128) * NB, (int64_t)((wrows + 127) / 128) * NB, a.status);
     }
+  }
+  if (vector_rows<OUT>(a.N)) {
+    static_assert(S::WN * S::WM * OutBlock<OUT, NA>::bytes <= (int)sizeof(slabs), "the waves' rows fit");
+    __syncthreads();   // every wave is done with the slabs
+    float *const buf = reinterpret_cast<float *>(slabs) + wv * (OutBlock<OUT, NA>::bytes / 4);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int32_t m = (wm * MB + j) * 16;
+      store_block<OUT>(a, buf, lane, acc, j, m0 + m, rows - m, n0 + wn * NA * 16);
+    }
+    return;
   }
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
@@ -517,13 +587,19 @@ typedef LinShape<2, 4, 4, 3, 2> Shape128x192;  // 128 channels x 192 tokens, 8 w
 typedef LinShape<2, 2, 4, 4, 2> Shape128;      // 128 x 128, 4 waves of 64 x 64
 typedef LinShape<2, 2, 2, 2, 4> Shape64;       // 64 x 64, 4 waves of 32 x 32
 
-// What a slab costs a compute unit that has its share of the tiles: `one` us for a
-// tile alone, `two` for two side by side (0: they do not fit).
+// Time of a compute unit's share of the tiles, in us: a tile alone on it takes `one`
+// a slab and `more` besides (prologue, results), two side by side `two` and `more2`
+// (0: two do not fit).  Measured with 256, 512, 768 and 1024 tiles at K 2048 and
+// 6144, shared by all forms of the scales.
+struct TileTimes {
+  double one, more, two, more2;
+};
 template <class S>
-static double tiles_cost(const Linear &n, double one, double two) {
+static double tiles_time(const Linear &n, const TileTimes &t) {
   const int64_t tiles = (int64_t)((n.M + S::BM - 1) / S::BM) * ((n.N + S::BN - 1) / S::BN);
-  const int64_t each = (tiles + 255) / 256;
-  return two > 0.0 ? (double)(each / 2) * two + (double)(each % 2) * one : (double)each * one;
+  const int64_t each = (tiles + 255) / 256, pairs = t.two > 0.0 ? each / 2 : 0;
+  const double slabs = n.K / 128;
+  return (double)pairs * (t.two * slabs + t.more2) + (double)(each - 2 * pairs) * (t.one * slabs + t.more);
 }
 static int64_t tiles_of(const Linear &n, int32_t b) {
   return (int64_t)((n.M + b - 1) / b) * ((n.N + b - 1) / b);
@@ -550,19 +626,17 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
 #undef L
     return;
   }
-  if constexpr (OUT == kOutFp32) {
-    const double c192 = tiles_cost<Shape128x192>(n, 1.3, 0.0), c128 = tiles_cost<Shape128>(n, 1.0, 1.7),
-                 c64 = tiles_cost<Shape64>(n, 0.36, 0.6);
-    if (c192 <= c128 && c192 <= c64) launch_tiles<Shape128x192, ROW, POW2, OUT>(a, 5, s);
-    else if (c128 <= c64) launch_tiles<Shape128, ROW, POW2, OUT>(a, 8, s);
-    else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
-  } else {
-    const double c256 = tiles_cost<Shape256>(n, 1.9, 0.0), c128 = tiles_cost<Shape128>(n, 0.77, 1.22),
-                 c64 = tiles_cost<Shape64>(n, 0.30, 0.54);
-    if (c256 <= c128 && c256 <= c64) launch_tiles<Shape256, ROW, POW2, OUT>(a, 4, s);
-    else if (c128 <= c64) launch_tiles<Shape128, ROW, POW2, OUT>(a, 8, s);
-    else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
-  }
+  // the fastest tile by those times: of 333 x 4096 x 4096 64 x 64 (15.6 us; 128 x 128 18.6, 256 x 256
+  // 42), of 512 x 7168 x 2048 128 x 128 (13.4; 18.5, 25.7), of 4096 x 4096 x 7168 256 x 256 (fp32
+  // results: 128 x 192 where 1536 x 4096 x 16384 takes 173, 128 x 128 215)
+  const bool fp32 = OUT == kOutFp32;
+  using Large = std::conditional_t<OUT == kOutFp32, Shape128x192, Shape256>;
+  const double large = tiles_time<Large>(n, fp32 ? TileTimes{1.3, 8.5, 0.0, 0.0} : TileTimes{1.6, 9.0, 0.0, 0.0}),
+               mid = tiles_time<Shape128>(n, fp32 ? TileTimes{0.93, 7.0, 1.7, 6.0} : TileTimes{0.8, 1.5, 1.0, 6.0}),
+               small = tiles_time<Shape64>(n, fp32 ? TileTimes{0.43, 4.0, 0.67, 4.0} : TileTimes{0.27, 3.0, 0.48, 3.0});
+  if (large <= mid && large <= small) launch_tiles<Large, ROW, POW2, OUT>(a, fp32 ? 5 : 4, s);
+  else if (mid <= small) launch_tiles<Shape128, ROW, POW2, OUT>(a, 8, s);
+  else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
 }
 
 // A launch counts its threads in 32 bits, and a tile index is an int32.

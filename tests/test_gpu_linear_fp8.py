@@ -116,7 +116,9 @@ def test_small(M, N, K, square, dtype, add):
 
 # 128 x 128 tiles (256 of them, 64 of 256 x 256), then 256 x 256 (192 and more), ragged ones among them
 TILES = [(2048, 2048, 128), (2040, 2017, 384), (1900, 2100, 256), (4096, 2960, 128), (4095, 2951, 384), (3900, 3100, 256),
-         (300, 25000, 512)]
+         (300, 25000, 512), (4096, 4096, 128), (4096, 4096, 384), (4095, 4087, 640),
+         # fp32: tiles of 128 channels x 192 tokens
+         (1536, 4096, 1152), (1531, 4091, 1280)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -131,7 +133,7 @@ def test_tiles(M, N, K, square, dtype):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (33, 272, 640), (90, 160, 384), (2047, 2064, 256),
-                                   (4090, 2976, 256)])
+                                   (4090, 2976, 256), (4090, 4064, 384)])
 @pytest.mark.parametrize("square", [True, False])
 def test_swiglu(M, N, K, square):
     rng = np.random.default_rng(M)
