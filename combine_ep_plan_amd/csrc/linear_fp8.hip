@@ -171,9 +171,15 @@ __device__ __forceinline__ void check_scales(const float *s, int64_t n, uint32_t
 // tiles
 //
 // WN x WM waves, each NA x MB blocks of 16 channels x 16 tokens.  Slabs go from
-// global memory straight into LDS, two buffers; the next slab's loads are issued
-// behind the barrier that publishes this one, so they have this slab's products
-// to land in.
+// global memory straight into LDS, ST buffers of them: slab k + ST is sent for once
+// slab k has been read, so it has ST - 1 slabs' products to land in.  Two slabs of the
+// large tiles fill LDS; the smallest, which wait for memory, hold four.
+//
+// fp32 results (a main gradient) want every product whole: the FP8 instruction cuts
+// the products of 8 neighbouring k at 2^-13 of the largest one's binade, which a bf16
+// result does not show and an fp32 one does.  Their operands are widened to bf16,
+// which is exact, at half the instruction's rate.  Power-of-two scales go into the
+// instruction's (or the widening's) exponents and leave nothing to fold.
 
 template <int WN_, int WM_, int NA_, int MB_, int ST_>
 struct LinShape {
@@ -247,8 +253,10 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
   const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(of_x ? a.xs + (int64_t)m0 * NB : a.ws + (int64_t)first * NB), (short)0,
       (left < 512 ? left : 512) * NB * 4, kBufDword3);
-  const auto issue_scales = [&](int32_t four, int piece) {   // rows past the end, slabs past the last: unused
-    lds_load4(rS, LDS_ADDR(&ssc[four & (SB - 1)][part * 64 + piece * 16][0]), osc + (uint32_t)(piece * 16 * NB * 4), four * 16);
+  // rows past the end, slabs past the last: unused.  The whole offset is the lane's: what lies past the
+  // last row's last slab is out of the resource's range
+  const auto issue_scales = [&](int32_t four, int piece) {
+    lds_load4(rS, LDS_ADDR(&ssc[four & (SB - 1)][part * 64 + piece * 16][0]), osc + (uint32_t)(piece * 64 * NB + four * 16), 0);
   };
   static_assert(128 % (NA * 16) == 0 && NA % 2 == 0, "a wave's channels lie in one square");
   constexpr int kLoads = LW + LX + 1;   // of a wave, a slab
@@ -639,7 +647,8 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
   else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
 }
 
-// A launch counts its threads in 32 bits, and a tile index is an int32.
+// A launch counts its threads in 32 bits, and a tile index is an int32.  (Up to 64 tokens may go either
+// way: the limit of the launch of 16 channels a workgroup is the lower one.)
 bool linear_fp8_fits(const Linear &n) {
   const int64_t few = ((int64_t)n.N + 15) / 16;
   return n.M <= 64 ? few * 512 < (int64_t)1 << 32

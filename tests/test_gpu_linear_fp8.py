@@ -114,7 +114,7 @@ def test_small(M, N, K, square, dtype, add):
     _check(_problem(M, N, K, square, False), square, dtype, a)
 
 
-# 128 x 128 tiles (256 of them, 64 of 256 x 256), then 256 x 256 (192 and more), ragged ones among them
+# 128 x 128 tiles, 256 x 256, ragged ones among them
 TILES = [(2048, 2048, 128), (2040, 2017, 384), (1900, 2100, 256), (4096, 2960, 128), (4095, 2951, 384), (3900, 3100, 256),
          (300, 25000, 512), (4096, 4096, 128), (4096, 4096, 384), (4095, 4087, 640),
          # fp32: tiles of 128 channels x 192 tokens
