@@ -167,7 +167,7 @@ def test_in_place_stream(T, H, dtype):
 
 
 BWD = [(1, 8), (3, 128), (7, 512), (300, 520), (600, 1000), (130, 1024), (1500, 64), (33, 4096), (520, 2048),
-       (2, 8192), (5, 8200), (3, 16384), (2, 32768), (2100, 256)]
+       (2, 8192), (5, 8200), (3, 16384), (2, 32768), (2100, 256), (600, 8200), (270, 16392)]
 
 
 @pytest.mark.parametrize("T,H", BWD)
