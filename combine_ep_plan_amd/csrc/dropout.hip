@@ -21,9 +21,8 @@ __device__ __forceinline__ float drop_add(float x, bool stay, float scale, float
 constexpr int kDropThreads = 256;
 
 template <typename XT, typename OT, bool RES>
-__global__ __launch_bounds__(kDropThreads) void k_dropout(const void *__restrict__ x,
-                                                          const void *residual, void *out,
-                                                          int64_t nvec, Dropout d) {
+__global__ __launch_bounds__(kDropThreads) void k_dropout(const void *x, const void *residual,
+                                                          void *out, int64_t nvec, Dropout d) {
   const PhiloxKey key = philox_key(d.rng);
   const int64_t step = (int64_t)gridDim.x * kDropThreads;
   for (int64_t v = (int64_t)blockIdx.x * kDropThreads + threadIdx.x; v < nvec; v += step) {

@@ -1419,8 +1419,9 @@ ep_status_t ep_linear_fp8(const ep_linear_rule_t *rule, const ep_tensor_t *x,
   if (st != EP_OK) return st;
   if (x->ndim < 2 || w->ndim != 2) return EP_ERR_BAD_SHAPE;
   const int64_t K = x->sizes[x->ndim - 1], N = w->sizes[0];
-  if (K <= 0 || K % 128 != 0 || w->sizes[1] != K) return EP_ERR_BAD_SHAPE;
-  const int64_t M = numel(x) / K;
+  if (K % 128 != 0 || w->sizes[1] != K) return EP_ERR_BAD_SHAPE;
+  int64_t M = 1;   // (K may be 0: the weight gradient of no tokens)
+  for (int i = 0; i + 1 < x->ndim; ++i) M *= x->sizes[i];
   if (K > epk::kLinearMaxK || M > INT32_MAX - 255 || N > INT32_MAX - 255) return EP_ERR_UNSUPPORTED;
   if (glu && N % 16 != 0) return EP_ERR_BAD_SHAPE;
   if (!is_rows(x_scales, M, K / 128)) return EP_ERR_BAD_SHAPE;

@@ -624,7 +624,8 @@ template <bool ROW, bool POW2, int OUT>
 static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
   // 33 to 64 tokens: while a compute unit has at most one workgroup of 16 channels (64 x 2048 x 7168
   // 13.3 us against 16.6 with 64 x 64 tiles, 64 x 7168 x 2048 9.2 against 7.4)
-  if (n.M <= 32 || (n.M <= 64 && n.N <= 4096)) {
+  // (and K 0, which leaves the addend, or zeros)
+  if (n.M <= 32 || (n.M <= 64 && n.N <= 4096) || n.K == 0) {
     const int mt = n.M <= 16 ? 1 : n.M <= 32 ? 2 : 4;
     const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
 #define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * FewShape<MT>::waves), 0, s, a)
@@ -651,8 +652,8 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
 // way: the limit of the launch of 16 channels a workgroup is the lower one.)
 bool linear_fp8_fits(const Linear &n) {
   const int64_t few = ((int64_t)n.N + 15) / 16;
-  return n.M <= 64 ? few * 512 < (int64_t)1 << 32
-                   : tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
+  return n.M <= 64 || n.K == 0 ? few * 512 < (int64_t)1 << 32 && (n.M + 63) / 64 <= 65535
+                               : tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
 }
 
 hipError_t launch_linear_fp8(const Linear &n, hipStream_t s) {

@@ -923,10 +923,15 @@ typedef struct ep_linear_rule {
 /* Product of FP8 rows and FP8 weights with a scale per block of 128:
  *   out[m, n] = round( sum_b xs[m, b] * ws[., b] * sum_{c in block b} x[m, c] * w[n, c]
  *                      + addend[m, n] )
- * (exact e4m3 products, fp32 accumulation; the addend joins in fp32).  With
- * swiglu the rows of w interleave gate (even) and up (odd) projections and out
- * [M, N/2] is silu(gate) * up of the fp32 sums, rounded once.
- * x:        e4m3 [M, K] (any leading shape), tag TOKENS; K % 128 == 0, K <= 2^22.
+ * (fp32 accumulation; the addend joins in fp32).  With swiglu the rows of w
+ * interleave gate (even) and up (odd) projections and out [M, N/2] is silu(gate) *
+ * up of the fp32 sums, rounded once.  For fp32 results every product is exact; for
+ * bf16 ones the matrix cores cut the products of 8 neighbouring k below 2^-13 of the
+ * largest's power of two, as in ep_expert_gemm_fp8.  xs * ws is formed in fp32 with
+ * EP_FP8_SCALES_AMAX and has to lie in its range; with _POW2 and fp32 results each
+ * operand, code times scale, has to lie in bf16's normal range to be exact.
+ * x:        e4m3 [M, K] (any leading shape), tag TOKENS; K % 128 == 0, K <= 2^22
+ *           (K 0, a weight gradient of no tokens: the addend, or zeros).
  * x_scales: fp32 [M, K/128], tag FP8_SCALES.
  * w:        e4m3 [N, K], tag EXPERT_WEIGHTS.
  * w_scales: fp32, tag FP8_SCALES: [ceil(N/128), K/128], one per 128 x 128 square,

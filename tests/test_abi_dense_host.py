@@ -155,7 +155,7 @@ def test_linear_refusals(lib):  # noqa: F811
     out = view(FP32, T_, 5, 130)
     good = [x, view(FP32, F8S, 5, 2), w, view(FP32, F8S, 2, 2), out, out, view(I32, ST, 1)]
     for at, v, want in [(0, None, INVALID), (0, view(BF16, T_, 5, 256), DTYPE), (0, view(FP8, T_, 5, 200), SHAPE),
-                        (0, view(FP8, T_, 5, 384), SHAPE), (0, view(FP8, T_, 256), SHAPE), (1, None, INVALID),
+                        (0, view(FP8, T_, 5, 384), SHAPE), (0, view(FP8, T_, 5, 0), SHAPE), (0, view(FP8, T_, 256), SHAPE), (1, None, INVALID),
                         (1, view(FP32, F8S, 5, 3), SHAPE), (1, view(FP32, RS, 5, 2), TAG), (2, None, INVALID),
                         (2, view(FP8, T_, 130, 256), TAG), (2, view(FP8, EW, 1, 130, 256), SHAPE),
                         (2, view(BF16, EW, 130, 256), DTYPE), (3, view(FP32, F8S, 3, 2), SHAPE),

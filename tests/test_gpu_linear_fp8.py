@@ -255,3 +255,42 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert all(torch.equal(v, w) for v in o)
+
+
+@pytest.mark.parametrize("M,N", [(5, 130), (300, 64), (70, 4100)])
+def test_no_channels_leave_the_addend(M, N):
+    """K 0, the weight gradient of no tokens: through the transposed quantiser's empty operands."""
+    f8 = lambda *s: torch.empty(*s, dtype=torch.float8_e4m3fn, device="cuda")  # noqa: E731
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    _, _, c, s = ep.Buffer.quantize_fp8_2d(x, "rows", rows=False)
+    assert c.shape == (128, 0) and s.shape == (128, 0)
+    for dt in (torch.float32, torch.bfloat16):
+        add = _addend(M, N, dt)
+        a = (f8(M, 0), torch.empty(M, 0, device="cuda"), f8(N, 0))
+        for ws in (torch.empty(N, 0, device="cuda"), torch.empty((N + 127) // 128, 0, device="cuda")):
+            assert torch.equal(ep.Buffer.linear_fp8(*a, ws, addend=add), add)
+            assert torch.all(ep.Buffer.linear_fp8(*a, ws, out_dtype=dt) == 0)
+
+
+@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("square", [True, False])
+@pytest.mark.parametrize("pow2", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_codes_reach_their_row_and_channel_only(M, square, pow2, dtype):
+    p = _problem(M, 200, 256, square, True)
+    p[0][1, 130], p[2][77, 5] = 0x7F, 0xFF   # both NaN
+    y = ep.Buffer.linear_fp8(*_dev(p), pow2=pow2, out_dtype=dtype)
+    want = torch.zeros(M, 200, dtype=torch.bool, device="cuda")
+    want[1] = want[:, 77] = True
+    assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.parametrize("M", [3, 80])
+@pytest.mark.parametrize("square", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_scales_of_powers_of_two(M, square, dtype):
+    """What the quantiser gives a block that is not finite: codes 0 and a NaN scale."""
+    p = _problem(M, 200, 256, square, True)
+    p[0][2, 128:], p[1][2, 1] = 0, np.nan
+    y = ep.Buffer.linear_fp8(*_dev(p), pow2=True, out_dtype=dtype)
+    assert torch.isnan(y[2]).all() and torch.isfinite(torch.cat([y[:2], y[3:]])).all()
