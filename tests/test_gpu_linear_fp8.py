@@ -132,7 +132,7 @@ def test_tiles(M, N, K, square, dtype):
         _check(_problem(M, N, K, square, False), square, dtype)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (33, 272, 640), (90, 160, 384), (2047, 2064, 256),
+@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (17, 32, 384), (32, 4112, 128), (33, 272, 640), (90, 160, 384), (2047, 2064, 256),
                                    (4090, 2976, 256), (4090, 4064, 384)])
 @pytest.mark.parametrize("square", [True, False])
 def test_swiglu(M, N, K, square):
