@@ -99,7 +99,7 @@ def test_add_layernorm(T, H, residual, quant, p):
         assert np.all(np.abs(host(codes.float()) * se - y64) <= 2.0 ** -4 * np.abs(y64) + se * 2.0 ** -10 + 2 * slack)
 
 
-@pytest.mark.parametrize("T,H", [(4103, 8), (4096, 512), (4103, 1000), (4097, 2048)])
+@pytest.mark.parametrize("T,H", [(4103, 8), (4096, 512), (4103, 1000), (4097, 2048), (600, 4104)])
 @pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("quant,p", [("none", 0.0), ("int8", 0.3), ("fp8", 0.3), ("fp8_pow2", 0.0)])
 def test_many_rows_a_wave_each(T, H, residual, quant, p):
