@@ -180,6 +180,13 @@ __device__ __forceinline__ void check_scales(const float *s, int64_t n, uint32_t
 // result does not show and an fp32 one does.  Their operands are widened to bf16,
 // which is exact, at half the instruction's rate.  Power-of-two scales go into the
 // instruction's (or the widening's) exponents and leave nothing to fold.
+//
+// 4096 x 4096 x 7168: 109 us with amax scales (2.2 PFLOP/s), 97 with powers of two,
+// 192 and 174 with fp32 results; 8192^3 450 and 421 (2.45 and 2.6).  Of the large
+// tiles' time the matrix cores are busy half: loads into LDS, reads out of it and the
+// fold of the sums interleave with the products and are none of them the bound alone
+// (without the loads 94 us, without the reads 98).  Small tiles wait for their
+// operands, which reach a compute unit at 65 to 70 GB/s.
 
 template <int WN_, int WM_, int NA_, int MB_, int ST_>
 struct LinShape {
@@ -635,8 +642,8 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
 #undef L
     return;
   }
-  // the fastest tile by those times: of 333 x 4096 x 4096 64 x 64 (15.6 us; 128 x 128 18.6, 256 x 256
-  // 42), of 512 x 7168 x 2048 128 x 128 (13.4; 18.5, 25.7), of 4096 x 4096 x 7168 256 x 256 (fp32
+  // the fastest tile by those times: of 333 x 4096 x 4096 64 x 64 (15.6 us; 128 x 128 24, 256 x 256
+  // 42), of 512 x 7168 x 2048 128 x 128 (15; 64 x 64 18, 256 x 256 26), of 4096 x 4096 x 7168 256 x 256 (fp32
   // results: 128 x 192 where 1536 x 4096 x 16384 takes 173, 128 x 128 215)
   const bool fp32 = OUT == kOutFp32;
   using Large = std::conditional_t<OUT == kOutFp32, Shape128x192, Shape256>;

