@@ -313,3 +313,27 @@ def test_repeats_bit_for_bit():
     a = ep.Buffer.add_layernorm_bwd(h, w, gy)
     for _ in range(3):
         assert all(torch.equal(p, q) for p, q in zip(a, ep.Buffer.add_layernorm_bwd(h, w, gy)))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 values: the last rows as they are alone."""
+    T, H = 131090, 32768
+    rng = np.random.default_rng(8)
+    last = _rows(rng, 3, H, torch.bfloat16)
+    gy = _rows(rng, 3, H, torch.bfloat16)
+    w, b = torch.ones(H, device="cuda"), torch.ones(H, device="cuda")
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = last
+    _, y, codes, scales = ep.Buffer.add_layernorm(x, None, w, b, EPS, "fp8")
+    _, y1, c1, s1 = ep.Buffer.add_layernorm(last, None, w, b, EPS, "fp8")
+    assert torch.equal(y[-3:], y1) and torch.equal(scales[-3:], s1)
+    assert torch.equal(codes[-3:].view(torch.uint8), c1.view(torch.uint8))
+    assert torch.all(y[0] == 1) and torch.all(y[T // 2] == 1)
+    y.zero_()
+    y[-3:] = gy
+    g, _, gw, gb = ep.Buffer.add_layernorm_bwd(x, w, y, None, EPS)
+    g1, _, gw1, gb1 = ep.Buffer.add_layernorm_bwd(last, w, gy, None, EPS)
+    assert torch.equal(g[-3:], g1) and not g[:-3].any()
+    # three rows' terms in another order: two sums, each within half a step
+    for a, c in ((gw, gw1), (gb, gb1)):
+        assert torch.all((a - c).abs() <= 4 * U * 16 * 8)

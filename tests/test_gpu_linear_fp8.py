@@ -294,3 +294,26 @@ def test_nan_scales_of_powers_of_two(M, square, dtype):
     p[0][2, 128:], p[1][2, 1] = 0, np.nan
     y = ep.Buffer.linear_fp8(*_dev(p), pow2=True, out_dtype=dtype)
     assert torch.isnan(y[2]).all() and torch.isfinite(torch.cat([y[:2], y[3:]])).all()
+
+
+@pytest.mark.parametrize("M,N,dtype", [(66000, 65600, torch.bfloat16), (66001, 32801, torch.float32), (3, (1 << 25) + 5, torch.bfloat16)])
+def test_offsets_past_32_bits(M, N, dtype):
+    """Results (or weights) of more than 2^32 bytes: the first and the last rows and channels, exactly."""
+    K = 128
+    one = lambda r: torch.full((r, K), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # noqa: E731
+    x, w = one(M), one(N)
+    x.view(torch.uint8)[-1] = 0x40            # 2.0
+    w.view(torch.uint8)[-1] = 0xB8            # -1.0
+    xs = torch.ones(M, 1, device="cuda")
+    xs[-2:] = 0.5
+    ws = torch.ones(N, 1, device="cuda")
+    ws[-2:] = 4.0
+    y = ep.Buffer.linear_fp8(x, xs, w, ws, out_dtype=dtype)
+    rows = torch.full((M,), 128.0, device="cuda")
+    rows[-2], rows[-1] = 64.0, 128.0
+    cols = torch.ones(N, device="cuda")
+    cols[-2], cols[-1] = 4.0, -4.0
+    for m in (0, 1, M // 2, M - 2, M - 1):
+        assert torch.equal(y[m].float(), rows[m] * cols), m
+    for n in (0, N // 2, N - 2, N - 1):
+        assert torch.equal(y[:, n].float(), rows * cols[n]), n

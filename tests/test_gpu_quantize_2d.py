@@ -117,3 +117,19 @@ def test_two_dimensional_only():
     with pytest.raises(ep.EpError):
         x = torch.zeros(2, 2, 128, device="cuda", dtype=torch.bfloat16)
         ep.ep_quantize_fp8_2d(x, x.to(torch.float8_e4m3fn), torch.zeros(4, 1, device="cuda"), None, None)
+
+
+@pytest.mark.parametrize("block", ["rows", "square"])
+def test_offsets_past_32_bits(block):
+    """A matrix of more than 2^32 values: its last tile as it is alone."""
+    R, C = 65700, 65536
+    x = torch.zeros(R, C, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(R % 128, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    x[-last.shape[0]:, -128:] = last
+    got = ep.Buffer.quantize_fp8_2d(x, block)
+    want = ep.Buffer.quantize_fp8_2d(last, block)
+    u8 = lambda t: t.view(torch.uint8)  # noqa: E731
+    n = last.shape[0] if block == "rows" else 1
+    assert torch.equal(u8(got[0])[-last.shape[0]:, -128:], u8(want[0])) and torch.equal(got[1][-n:, -1:], want[1])
+    assert torch.equal(u8(got[2])[-128:, -128:], u8(want[2])) and torch.equal(got[3][-want[3].shape[0]:, -1:], want[3])
+    assert not u8(got[0])[:, 0].any() and not u8(got[2])[0].any()
