@@ -478,8 +478,8 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 // ---------------------------------------------------------------------------
 // few tokens
 //
-// The weights are streamed once: a workgroup takes 16 channels and all the tokens
-// (16 MT of them), its waves every so many slabs each.  A wave keeps a ring of slabs
+// A workgroup takes 16 channels and 16 MT tokens, its waves every so many slabs each:
+// the weights are streamed once where that is all the tokens.  A wave keeps a ring of slabs
 // in LDS of its own -- no barrier until the end -- filled by loads whose lanes
 // follow the memory: in the matrix instruction's order consecutive lanes are rows
 // apart and a load of 1 KB holds the address unit 88 cycles where it takes 22 (16
@@ -627,13 +627,22 @@ static void launch_tiles(const LinArgs &a, int32_t span, hipStream_t s) {
   hipLaunchKernelGGL((k_linear_fp8<S, ROW, POW2, OUT>), dim3(grid), dim3(S::threads), 0, s, a, tm, tn, span);
 }
 
+// Blocks of 16 tokens a workgroup of the kernel for few tokens takes, or 0 for tiles: as few as keep its
+// workgroups, whose waves share K, to one a compute unit (128 x 1024 x 7168 8.0 us, fp32 results 8.3,
+// against 16.8 and 26.4 with 64 x 64 tiles; 256 x 1024 x 7168 13.1 against 17.0; twice as many, 128 x 4096
+// x 4096 16.3 against 11.2), and up to 32 tokens whatever the channels.  K 0 leaves the addend, or zeros.
+static int few_blocks(const Linear &n) {
+  if (n.K == 0) return 4;
+  for (int mt = 1; mt <= 4; mt *= 2) {
+    const int64_t groups = ((int64_t)n.N + 15) / 16 * ((n.M + 16 * mt - 1) / (16 * mt));
+    if (groups <= 256 || (mt <= 2 && n.M <= 16 * mt)) return mt;
+  }
+  return 0;
+}
+
 template <bool ROW, bool POW2, int OUT>
 static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
-  // 33 to 64 tokens: while a compute unit has at most one workgroup of 16 channels (64 x 2048 x 7168
-  // 13.3 us against 16.6 with 64 x 64 tiles, 64 x 7168 x 2048 9.2 against 7.4)
-  // (and K 0, which leaves the addend, or zeros)
-  if (n.M <= 32 || (n.M <= 64 && n.N <= 4096) || n.K == 0) {
-    const int mt = n.M <= 16 ? 1 : n.M <= 32 ? 2 : 4;
+  if (const int mt = few_blocks(n)) {
     const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
 #define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * FewShape<MT>::waves), 0, s, a)
     if (mt == 1) L(1);
@@ -655,12 +664,11 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
   else launch_tiles<Shape64, ROW, POW2, OUT>(a, 8, s);
 }
 
-// A launch counts its threads in 32 bits, and a tile index is an int32.  (Up to 64 tokens may go either
-// way: the limit of the launch of 16 channels a workgroup is the lower one.)
+// A launch counts its threads in 32 bits, and a tile index is an int32.
 bool linear_fp8_fits(const Linear &n) {
-  const int64_t few = ((int64_t)n.N + 15) / 16;
-  return n.M <= 64 || n.K == 0 ? few * 512 < (int64_t)1 << 32 && (n.M + 63) / 64 <= 65535
-                               : tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
+  if (const int mt = few_blocks(n))
+    return ((int64_t)n.N + 15) / 16 * 512 < (int64_t)1 << 32 && (n.M + 16 * mt - 1) / (16 * mt) <= 65535;
+  return tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
 }
 
 hipError_t launch_linear_fp8(const Linear &n, hipStream_t s) {

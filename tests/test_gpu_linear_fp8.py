@@ -98,9 +98,11 @@ def _check(p, square, out_dtype, addend=None, swiglu=False, exact=False, pow2=Fa
     return y
 
 
-# few tokens; 64 x 64 tiles; ragged in both directions
+# 16, 32 and 64 tokens a workgroup; 64 x 64 tiles (from 129 x 2064 on); ragged in both directions
 SMALL = [(1, 1, 128), (1, 16, 256), (3, 130, 384), (16, 100, 1152), (17, 272, 2048), (32, 127, 128), (33, 48, 640),
-         (64, 257, 4224), (65, 64, 128), (65, 1, 256), (100, 129, 384), (130, 272, 1152), (333, 500, 256), (1, 7168, 2048)]
+         (64, 257, 4224), (65, 64, 128), (65, 1, 256), (100, 129, 384), (130, 272, 1152), (333, 500, 256), (1, 7168, 2048),
+         (20, 4200, 256), (40, 2100, 1280), (600, 300, 384), (1000, 17, 1152), (129, 2064, 384), (300, 1039, 1280),
+         (1100, 260, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SMALL)
@@ -132,7 +134,7 @@ def test_tiles(M, N, K, square, dtype):
         _check(_problem(M, N, K, square, False), square, dtype)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (17, 32, 384), (32, 4112, 128), (33, 272, 640), (90, 160, 384), (2047, 2064, 256),
+@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (17, 32, 384), (32, 4112, 128), (33, 272, 640), (90, 160, 384), (40, 2112, 256), (300, 1104, 384), (2047, 2064, 256),
                                    (4090, 2976, 256), (4090, 4064, 384)])
 @pytest.mark.parametrize("square", [True, False])
 def test_swiglu(M, N, K, square):
@@ -161,8 +163,8 @@ def test_swiglu_far_gates():
 def test_pow2_scales_out_of_form_are_reported():
     """A scale that is not a power of two sets the flag and nothing else; a call
     without the promise does not look."""
-    for M in (5, 100):
-        p = _problem(M, 256, 256, True, True)
+    for M, N in ((5, 256), (100, 256), (300, 1100)):
+        p = _problem(M, N, 256, True, True)
         for t, at in ((1, (M - 1, 1)), (3, (1, 0))):
             for bad in (3.0, 0.0, -1.0, np.inf, np.nan, 1e-40):
                 q = [v.copy() for v in p]
@@ -179,8 +181,8 @@ def test_pow2_scales_out_of_form_are_reported():
 
 
 def test_nan_scale_reaches_its_rows_only():
-    for M in (3, 80):
-        p = _problem(M, 200, 256, True, True)
+    for M, N in ((3, 200), (80, 200), (300, 1100)):
+        p = _problem(M, N, 256, True, True)
         p[1][1, 1] = np.nan
         y = ep.Buffer.linear_fp8(*_dev(p))
         assert torch.isnan(y[1]).all() and torch.isfinite(torch.cat([y[:1], y[2:]])).all()
@@ -217,7 +219,7 @@ def test_empty_and_leading_shapes():
 
 
 def test_streams_prepared_and_captured():
-    for M, N, K in ((8, 512, 1024), (300, 512, 1024)):
+    for M, N, K in ((8, 512, 1024), (300, 512, 1024), (300, 1100, 1024)):
         d = _dev(_problem(M, N, K, True, False))
         want = ep.Buffer.linear_fp8(*d)
         s = torch.cuda.Stream()
@@ -272,25 +274,25 @@ def test_no_channels_leave_the_addend(M, N):
             assert torch.all(ep.Buffer.linear_fp8(*a, ws, out_dtype=dt) == 0)
 
 
-@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("M,N", [(3, 200), (40, 200), (200, 200), (300, 1100)])
 @pytest.mark.parametrize("square", [True, False])
 @pytest.mark.parametrize("pow2", [True, False])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_nan_codes_reach_their_row_and_channel_only(M, square, pow2, dtype):
-    p = _problem(M, 200, 256, square, True)
+def test_nan_codes_reach_their_row_and_channel_only(M, N, square, pow2, dtype):
+    p = _problem(M, N, 256, square, True)
     p[0][1, 130], p[2][77, 5] = 0x7F, 0xFF   # both NaN
     y = ep.Buffer.linear_fp8(*_dev(p), pow2=pow2, out_dtype=dtype)
-    want = torch.zeros(M, 200, dtype=torch.bool, device="cuda")
+    want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
     want[1] = want[:, 77] = True
     assert torch.equal(torch.isnan(y), want)
 
 
-@pytest.mark.parametrize("M", [3, 80])
+@pytest.mark.parametrize("M,N", [(3, 200), (80, 200), (300, 1100)])
 @pytest.mark.parametrize("square", [True, False])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_nan_scales_of_powers_of_two(M, square, dtype):
+def test_nan_scales_of_powers_of_two(M, N, square, dtype):
     """What the quantiser gives a block that is not finite: codes 0 and a NaN scale."""
-    p = _problem(M, 200, 256, square, True)
+    p = _problem(M, N, 256, square, True)
     p[0][2, 128:], p[1][2, 1] = 0, np.nan
     y = ep.Buffer.linear_fp8(*_dev(p), pow2=True, out_dtype=dtype)
     assert torch.isnan(y[2]).all() and torch.isfinite(torch.cat([y[:2], y[3:]])).all()
