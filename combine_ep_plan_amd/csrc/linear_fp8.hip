@@ -478,7 +478,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 // ---------------------------------------------------------------------------
 // few tokens
 //
-// A workgroup takes 16 channels and 16 MT tokens, its waves every so many slabs each:
+// A workgroup takes 16 NC channels and 16 MT tokens, its waves every so many slabs each:
 // the weights are streamed once where that is all the tokens.  A wave keeps a ring of slabs
 // in LDS of its own -- no barrier until the end -- filled by loads whose lanes
 // follow the memory: in the matrix instruction's order consecutive lanes are rows
@@ -488,18 +488,18 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear_fp8(LinArgs a, int32_t
 
 template <int MT>
 struct FewShape {
-  static constexpr int waves = MT == 4 ? 4 : 8, ring = MT == 1 ? 4 : 3;   // LDS: 147, 160, 129 KB
+  static constexpr int waves = MT == 4 ? 4 : 8, ring = MT == 1 ? 4 : 3;   // LDS: 147, 160, 129 (153) KB
 };
 
-template <int MT, bool ROW, bool POW2, int OUT>
+template <int MT, int NC, bool ROW, bool POW2, int OUT>
 __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(LinArgs a) {
-  constexpr int W = FewShape<MT>::waves, R = FewShape<MT>::ring;
-  __shared__ u32x4 slabs[W][R][(1 + MT) * 16 * kChunks];   // 16 rows of weights, then the tokens
+  constexpr int W = FewShape<MT>::waves, R = FewShape<MT>::ring, BN = NC * 16;
+  __shared__ u32x4 slabs[W][R][(NC + MT) * 16 * kChunks];   // the rows of weights, then the tokens
   __shared__ float scales[W][R][128];                      // the tokens', then the channels' or the square's
   const int tid = threadIdx.x, lane = tid & 63, rl = lane & 15, q4 = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16, NB = a.K / 128;
-  const int32_t rows = a.M - m0 < MT * 16 ? a.M - m0 : MT * 16, wrows = a.N - n0 < 16 ? a.N - n0 : 16;
+  const int32_t n0 = blockIdx.x * BN, m0 = blockIdx.y * MT * 16, NB = a.K / 128;
+  const int32_t rows = a.M - m0 < MT * 16 ? a.M - m0 : MT * 16, wrows = a.N - n0 < BN ? a.N - n0 : BN;
   const __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc(
       (void *)(a.w + (int64_t)n0 * (a.K / 16)), (short)0, wrows * a.K, kBufDword3);
   const __amdgpu_buffer_rsrc_t rX = __builtin_amdgcn_make_buffer_rsrc(
@@ -511,51 +511,60 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
   // eight rows a load, chunks in the order of swz; rows past the end are out of range
   const uint32_t off = (uint32_t)((lane >> 3) * a.K + ((lane & 7) ^ ((lane >> 4) & 3)) * 16);
   const uint32_t oxs = (uint32_t)((lane < rows ? lane : rows - 1) * NB * 4);
-  const uint32_t ows = ROW ? (uint32_t)((rl < wrows ? rl : wrows - 1) * NB * 4) : 0u;
-  constexpr int kLoads = 2 + 2 * MT + 2;
+  const int32_t cw = lane & (BN - 1);
+  const uint32_t ows = ROW ? (uint32_t)((cw < wrows ? cw : wrows - 1) * NB * 4) : 0u;
+  constexpr int kLoads = 2 * NC + 2 * MT + 2;
   const auto issue = [&](int32_t k, int slot) {
     u32x4 *const d = slabs[wv][slot];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)   // rows 8 i ..: their chunks are permuted by 4 i more
-      lds_load16_stream(rW, LDS_ADDR(d + i * 64), (off ^ (uint32_t)(i * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
+    for (int i = 0; i < 2 * NC; ++i)   // rows 8 i ..: every second eight's chunks are permuted by 4 more
+      lds_load16_stream(rW, LDS_ADDR(d + i * 64), (off ^ (uint32_t)((i & 1) * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i)
-      lds_load16(rX, LDS_ADDR(d + (2 + i) * 64), (off ^ (uint32_t)((i & 1) * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
+      lds_load16(rX, LDS_ADDR(d + (2 * NC + i) * 64), (off ^ (uint32_t)((i & 1) * 64)) + (uint32_t)(i * 8 * a.K), k * 128);
     lds_load4(rXS, LDS_ADDR(&scales[wv][slot][0]), oxs, k * 4);
     lds_load4(rWS, LDS_ADDR(&scales[wv][slot][64]), ows, k * 4);
   };
-  f32x4 acc[MT];
+  f32x4 acc[NC][MT];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   // slab in `slot`, landed; `next`, if it is one, is sent for into its place once it is read
   const auto slab = [&](int slot, int32_t next) {
     const u32x4 *const d = slabs[wv][slot];
     const float *const sc = scales[wv][slot];
-    const i32x8 fw = join_codes(d[swz(rl, q4)], d[swz(rl, q4 + 4)]);
-    i32x8 fx[MT];
+    i32x8 fw[NC], fx[MT];
     float s[MT];
-    f32x4 sn;
+    f32x4 sn[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) fw[c] = join_codes(d[swz(c * 16 + rl, q4)], d[swz(c * 16 + rl, q4 + 4)]);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      fx[j] = join_codes(d[swz((1 + j) * 16 + rl, q4)], d[swz((1 + j) * 16 + rl, q4 + 4)]);
+      fx[j] = join_codes(d[swz((NC + j) * 16 + rl, q4)], d[swz((NC + j) * 16 + rl, q4 + 4)]);
       s[j] = sc[j * 16 + rl];
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sn[r] = sc[64 + (ROW ? q4 * 4 + r : 0)];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sn[c][r] = sc[64 + (ROW ? c * 16 + q4 * 4 + r : 0)];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (next < NB) issue(next, slot);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (OUT == kOutFp32) {
+    for (int c = 0; c < NC; ++c) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw, c, 1.0f), widen(fx[j], c, 1.0f), p, 0, 0, 0);
-      } else {
-        p = mfma_slab(fw, fx[j], p);
+      for (int j = 0; j < MT; ++j) {
+        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (OUT == kOutFp32) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[c], g, 1.0f), widen(fx[j], g, 1.0f), p, 0, 0, 0);
+        } else {
+          p = mfma_slab(fw[c], fx[j], p);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[c][j][r] = __builtin_fmaf(p[r], sn[c][r] * s[j], acc[c][j][r]);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], sn[r] * s[j], acc[j][r]);
     }
   };
   int32_t k = wv;
@@ -581,17 +590,19 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
     }
   }
   f32x4 *const red = reinterpret_cast<f32x4 *>(&slabs[0][0][0]);
-  static_assert(W * MT * 64 * 16 <= (int)sizeof(slabs), "the waves' sums fit");
+  static_assert(W * NC * MT * 64 * 16 <= (int)sizeof(slabs), "the waves' sums fit");
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < MT; ++j) red[(wv * MT + j) * 64 + lane] = acc[j];
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) red[((wv * NC + c) * MT + j) * 64 + lane] = acc[c][j];
   __syncthreads();
-  for (int e = tid; e < MT * 64; e += 64 * W) {
+  for (int e = tid; e < NC * MT * 64; e += 64 * W) {
     f32x4 v = red[e];
 #pragma unroll
-    for (int i = 1; i < W; ++i) v += red[i * MT * 64 + e];
-    const int32_t m = m0 + (e >> 6) * 16 + (e & 15);
-    if (m < a.M) store4<OUT>(a, m, n0 + ((e >> 4) & 3) * 4, v);
+    for (int i = 1; i < W; ++i) v += red[i * NC * MT * 64 + e];
+    const int32_t b = e >> 6, m = m0 + (b % MT) * 16 + (e & 15);
+    if (m < a.M) store4<OUT>(a, m, n0 + (b / MT) * 16 + ((e >> 4) & 3) * 4, v);
   }
 }
 
@@ -627,27 +638,38 @@ static void launch_tiles(const LinArgs &a, int32_t span, hipStream_t s) {
   hipLaunchKernelGGL((k_linear_fp8<S, ROW, POW2, OUT>), dim3(grid), dim3(S::threads), 0, s, a, tm, tn, span);
 }
 
-// Blocks of 16 tokens a workgroup of the kernel for few tokens takes, or 0 for tiles: as few as keep its
-// workgroups, whose waves share K, to one a compute unit (128 x 1024 x 7168 8.0 us, fp32 results 8.3,
-// against 16.8 and 26.4 with 64 x 64 tiles; 256 x 1024 x 7168 13.1 against 17.0; twice as many, 128 x 4096
-// x 4096 16.3 against 11.2), and up to 32 tokens whatever the channels.  K 0 leaves the addend, or zeros.
-static int few_blocks(const Linear &n) {
-  if (n.K == 0) return 4;
-  for (int mt = 1; mt <= 4; mt *= 2) {
-    const int64_t groups = ((int64_t)n.N + 15) / 16 * ((n.M + 16 * mt - 1) / (16 * mt));
-    if (groups <= 256 || (mt <= 2 && n.M <= 16 * mt)) return mt;
-  }
-  return 0;
+// Blocks of 16 tokens and of 16 channels a workgroup of the kernel for few tokens takes, or no tokens for
+// tiles: as few as keep its workgroups, whose waves share K, to one a compute unit (128 x 1024 x 7168 8.0
+// us, fp32 results 8.3, against 16.8 and 26.4 with 64 x 64 tiles), and up to 32 tokens whatever the
+// channels.  64 tokens and 32 channels, whose slabs are as long in coming as a tile's, only where their
+// widening is shared by the waves or K is short (256 x 2048 x 7168 with fp32 results 18.0 against 26.7,
+// in bf16 17.0 both, 64 x 8192 x 7168 19.4 against 17.1; 256 x 2048 x 1024 4.2 against 5.0).  K 0 leaves
+// the addend, or zeros.
+struct FewBlocks {
+  int mt, nc;
+  int64_t channels(const Linear &n) const { return ((int64_t)n.N + 16 * nc - 1) / (16 * nc); }
+  int64_t tokens(const Linear &n) const { return (n.M + 16 * mt - 1) / (16 * mt); }
+};
+static FewBlocks few_blocks(const Linear &n) {
+  if (n.K == 0) return {4, 1};
+  for (const FewBlocks b : {FewBlocks{1, 1}, FewBlocks{2, 1}, FewBlocks{4, 1}, FewBlocks{4, 2}})
+    if ((b.nc == 1 || n.out_fp32 || n.K <= 2048) &&
+        (b.channels(n) * b.tokens(n) <= 256 || (b.mt <= 2 && n.M <= 16 * b.mt)))
+      return b;
+  return {0, 0};
 }
 
 template <bool ROW, bool POW2, int OUT>
 static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s) {
-  if (const int mt = few_blocks(n)) {
-    const dim3 grid((unsigned)((n.N + 15) / 16), (unsigned)((n.M + 16 * mt - 1) / (16 * mt)));
-#define L(MT) hipLaunchKernelGGL((k_linear_fp8_few<MT, ROW, POW2, OUT>), grid, dim3(64 * FewShape<MT>::waves), 0, s, a)
-    if (mt == 1) L(1);
-    else if (mt == 2) L(2);
-    else L(4);
+  const FewBlocks b = few_blocks(n);
+  if (b.mt > 0) {
+    const dim3 grid((unsigned)b.channels(n), (unsigned)b.tokens(n));
+#define L(MT, NC) \
+  hipLaunchKernelGGL((k_linear_fp8_few<MT, NC, ROW, POW2, OUT>), grid, dim3(64 * FewShape<MT>::waves), 0, s, a)
+    if (b.mt == 1) L(1, 1);
+    else if (b.mt == 2) L(2, 1);
+    else if (b.nc == 1) L(4, 1);
+    else L(4, 2);
 #undef L
     return;
   }
@@ -666,8 +688,8 @@ static void launch_linear_form(const Linear &n, const LinArgs &a, hipStream_t s)
 
 // A launch counts its threads in 32 bits, and a tile index is an int32.
 bool linear_fp8_fits(const Linear &n) {
-  if (const int mt = few_blocks(n))
-    return ((int64_t)n.N + 15) / 16 * 512 < (int64_t)1 << 32 && (n.M + 16 * mt - 1) / (16 * mt) <= 65535;
+  const FewBlocks b = few_blocks(n);
+  if (b.mt > 0) return b.channels(n) * 512 < (int64_t)1 << 32 && b.tokens(n) <= 65535;
   return tiles_of(n, 64) + kXcds < (int64_t)1 << 24;
 }
 

@@ -98,11 +98,12 @@ def _check(p, square, out_dtype, addend=None, swiglu=False, exact=False, pow2=Fa
     return y
 
 
-# 16, 32 and 64 tokens a workgroup; 64 x 64 tiles (from 129 x 2064 on); ragged in both directions
+# 16, 32 and 64 tokens a workgroup, 64 x 32 (from 129 x 2064 on); 64 x 64 tiles (from 129 x 2900 on);
+# ragged in both directions
 SMALL = [(1, 1, 128), (1, 16, 256), (3, 130, 384), (16, 100, 1152), (17, 272, 2048), (32, 127, 128), (33, 48, 640),
          (64, 257, 4224), (65, 64, 128), (65, 1, 256), (100, 129, 384), (130, 272, 1152), (333, 500, 256), (1, 7168, 2048),
          (20, 4200, 256), (40, 2100, 1280), (600, 300, 384), (1000, 17, 1152), (129, 2064, 384), (300, 1039, 1280),
-         (1100, 260, 128)]
+         (1100, 260, 128), (129, 2900, 384), (300, 1701, 1280), (1100, 513, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SMALL)
@@ -134,7 +135,7 @@ def test_tiles(M, N, K, square, dtype):
         _check(_problem(M, N, K, square, False), square, dtype)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (17, 32, 384), (32, 4112, 128), (33, 272, 640), (90, 160, 384), (40, 2112, 256), (300, 1104, 384), (2047, 2064, 256),
+@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (5, 48, 256), (17, 32, 384), (32, 4112, 128), (33, 272, 640), (90, 160, 384), (40, 2112, 256), (300, 1104, 384), (300, 1712, 384), (2047, 2064, 256),
                                    (4090, 2976, 256), (4090, 4064, 384)])
 @pytest.mark.parametrize("square", [True, False])
 def test_swiglu(M, N, K, square):
@@ -163,7 +164,7 @@ def test_swiglu_far_gates():
 def test_pow2_scales_out_of_form_are_reported():
     """A scale that is not a power of two sets the flag and nothing else; a call
     without the promise does not look."""
-    for M, N in ((5, 256), (100, 256), (300, 1100)):
+    for M, N in ((5, 256), (100, 256), (300, 1100), (300, 1700)):
         p = _problem(M, N, 256, True, True)
         for t, at in ((1, (M - 1, 1)), (3, (1, 0))):
             for bad in (3.0, 0.0, -1.0, np.inf, np.nan, 1e-40):
@@ -181,7 +182,7 @@ def test_pow2_scales_out_of_form_are_reported():
 
 
 def test_nan_scale_reaches_its_rows_only():
-    for M, N in ((3, 200), (80, 200), (300, 1100)):
+    for M, N in ((3, 200), (80, 200), (300, 1100), (300, 1700)):
         p = _problem(M, N, 256, True, True)
         p[1][1, 1] = np.nan
         y = ep.Buffer.linear_fp8(*_dev(p))
@@ -219,7 +220,7 @@ def test_empty_and_leading_shapes():
 
 
 def test_streams_prepared_and_captured():
-    for M, N, K in ((8, 512, 1024), (300, 512, 1024), (300, 1100, 1024)):
+    for M, N, K in ((8, 512, 1024), (300, 512, 1024), (300, 1100, 1024), (300, 1700, 1024)):
         d = _dev(_problem(M, N, K, True, False))
         want = ep.Buffer.linear_fp8(*d)
         s = torch.cuda.Stream()
@@ -274,7 +275,7 @@ def test_no_channels_leave_the_addend(M, N):
             assert torch.all(ep.Buffer.linear_fp8(*a, ws, out_dtype=dt) == 0)
 
 
-@pytest.mark.parametrize("M,N", [(3, 200), (40, 200), (200, 200), (300, 1100)])
+@pytest.mark.parametrize("M,N", [(3, 200), (40, 200), (200, 200), (300, 1100), (300, 1700)])
 @pytest.mark.parametrize("square", [True, False])
 @pytest.mark.parametrize("pow2", [True, False])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -287,7 +288,7 @@ def test_nan_codes_reach_their_row_and_channel_only(M, N, square, pow2, dtype):
     assert torch.equal(torch.isnan(y), want)
 
 
-@pytest.mark.parametrize("M,N", [(3, 200), (80, 200), (300, 1100)])
+@pytest.mark.parametrize("M,N", [(3, 200), (80, 200), (300, 1100), (300, 1700)])
 @pytest.mark.parametrize("square", [True, False])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_nan_scales_of_powers_of_two(M, N, square, dtype):
