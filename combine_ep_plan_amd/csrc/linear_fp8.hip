@@ -535,7 +535,7 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
     const u32x4 *const d = slabs[wv][slot];
     const float *const sc = scales[wv][slot];
     i32x8 fw[NC], fx[MT];
-    float s[MT];
+    float s[MT], sw[NC];
     f32x4 sn[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) fw[c] = join_codes(d[swz(c * 16 + rl, q4)], d[swz(c * 16 + rl, q4 + 4)]);
@@ -545,25 +545,40 @@ __global__ __launch_bounds__(64 * FewShape<MT>::waves) void k_linear_fp8_few(Lin
       s[j] = sc[j * 16 + rl];
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (POW2) {   // of the fragment's row
+        sw[c] = sc[64 + (ROW ? c * 16 + rl : 0)];
+      } else {                // of the result's channels
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sn[c][r] = sc[64 + (ROW ? c * 16 + q4 * 4 + r : 0)];
+        for (int r = 0; r < 4; ++r) sn[c][r] = sc[64 + (ROW ? c * 16 + q4 * 4 + r : 0)];
+      }
+    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (next < NB) issue(next, slot);
+    // powers of two go into the operands' exponents, as in the tiles: the product of two may lie outside
+    // fp32 where the result does not
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 p = POW2 ? acc[c][j] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (OUT == kOutFp32) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[c], g, 1.0f), widen(fx[j], g, 1.0f), p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fw[c], g, POW2 ? sw[c] : 1.0f),
+                                                        widen(fx[j], g, POW2 ? s[j] : 1.0f), p, 0, 0, 0);
+        } else if constexpr (POW2) {
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[c], fx[j], p, 0, 0, 0, exponent_of(sw[c]), 0,
+                                                               exponent_of(s[j]));
         } else {
           p = mfma_slab(fw[c], fx[j], p);
         }
+        if constexpr (POW2) {
+          acc[c][j] = p;
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[c][j][r] = __builtin_fmaf(p[r], sn[c][r] * s[j], acc[c][j][r]);
+          for (int r = 0; r < 4; ++r) acc[c][j][r] = __builtin_fmaf(p[r], sn[c][r] * s[j], acc[c][j][r]);
+        }
       }
     }
   };

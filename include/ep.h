@@ -941,8 +941,9 @@ typedef struct ep_linear_rule {
  * out:      bf16 or fp32 [M, N], tag TOKENS; with swiglu bf16 [M, N/2], N % 16 == 0.
  * status:   NULL or int32 [1], tag STATUS.  With EP_FP8_SCALES_POW2, a scale that
  *           is not a positive normal power of two makes the call OR
- *           EP_FLAG_SCALE_FORMAT into it (the block is then taken at the
- *           scale's exponent).
+ *           EP_FLAG_SCALE_FORMAT into it; the block is then taken at the
+ *           scale's exponent (3 as 2, -1 as 1, 0 and subnormal ones as 2^-127;
+ *           NaN where it is infinite or NaN).
  * The gradients are this product too.  With grad_out [M, N] quantised by
  * ep_quantize_fp8_2d (ROWS): the data gradient is x = codes, w = the weight's
  * transposed codes (SQUARE); the weight gradient [N, K] is x = codes_t of
