@@ -82,7 +82,8 @@ __global__ __launch_bounds__(kQThreads) void k_quantize_2d(const u32x4 *__restri
                                                            float *__restrict__ scales_t, bool pow2) {
   __shared__ u32x4 s_max[4][16];                // of the waves' columns
   __shared__ f32x2 s_row[kQT], s_col[kQT];      // scales and reciprocals
-  __shared__ u32x2 s_t[kQT * 16];               // [column][8-byte chunk of rows]
+  __shared__ u32x4 s_t[kQT * 8];                // [column][8-byte chunk of rows, two to a vector]
+  static_assert(alignof(decltype(s_t)) >= 16, "read as 16-byte vectors");
   const int tid = threadIdx.x, cl = tid & 15, rl = tid >> 4, wv = tid >> 6;
   const int32_t nb = C / kQT, tr = blockIdx.x / nb, tc = blockIdx.x - tr * nb;
   const int64_t Rp = (int64_t)((R + kQT - 1) / kQT) * kQT;
@@ -156,14 +157,15 @@ __global__ __launch_bounds__(kQThreads) void k_quantize_2d(const u32x4 *__restri
     float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = (c & 1) ? bf16_hi(v[i][c >> 1]) : bf16_lo(v[i][c >> 1]);
-    s_t[(cl * 8 + c) * 16 + (rl ^ cl)] = codes8(f, SQUARE ? sq : s_col[cl * 8 + c]);   // chunk rl, permuted by the column's group
+    reinterpret_cast<u32x2 *>(s_t)[(cl * 8 + c) * 16 + (rl ^ cl)] =   // chunk rl, permuted by the column's group
+        codes8(f, SQUARE ? sq : s_col[cl * 8 + c]);
   }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int k = j * kQThreads + tid, c = k >> 3, p = k & 7;   // column, 16-byte piece of its 128 rows
     const int g = (c >> 3) & 15;
-    const u32x4 d = *reinterpret_cast<const u32x4 *>(&s_t[c * 16 + ((2 * p) ^ (g & ~1))]);
+    const u32x4 d = s_t[c * 8 + (p ^ (g >> 1))];
     *reinterpret_cast<u32x4 *>(codes_t + ((int64_t)tc * kQT + c) * Rp + (int64_t)tr * kQT + 16 * p) =
         (g & 1) ? u32x4{d.z, d.w, d.x, d.y} : d;
   }
