@@ -225,12 +225,14 @@ hipError_t launch_add_layernorm(const LayerNorm &n, hipStream_t s) {
 // exact in fp64: means of terms that cancel keep no rounding of theirs.
 // A workgroup takes every G-th row (or group of rows), the next row's loads in
 // flight while one is reduced, and keeps its share of grad_w and grad_b in
-// registers; the G partial rows, both side by side, go to the workspace and
-// norm.hip's second kernel adds them in order, in fp64.  They are twice as long as
-// the RMS norm's, so there are no more workgroups of over 512 threads than compute
-// units (one fits: 4096 x 7168 with dropout 74 us against 79 with up to 512), and
-// fp32 rows of 2049 to 4096 channels go two to a workgroup of up to 1024 threads
-// (16384 x 4096 200 us against 210; bf16 rows 152 against 147, one to a workgroup).
+// registers, in fp32: T / 512 rows, T / 256 above 4096 channels, so that 16384 rows
+// are 32 or 64 additions of half a step each at most.  The G partial rows, both side
+// by side, go to the workspace and norm.hip's second kernel adds them in order, in
+// fp64.  They are twice as long as the RMS norm's, so there are no more workgroups of
+// over 512 threads than compute units (one fits: 4096 x 7168 with dropout 74 us
+// against 79 with up to 512), and fp32 rows of 2049 to 4096 channels go two to a
+// workgroup of up to 1024 threads (16384 x 4096 200 us against 210; bf16 rows 152
+// against 147, one to a workgroup).
 
 static BwdShape ln_bwd_shape(int32_t V, bool fp32) {
   BwdShape b = bwd_shape(V);

@@ -876,7 +876,11 @@ ep_status_t ep_add_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H, size_t
  * workspace:         fp32, 1-D, tag WORKSPACE, of at least
  *                    ep_add_layernorm_bwd_workspace_bytes; may be NULL where
  *                    neither is asked for.  One call in flight at a time may use it.
- * The sums are added in a fixed order: results repeat bit for bit.
+ * The sums over rows run in fp32 over the rows that one workgroup takes, at most
+ * T / 256 + 2 of them (T / 512 + 2 for H <= 4096), and in double over the
+ * workgroups: each is within that many half steps (2^-24) of the sum of its
+ * terms' magnitudes, and those of the terms.  They are added in a fixed order:
+ * results repeat bit for bit.
  * Enqueues up to two kernels. */
 typedef struct ep_layernorm_bwd {
   const ep_tensor_t *hidden, *weight, *grad_y, *grad_residual_out, *rng;
