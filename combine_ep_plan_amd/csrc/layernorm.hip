@@ -130,7 +130,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_add_layernorm(LnArgs a) {
   }
   row_reduce2<WAVE>(s1, s2);
   const double m1 = s1 * a.inv_h, mean = shift + m1;
-  const float rstd = rstd_of(not_below_zero(__builtin_fma(-m1, s1, s2)), a.inv_h, a.eps);
+  // half of h - mean, whose whole may lie outside fp32, times twice the reciprocal: the same roundings
+  const double half_mean = 0.5 * mean;
+  const float rstd2 = 2.0f * rstd_of(not_below_zero(__builtin_fma(-m1, s1, s2)), a.inv_h, a.eps);
   // the stream's rows are stored here, behind the reduction: they may replace
   // the residual, whose first value every thread reads.  Not read again before
   // the whole layer: past the caches, as the RMS norm's.
@@ -158,7 +160,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_add_layernorm(LnArgs a) {
     if (a.b) load_weight8(a.b, a.w_fp32, v, b);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float n = (float)((double)h[i][c] - mean) * rstd;
+      const float n = (float)__builtin_fma((double)h[i][c], 0.5, -half_mean) * rstd2;
       h[i][c] = a.b ? __builtin_fmaf(n, w[c], b[c]) : n * w[c];
       m = umax(m, magnitude_bits(h[i][c]));
     }
@@ -350,8 +352,9 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
     }
     const double m1 = s[0] * a.inv_h, mean = shift + m1;
     const float rstd = rstd_of(not_below_zero(__builtin_fma(-m1, s[0], s[1])), a.inv_h, a.eps);
-    // n = (h - mean) * rstd with the mean in two floats: no step of n is wider than fp32
-    const float mh = (float)mean, ml = (float)(mean - (double)mh) * rstd;
+    // n = (h - mean) * rstd with the mean in two floats: no step of n is wider than fp32 (nor larger: half
+    // of h - mean times twice rstd, as in the forward)
+    const float mh = (float)mean, ml = (float)(mean - (double)mh) * rstd, mh2 = 0.5f * mh, rstd2 = 2.0f * rstd;
     const float mg = (float)(s[2] * a.inv_h);
     const float mn = (float)(__builtin_fma(-m1, s[2], s[3]) * (double)rstd * a.inv_h);  // mean of g * n
 #pragma unroll
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
       float o[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float n = __builtin_fmaf(h[c] - mh, rstd, -ml);
+        const float n = __builtin_fmaf(__builtin_fmaf(h[c], 0.5f, -mh2), rstd2, -ml);
         o[c] = rstd * ((g[c] * w[c] - mg) - n * mn) + r[c];
         dw[i][c] += g[c] * n;
         db[i][c] += g[c];
