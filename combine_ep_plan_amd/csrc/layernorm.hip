@@ -281,7 +281,9 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd(LnBwdArgs a) {
   const PhiloxKey key = drop ? philox_key(a.drop.rng) : PhiloxKey{};
   // one vector a thread: the next row's loads in flight under this row, and the weight in registers.
   // More: the row is read again behind the reduction, out of the L2, for registers that spill cost more
-  // (held packed, 4096 x 12288 with dropout takes 154 us in bf16 and 207 in fp32 against 131 and 195)
+  // (held packed, 4096 x 12288 with dropout takes 154 us in bf16 and 207 in fp32 against 131 and 195).
+  // Above 16384 channels the two sums alone are 64 registers: 64 (bf16) and 63 (fp32) of all spill, and
+  // 2048 x 20480 takes 202 and 227 us, 40 and 57% of the copy rate
   constexpr bool AHEAD = VPT == 1;
   float w[8], dw[VPT][8], db[VPT][8];
   Raw8<RT> hr, rr;

@@ -45,7 +45,9 @@ __device__ __forceinline__ float silu_times(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// Channels n .. n + 3 of token m (m < M).
+// Channels n .. n + 3 of token m (m < M).  Where rows are not whole vectors each value is a load of
+// the addend, which may be the result, and a store behind it: 664 x 1917 x 1536 10.4 us, with an addend
+// 12.1, against 7.6 and 7.8 for 1920 channels; 4095 x 2951 x 1280 38 and 62 against 21 and 25 for 2952.
 template <int OUT>
 __device__ __forceinline__ void store4(const LinArgs &a, int32_t m, int32_t n, f32x4 v) {
   if (n >= a.N) return;
@@ -186,7 +188,7 @@ __device__ __forceinline__ void check_scales(const float *s, int64_t n, uint32_t
 // tiles' time the matrix cores are busy half: loads into LDS, reads out of it and the
 // fold of the sums interleave with the products and are none of them the bound alone
 // (without the loads 94 us, without the reads 98).  Small tiles wait for their
-// operands, which reach a compute unit at 65 to 70 GB/s.
+// operands, which were measured to reach a compute unit at 65 to 70 GB/s.
 
 template <int WN_, int WM_, int NA_, int MB_, int ST_>
 struct LinShape {

@@ -934,6 +934,7 @@ typedef struct ep_linear_rule {
  * largest's power of two, as in ep_expert_gemm_fp8.  xs * ws is formed in fp32 with
  * EP_FP8_SCALES_AMAX and has to lie in its range; with _POW2 and fp32 results each
  * operand, code times scale, has to lie in bf16's normal range to be exact.
+ * The SwiGLU store keeps neither gate nor up: it has no backward here.
  * x:        e4m3 [M, K] (any leading shape), tag TOKENS; K % 128 == 0, K <= 2^22
  *           (K 0, a weight gradient of no tokens: the addend, or zeros).
  * x_scales: fp32 [M, K/128], tag FP8_SCALES.
